@@ -1,5 +1,6 @@
-"""Build libibp.so (the IBP library) and libibp_ceiling.so (the gather-copy
-floor the benchmark measures it against) in-tree with hipcc for gfx950.
+"""Build libibp.so (the IBP library), libibp_kv.so (the 8-bit KV page cache)
+and libibp_ceiling.so (the gather-copy floor the benchmark measures the IBP
+library against) in-tree with hipcc for gfx950.
 
 Usage: python -m lossless_bit_level_amd.build
 """
@@ -14,6 +15,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "ibp.hip")
 LIB = os.path.join(PKG, "libibp.so")
+KV_SRC = os.path.join(PKG, "csrc", "ibp_kv.hip")
+KV_LIB = os.path.join(PKG, "libibp_kv.so")
 CEILING_SRC = os.path.join(PKG, "csrc", "ceiling.hip")
 CEILING_LIB = os.path.join(PKG, "libibp_ceiling.so")
 INCLUDE = os.path.join(ROOT, "include")
@@ -35,10 +38,10 @@ def command(out: str = LIB, extra=(), src: str = SRC) -> list[str]:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile both libraries, side by side (always recompiles; the IBP
+    """Compile the libraries, side by side (always recompiles; the IBP
     library takes about a minute)."""
     jobs = []
-    for src, lib in ((SRC, LIB), (CEILING_SRC, CEILING_LIB)):
+    for src, lib in ((SRC, LIB), (KV_SRC, KV_LIB), (CEILING_SRC, CEILING_LIB)):
         cmd = command(lib + ".tmp", src=src)
         if verbose:
             print(" ".join(cmd), flush=True)

@@ -1,0 +1,1288 @@
+// libibp_kv: an 8-bit KV page cache and the attention that reads it, for AMD
+// Instinct MI355X (gfx950, CDNA4).  Formats and calls: include/ibp_kv.h.
+#include <hip/hip_runtime.h>
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "ibp_kv.h"
+
+namespace {
+
+constexpr int kWave = 64;
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kTile = 16;       // tokens of a tile
+constexpr int kStepTiles = 4;   // tiles a wave takes at a time
+constexpr int kStep = kTile * kStepTiles;
+constexpr int kUnit = 1024;     // bytes of a tile that one wide load of a wave takes
+constexpr int kMaxSplits = 64;
+constexpr int kExpMin = -126, kExpMax = 119;  // exponents of a page's scale
+constexpr float kE4m3Max = 448.f;
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+
+// ---------------------------------------------------------- conversions ----
+
+template <bool F16>
+__device__ __forceinline__ float to_float(uint16_t x) {
+  if constexpr (F16) return (float)__builtin_bit_cast(_Float16, x);
+  return __builtin_bit_cast(float, (uint32_t)x << 16);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint16_t to_half(float x) {
+  if constexpr (F16) return __builtin_bit_cast(uint16_t, (_Float16)x);
+  return __builtin_bit_cast(uint16_t, (__bf16)x);
+}
+
+// Eight e4m3 codes as eight 16-bit numbers, which hold them exactly.
+template <bool F16>
+__device__ __forceinline__ u32x4 widen8(uint32_t lo, uint32_t hi) {
+  u32x4 r;
+  if constexpr (F16) {
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true));
+    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false));
+    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true));
+  } else {
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true));
+    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false));
+    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true));
+  }
+  return r;
+}
+
+template <bool F16>
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float log2_fast(float x) { return __builtin_amdgcn_logf(x); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  bf16x2 p;
+  p[0] = (__bf16)a;
+  p[1] = (__bf16)b;
+  return __builtin_bit_cast(uint32_t, p);
+}
+
+__device__ __forceinline__ float bf16_low(uint32_t p) { return __builtin_bit_cast(float, p << 16); }
+__device__ __forceinline__ float bf16_high(uint32_t p) {
+  return __builtin_bit_cast(float, p & 0xFFFF0000u);
+}
+
+__device__ __forceinline__ bool finite(float x) {
+  return (__builtin_bit_cast(uint32_t, x) & 0x7F800000u) != 0x7F800000u;
+}
+
+// 2^e for e in [-126, 127].
+__device__ __forceinline__ float power2(int e) {
+  return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23);
+}
+
+// Smallest e with amax <= 448 * 2^e (448 = 1.75 * 2^8), in a scale's range.
+// Zero and subnormal numbers end at the lowest.
+__device__ __forceinline__ int scale_exponent(float amax) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, amax);
+  const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return min(max(e, kExpMin), kExpMax);
+}
+
+// Smallest e with scale <= 2^e: the exponent of a page's scale, which an
+// append writes as a power of two.
+__device__ __forceinline__ int held_exponent(float scale) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, scale);
+  const int e = (int)((b >> 23) & 255) - 127 + ((b & 0x7FFFFFu) ? 1 : 0);
+  return min(max(e, kExpMin), kExpMax);
+}
+
+// The number to convert for x / 2^e: saturated, and NaN for what is not finite.
+__device__ __forceinline__ float code_value(float x, float inv) {
+  const float y = fminf(fmaxf(x * inv, -kE4m3Max), kE4m3Max);
+  return finite(x) ? y : __builtin_bit_cast(float, 0x7FC00000u);
+}
+
+// The top bits of the bytes of `c` that are one of the two NaN codes.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t c) {
+  return ~(((c & 0x7F7F7F7Fu) ^ 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & 0x80808080u;
+}
+
+// Rounded to nearest, ties to even; NaN becomes 0x7F whatever its sign (which
+// the compiler may choose for a NaN constant).
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+  return (uint32_t)r & ~nan_codes((uint32_t)r);
+}
+
+// Four codes of scale `was` at another scale: ratio = was / now, at most 1.
+__device__ __forceinline__ uint32_t rescale4(uint32_t c, float ratio) {
+  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false);
+  const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
+  return codes4(code_value(a[0], ratio), code_value(a[1], ratio), code_value(b[0], ratio),
+                code_value(b[1], ratio));
+}
+
+__device__ __forceinline__ uint32_t byte_mask(int n) {  // the first n bytes of four
+  return n <= 0 ? 0u : n >= 4 ? ~0u : (1u << (8 * n)) - 1u;
+}
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// ---------------------------------------------------------------- rows ----
+
+struct Pool {
+  uint8_t* k_codes;
+  float* k_scales;
+  uint8_t* v_codes;
+  float* v_scales;
+  uint32_t n_pages;     // ids at or past this are holes
+  uint32_t page_bytes;  // of the keys, and of the values
+  uint32_t tile_shift;  // log2 of a page's tiles
+};
+
+struct Rows {
+  const int32_t* pages;
+  const int32_t* lengths;
+  const int32_t* counts;
+  uint32_t heads;
+  uint32_t max_pages;
+  int32_t capacity;  // tokens
+  int32_t n_new;
+};
+
+struct Strided {
+  uint16_t* data;
+  int64_t seq, token, head;
+  uint32_t wide;  // 16-byte accesses are aligned
+};
+
+__device__ __forceinline__ int row_length(const Rows& r, uint32_t row) {
+  return min(max(r.lengths[row], 0), r.capacity);
+}
+
+__device__ __forceinline__ int new_count(const Rows& r, uint32_t seq) {
+  return r.counts ? min(max(r.counts[seq], 0), r.n_new) : r.n_new;
+}
+
+// -------------------------------------------------------------- append ----
+
+template <bool F16>
+__device__ __forceinline__ void load8(const uint16_t* p, bool wide, float* x) {
+  u16x8 h;
+  if (wide) {
+    h = *(const u16x8*)p;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = p[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = to_float<F16>(h[i]);
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int s = 32; s; s >>= 1) x = fmaxf(x, __shfl_xor(x, s));
+  return x;
+}
+
+// One wave per 16-token tile of a page that receives new tokens; the waves of
+// a page exchange their largest value through LDS.  A lane's 16 bytes of a
+// key unit are 16 dims of one token, so keys go straight from the loads to
+// the store.  A lane's 16 bytes of a value unit are 4 tokens x 4 dims: the
+// lane that loads 8 dims of 4 tokens writes 8 words of 4 codes to LDS, from
+// which units are read back.
+template <int DJ, bool F16>
+__global__ __launch_bounds__(kThreads) void append_kernel(Pool pool, Rows rows, Strided k,
+                                                          Strided v, uint32_t pages_per_row,
+                                                          uint64_t n_tasks) {
+  constexpr int D = 64 * DJ;
+  constexpr int kOctets = D / 8;
+  constexpr int kPasses = (kOctets * 4 + kWave - 1) / kWave;
+  __shared__ uint32_t s_tile[kWaves][4 * D];
+  __shared__ float s_max[2][kWaves];
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const int tiles = 1 << pool.tile_shift;
+  const uint64_t task = (uint64_t)blockIdx.x * (kWaves >> pool.tile_shift) + (wave >> pool.tile_shift);
+  const int tile = wave & (tiles - 1);
+  const uint32_t row = (uint32_t)(min(task, n_tasks - 1) / pages_per_row);
+  const uint32_t seq = row / rows.heads, head = row % rows.heads;
+  const int end = row_length(rows, row), count = new_count(rows, seq);
+  const int first = max(end - count, 0);      // position of the first new token that exists
+  const int origin = end - count;             // position of token 0
+  const int page_tokens = kTile << pool.tile_shift;
+  const int page = first / page_tokens + (int)(min(task, n_tasks - 1) % pages_per_row);
+  const int page_at = page * page_tokens, at = page_at + tile * kTile;
+  bool live = task < n_tasks && count > 0 && page_at < end;
+  int32_t id = -1;
+  if (live) id = rows.pages[(uint64_t)row * rows.max_pages + page];
+  live = live && (uint32_t)id < pool.n_pages;
+
+  // keys: token at + lane % 16, dims 64 j + 16 (lane / 16) + 0..15
+  float kx[DJ][16], vx[kPasses][4][8];
+  const int kt = at + lane % 16, kg = lane / 16;
+  const bool k_new = live && kt >= first && kt < end;
+  float k_max = 0.f, v_max = 0.f;
+#pragma unroll
+  for (int j = 0; j < DJ; ++j)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) kx[j][i] = 0.f;
+  if (k_new) {
+    const uint16_t* p = k.data + seq * k.seq + (int64_t)(kt - origin) * k.token + head * k.head + 16 * kg;
+#pragma unroll
+    for (int j = 0; j < DJ; ++j) {
+      load8<F16>(p + 64 * j, k.wide, kx[j]);
+      load8<F16>(p + 64 * j + 8, k.wide, kx[j] + 8);
+    }
+  }
+  // values: octet `item % kOctets` of dims, tokens at + 4 (item / kOctets) + 0..3
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int item = p * kWave + lane;
+    const int g = item / kOctets, o = item % kOctets;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = at + 4 * g + r;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) vx[p][r][i] = 0.f;
+      if (live && g < 4 && t >= first && t < end)
+        load8<F16>(v.data + seq * v.seq + (int64_t)(t - origin) * v.token + head * v.head + 8 * o,
+                   v.wide, vx[p][r]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < DJ; ++j)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (finite(kx[j][i])) k_max = fmaxf(k_max, fabsf(kx[j][i]));
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (finite(vx[p][r][i])) v_max = fmaxf(v_max, fabsf(vx[p][r][i]));
+  k_max = wave_max(k_max);
+  v_max = wave_max(v_max);
+  // a page that held tokens keeps a larger scale
+  const bool held = live && page_at < first;
+  float k_was = 0.f, v_was = 0.f;
+  if (held) {
+    k_was = pool.k_scales[id];
+    v_was = pool.v_scales[id];
+  }
+  if (tiles > 1) {  // read by all waves of the page before one of them writes
+    if (lane == 0) {
+      s_max[0][wave] = k_max;
+      s_max[1][wave] = v_max;
+    }
+    __syncthreads();
+    for (int w = wave & ~(tiles - 1), n = 0; n < tiles; ++n) {
+      k_max = fmaxf(k_max, s_max[0][w + n]);
+      v_max = fmaxf(v_max, s_max[1][w + n]);
+    }
+  }
+  if (!live) return;
+  int ke = scale_exponent(k_max), ve = scale_exponent(v_max);
+  if (held) {
+    ke = max(ke, held_exponent(k_was));
+    ve = max(ve, held_exponent(v_was));
+  }
+  const float k_inv = power2(-ke), v_inv = power2(-ve);
+  const float k_ratio = k_was * k_inv, v_ratio = v_was * v_inv;
+  if (tile == 0 && lane == 0) {
+    pool.k_scales[id] = power2(ke);
+    pool.v_scales[id] = power2(ve);
+  }
+  const uint64_t base = (uint64_t)(uint32_t)id * pool.page_bytes + (uint32_t)(tile * kTile * D);
+  uint8_t* kp = pool.k_codes + base + lane * 16;
+  uint8_t* vp = pool.v_codes + base + lane * 16;
+
+  const bool k_old = kt < first;
+#pragma unroll
+  for (int j = 0; j < DJ; ++j) {
+    u32x4 c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c[i] = codes4(code_value(kx[j][4 * i], k_inv), code_value(kx[j][4 * i + 1], k_inv),
+                    code_value(kx[j][4 * i + 2], k_inv), code_value(kx[j][4 * i + 3], k_inv));
+    if (k_old) {
+      c = *(const u32x4*)(kp + j * kUnit);
+      if (k_ratio != 1.f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = rescale4(c[i], k_ratio);
+      }
+    }
+    *(u32x4*)(kp + j * kUnit) = c;
+  }
+
+  uint32_t* tile_words = s_tile[wave];
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int item = p * kWave + lane;
+    const int g = item / kOctets, o = item % kOctets;
+    if (g < 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int d = 8 * o + i;
+        tile_words[(d / 64) * 256 + g * 64 + (d % 16) * 4 + d % 64 / 16] =
+            codes4(code_value(vx[p][0][i], v_inv), code_value(vx[p][1][i], v_inv),
+                   code_value(vx[p][2][i], v_inv), code_value(vx[p][3][i], v_inv));
+      }
+    }
+  }
+  // the wave's own words only: LDS operations of a wave stay in order
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  const uint32_t old = byte_mask(first - (at + 4 * kg));
+#pragma unroll
+  for (int j = 0; j < DJ; ++j) {
+    u32x4 c = *(const u32x4*)(tile_words + j * 256 + lane * 4);
+    if (old) {
+      const u32x4 was = *(const u32x4*)(vp + j * kUnit);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = v_ratio != 1.f ? rescale4(was[i], v_ratio) : was[i];
+        c[i] = (c[i] & ~old) | (w & old);
+      }
+    }
+    *(u32x4*)(vp + j * kUnit) = c;
+  }
+}
+
+// ----------------------------------------------------------- attention ----
+
+struct Attention {
+  Pool pool;
+  Rows rows;
+  Strided q, out;
+  const float* w_in;
+  float* w_out;
+  float* ws_o;     // [unit][split][unit_rows][D] sums of p v
+  f32x2* ws_ml;    // [unit][split][unit_rows] maximum and sum
+  float* ws_mass;  // [unit][unit_rows][cap_tiles] log2 of a tile's share of exp2(s)
+  float scale;     // scale * log2(e)
+  int32_t group;
+  int32_t m_rows;      // group * n_new: query rows of a key/value head
+  int32_t m_groups;    // units a head's query rows are cut into
+  int32_t unit_rows;   // query rows of a unit
+  int32_t cap_tiles;
+  uint32_t n_units;
+  uint32_t n_splits;
+  uint32_t weight_blocks;  // of a row, in the combining kernel
+};
+
+// What a unit (some query rows of a head) reads: the tiles up to what its
+// last query sees, cut into steps of 64 tokens, cut into splits.
+struct Plan {
+  uint32_t row, seq, head;
+  int m0;      // first query row
+  int origin;  // position of new token 0
+  int count;
+  int end;     // tokens that some query sees
+  int full;    // tokens that every query with any sees
+  int tiles, steps, split_steps, splits;
+};
+
+template <int MT>
+__device__ __forceinline__ Plan plan_unit(const Attention& a, uint32_t unit) {
+  Plan p;
+  p.row = unit / a.m_groups;
+  p.seq = p.row / a.rows.heads;
+  p.head = p.row % a.rows.heads;
+  p.m0 = (int)(unit % a.m_groups) * (MT * 16);
+  const int len = row_length(a.rows, p.row);
+  p.count = new_count(a.rows, p.seq);
+  p.origin = len - p.count;
+  const int t_low = p.m0 / a.group;
+  const int t_high = min((min(p.m0 + MT * 16, a.m_rows) - 1) / a.group, p.count - 1);
+  p.end = t_high >= t_low ? max(p.origin + t_high + 1, 0) : 0;
+  p.full = max(p.origin + t_low + 1, 1);
+  p.tiles = (p.end + kTile - 1) / kTile;
+  p.steps = (p.end + kStep - 1) / kStep;
+  // a split has a step for each of its waves at least
+  p.split_steps = max((p.steps + (int)a.n_splits - 1) / (int)a.n_splits, kWaves);
+  p.splits = (p.steps + p.split_steps - 1) / p.split_steps;
+  return p;
+}
+
+// Tokens of the row that query row m sees; 0: none, or no such row.
+__device__ __forceinline__ int seen_by(const Attention& a, const Plan& p, int m) {
+  const int t = m / a.group;
+  return m < a.m_rows && t < p.count ? max(p.origin + t + 1, 0) : 0;
+}
+
+__device__ __forceinline__ uint16_t* row_of(const Strided& x, const Attention& a, const Plan& p, int m) {
+  return x.data + p.seq * x.seq + (int64_t)(m / a.group) * x.token +
+         ((int64_t)p.head * a.group + m % a.group) * x.head;
+}
+
+template <int DJ, int MT>
+struct State {
+  f32x4 o[MT][4 * DJ];  // o[h * 4 + c][r]: dim 64 h + 16 c + 4 (lane / 16) + r of query lane % 16
+  float m[MT], l[MT];   // running maximum (log2) and sum of query lane % 16
+};
+
+template <int DJ>
+struct Tiles {
+  u32x4 k[kStepTiles][DJ], v[kStepTiles][DJ];
+  float ks[kStepTiles], vs[kStepTiles];
+  bool ok[kStepTiles];
+};
+
+template <int DJ>
+__device__ __forceinline__ void load_step(const Attention& a, const Plan& p, int step, int lane,
+                                          Tiles<DJ>& x) {
+#pragma unroll
+  for (int t = 0; t < kStepTiles; ++t) {
+    const int tile = step * kStepTiles + t;
+    int32_t id = -1;
+    if (tile < p.tiles)
+      id = a.rows.pages[(uint64_t)p.row * a.rows.max_pages + (tile >> a.pool.tile_shift)];
+    x.ok[t] = (uint32_t)id < a.pool.n_pages;
+    if (x.ok[t]) {
+      const uint64_t base = (uint64_t)(uint32_t)id * a.pool.page_bytes +
+                            (uint32_t)((tile & ((1 << a.pool.tile_shift) - 1)) * (DJ * kUnit));
+#pragma unroll
+      for (int j = 0; j < DJ; ++j)
+        x.k[t][j] = *(const u32x4*)(a.pool.k_codes + base + j * kUnit + lane * 16);
+#pragma unroll
+      for (int j = 0; j < DJ; ++j)
+        x.v[t][j] = *(const u32x4*)(a.pool.v_codes + base + j * kUnit + lane * 16);
+      x.ks[t] = a.pool.k_scales[id];
+      x.vs[t] = a.pool.v_scales[id];
+    } else {
+#pragma unroll
+      for (int j = 0; j < DJ; ++j) x.k[t][j] = x.v[t][j] = u32x4{0, 0, 0, 0};
+      x.ks[t] = x.vs[t] = 0.f;
+    }
+  }
+}
+
+// One step of a wave: 64 tokens against its 16 MT query rows.
+//   S^T = K Q^T: the lane gets the scores of query lane % 16 with tokens
+//   4 (lane / 16) + r of each tile.  These are, without any exchange, the
+//   P^T operand of O^T = V^T P^T when the matrix instruction's index k is
+//   taken as (tile of the pair, r) within lane / 16, and the layout of a value
+//   tile gives V^T in the same order.
+// P times the page's scale goes in as two 16-bit terms (bf16, so that any
+// scale fits): the products keep 16 bits of P.
+template <int DJ, bool F16, int MT, bool MASKED>
+__device__ __forceinline__ void attend_step(const Attention& a, const Plan& p, int step, int lane,
+                                            const u32x4 (&q)[MT][DJ][2], const int (&seen)[MT],
+                                            Tiles<DJ>& x, float* mass_row, State<DJ, MT>& st) {
+  const int g = lane / 16;
+  f32x4 s[MT][kStepTiles];
+#pragma unroll
+  for (int t = 0; t < kStepTiles; ++t) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) s[mt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < DJ; ++j)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const u32x4 kk = widen8<F16>(x.k[t][j][2 * half], x.k[t][j][2 * half + 1]);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) s[mt][t] = mfma<F16>(kk, q[mt][j][half], s[mt][t]);
+      }
+  }
+
+  const int at = step * kStep + 4 * g;  // the lane's first token
+  u32x4 hi[MT][2], lo[MT][2], sees[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < kStepTiles; ++t) {
+      const float c = x.ks[t] * a.scale;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float y = s[mt][t][r] * c;
+        if constexpr (MASKED)
+          if (!x.ok[t] || at + 16 * t + r >= seen[mt]) y = -INFINITY;
+        s[mt][t][r] = y;
+        top = fmaxf(top, y);
+      }
+    }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float m = fmaxf(st.m[mt], top);
+    const float base = m == -INFINITY ? 0.f : m;
+    const float keep = exp2_fast(st.m[mt] - base);
+    st.m[mt] = m;
+    float mass[kStepTiles], sum = 0.f;
+#pragma unroll
+    for (int t = 0; t < kStepTiles; ++t) {
+      float y[4], z[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        y[r] = exp2_fast(s[mt][t][r] - base);
+        z[r] = y[r] * x.vs[t];
+        if constexpr (MASKED) {
+          const bool on = x.ok[t] && at + 16 * t + r < seen[mt];
+          z[r] = on ? z[r] : 0.f;
+        }
+      }
+      mass[t] = (y[0] + y[1]) + (y[2] + y[3]);
+      const uint32_t h0 = pack_bf16(z[0], z[1]), h1 = pack_bf16(z[2], z[3]);
+      hi[mt][t / 2][t % 2 * 2] = h0;
+      hi[mt][t / 2][t % 2 * 2 + 1] = h1;
+      lo[mt][t / 2][t % 2 * 2] = pack_bf16(z[0] - bf16_low(h0), z[1] - bf16_high(h0));
+      lo[mt][t / 2][t % 2 * 2 + 1] = pack_bf16(z[2] - bf16_low(h1), z[3] - bf16_high(h1));
+      if constexpr (MASKED) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const int n = x.ok[t] ? seen[mt] - (at + 16 * t + 2 * w) : 0;
+          sees[mt][t / 2][t % 2 * 2 + w] = n <= 0 ? 0u : n == 1 ? 0x3F80u : 0x3F803F80u;
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kStepTiles; ++t) {
+      mass[t] += __shfl_xor(mass[t], 16);
+      mass[t] += __shfl_xor(mass[t], 32);
+      sum += mass[t];
+    }
+    st.l[mt] = st.l[mt] * keep + sum;
+#pragma unroll
+    for (int i = 0; i < 4 * DJ; ++i) st.o[mt][i] *= keep;
+    if (mass_row) {
+      const float mine = g == 0 ? mass[0] : g == 1 ? mass[1] : g == 2 ? mass[2] : mass[3];
+      const int tile = step * kStepTiles + g, m_local = mt * 16 + lane % 16;
+      if (tile < p.tiles && m_local < a.unit_rows)
+        mass_row[(uint64_t)m_local * a.cap_tiles + tile] = base + log2_fast(mine);
+    }
+  }
+
+#pragma unroll
+  for (int pair = 0; pair < 2; ++pair)
+#pragma unroll
+    for (int h = 0; h < DJ; ++h)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v0 = x.v[2 * pair][h][c], v1 = x.v[2 * pair + 1][h][c];
+        if constexpr (MASKED) {
+          // bytes past what any query sees may hold anything
+          v0 &= byte_mask(p.end - (at + 32 * pair));
+          v1 &= byte_mask(p.end - (at + 32 * pair + 16));
+          // a NaN that only some of the queries see: those get NaN, the
+          // products get 0 in its place
+          const uint32_t n0 = nan_codes(v0), n1 = nan_codes(v1);
+          if (__ballot((n0 | n1) != 0)) {
+            const uint32_t b0 = (n0 >> 7) * 255u, b1 = (n1 >> 7) * 255u;
+            const u32x4 is = widen8<false>(b0 & 0x38383838u, b1 & 0x38383838u);  // 1.0 where NaN
+            v0 &= ~b0;
+            v1 &= ~b1;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const f32x4 found = mfma<false>(is, sees[mt][pair], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (found[r] > 0.f) st.o[mt][h * 4 + c][r] = NAN;
+            }
+          }
+        }
+        const u32x4 vv = widen8<false>(v0, v1);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          st.o[mt][h * 4 + c] = mfma<false>(vv, hi[mt][pair], st.o[mt][h * 4 + c]);
+          st.o[mt][h * 4 + c] = mfma<false>(vv, lo[mt][pair], st.o[mt][h * 4 + c]);
+        }
+      }
+}
+
+// log2 of the sum of exp2 over a row's tokens; +inf where there is none, so
+// that every share comes out as 0.
+__device__ __forceinline__ float log_total(float m, float l) {
+  return l == 0.f ? INFINITY : (m == -INFINITY ? 0.f : m) + log2_fast(l);
+}
+
+// A workgroup takes one split of one unit; its waves take steps in turn and
+// join at the end.  With one split and one unit a row the result is written
+// here, else it is left in the workspace for the combining kernel.
+template <int DJ, bool F16, int MT>
+__global__ __launch_bounds__(kThreads) void attention_kernel(Attention a) {
+  constexpr int D = 64 * DJ;
+  constexpr int kPitch = 64 + 4;  // floats of a query row of 64 dims in LDS
+  __shared__ __attribute__((aligned(16))) float s_o[kWaves][16][kPitch];
+  __shared__ f32x2 s_ml[kWaves][MT * 16];
+  __shared__ float s_lse[MT * 16];
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const uint32_t unit = blockIdx.x % a.n_units, split = blockIdx.x / a.n_units;
+  const bool direct = a.n_splits == 1 && a.m_groups == 1;
+  const Plan p = plan_unit<MT>(a, unit);
+  const int first = (int)split * p.split_steps;
+  const int last = min(first + p.split_steps, p.steps);
+  if (first >= last && !direct) return;
+
+  u32x4 q[MT][DJ][2];
+  int seen[MT];
+  State<DJ, MT> st;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int m = p.m0 + mt * 16 + lane % 16;
+    seen[mt] = seen_by(a, p, m);
+    const uint16_t* src = row_of(a.q, a, p, m) + 16 * (lane / 16);
+#pragma unroll
+    for (int j = 0; j < DJ; ++j)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        u16x8 x = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (seen[mt] > 0) {
+          if (a.q.wide) {
+            x = *(const u16x8*)(src + 64 * j + 8 * half);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = src[64 * j + 8 * half + i];
+          }
+        }
+        q[mt][j][half] = __builtin_bit_cast(u32x4, x);
+      }
+    st.m[mt] = -INFINITY;
+    st.l[mt] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4 * DJ; ++i) st.o[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  float* mass_row = a.w_out ? a.ws_mass + (uint64_t)unit * a.unit_rows * a.cap_tiles : nullptr;
+
+  for (int step = first + wave; step < last; step += kWaves) {
+    Tiles<DJ> x;
+    load_step<DJ>(a, p, step, lane, x);
+    if (step * kStep + kStep <= p.full && x.ok[0] && x.ok[1] && x.ok[2] && x.ok[3])
+      attend_step<DJ, F16, MT, false>(a, p, step, lane, q, seen, x, mass_row, st);
+    else
+      attend_step<DJ, F16, MT, true>(a, p, step, lane, q, seen, x, mass_row, st);
+  }
+
+  if (lane < 16) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) s_ml[wave][mt * 16 + lane] = f32x2{st.m[mt], st.l[mt]};
+  }
+  __syncthreads();
+  const int n = threadIdx.x / 16, d4 = threadIdx.x % 16 * 4;  // query and dims of the joining
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int m_local = mt * 16 + n, m = p.m0 + m_local;
+    float top = -INFINITY, total = 0.f, f[kWaves];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_ml[w][m_local][0]);
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      f[w] = exp2_fast(s_ml[w][m_local][0] - base);
+      total += s_ml[w][m_local][1] * f[w];
+    }
+    const uint64_t part = ((uint64_t)unit * a.n_splits + split) * a.unit_rows + m_local;
+    const bool here = m_local < a.unit_rows && m < a.m_rows;
+    const float share = total == 0.f ? 0.f : 1.f / total;
+    const bool any = seen_by(a, p, m) > 0;
+    if (d4 == 0) {
+      if (direct)
+        s_lse[m_local] = log_total(top, total);
+      else if (here)
+        a.ws_ml[part] = f32x2{top, total};
+    }
+#pragma unroll
+    for (int h = 0; h < DJ; ++h) {
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        *(f32x4*)&s_o[wave][lane % 16][16 * c + 4 * (lane / 16)] = st.o[mt][h * 4 + c];
+      __syncthreads();
+      f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) o += *(const f32x4*)&s_o[w][n][d4] * f[w];
+      if (!here) continue;
+      const int d = 64 * h + d4;
+      if (direct) {
+        uint16_t* dst = row_of(a.out, a, p, m) + d;
+        u16x4 y;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[r] = any ? to_half<F16>(o[r] * share) : 0;
+        if (a.out.wide) {
+          *(u16x4*)dst = y;
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) dst[r] = y[r];
+        }
+      } else {
+        *(f32x4*)(a.ws_o + part * D + d) = o;
+      }
+    }
+  }
+  if (!direct || !a.w_out) return;
+  __syncthreads();
+  const uint64_t w_at = (uint64_t)p.row * a.rows.max_pages;
+  for (uint32_t page = threadIdx.x; page < a.rows.max_pages; page += kThreads) {
+    float w = 0.f;
+    const int t0 = (int)(page << a.pool.tile_shift);
+    const int t1 = min(t0 + (1 << a.pool.tile_shift), p.tiles);
+    for (int m = 0; m < a.unit_rows; ++m) {
+      if (seen_by(a, p, p.m0 + m) == 0) continue;
+      for (int t = t0; t < t1; ++t)
+        w += exp2_fast(mass_row[(uint64_t)m * a.cap_tiles + t] - s_lse[m]);
+    }
+    a.w_out[w_at + page] = a.w_in[w_at + page] + w;
+  }
+}
+
+// Joins the splits.  Workgroups below n_units * unit_rows take one query row
+// each; the others take 256 pages of a row each and sum their weights.
+template <int DJ, bool F16, int MT>
+__global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
+  constexpr int D = 64 * DJ;
+  constexpr int kVec = D / 4;                 // threads of a row of the output
+  constexpr int kGroups = kThreads / kVec;    // splits summed at a time
+  __shared__ __attribute__((aligned(16))) f32x4 s_sum[kGroups][kVec];
+  __shared__ float s_f[kThreads];
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const uint32_t out_blocks = a.n_units * (uint32_t)a.unit_rows;
+  if (blockIdx.x < out_blocks) {
+    const uint32_t unit = blockIdx.x / a.unit_rows;
+    const int m_local = (int)(blockIdx.x % a.unit_rows);
+    const Plan p = plan_unit<MT>(a, unit);
+    const int m = p.m0 + m_local;
+    if (m >= a.m_rows) return;
+    const bool any = seen_by(a, p, m) > 0;
+    const int splits = any ? p.splits : 0;
+    // kMaxSplits is a wave's lanes
+    f32x2 ml = {-INFINITY, 0.f};
+    if (lane < splits) ml = a.ws_ml[((uint64_t)unit * a.n_splits + lane) * a.unit_rows + m_local];
+    const float top = wave_max(ml[0]);
+    const float base = top == -INFINITY ? 0.f : top;
+    const float f = exp2_fast(ml[0] - base);
+    float total = ml[1] * f;
+#pragma unroll
+    for (int s = 32; s; s >>= 1) total += __shfl_xor(total, s);
+    if (wave == 0) s_f[lane] = total == 0.f ? 0.f : f / total;
+    __syncthreads();
+    const int d4 = threadIdx.x % kVec, group = threadIdx.x / kVec;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    if (group < kGroups) {
+      for (int s = group; s < splits; s += kGroups)
+        o += *(const f32x4*)(a.ws_o + (((uint64_t)unit * a.n_splits + s) * a.unit_rows + m_local) * D + 4 * d4) * s_f[s];
+      s_sum[group][d4] = o;
+    }
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) o += s_sum[i][d4];
+    uint16_t* dst = row_of(a.out, a, p, m) + 4 * d4;
+    u16x4 y;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) y[r] = to_half<F16>(o[r]);
+    if (a.out.wide) {
+      *(u16x4*)dst = y;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) dst[r] = y[r];
+    }
+    return;
+  }
+
+  const uint32_t b = blockIdx.x - out_blocks;
+  const uint32_t row = b / a.weight_blocks;
+  const uint32_t page = b % a.weight_blocks * kThreads + threadIdx.x;
+  const int t0 = (int)(page << a.pool.tile_shift);
+  float w = 0.f;
+  for (int g = 0; g < a.m_groups; ++g) {
+    const uint32_t unit = row * a.m_groups + g;
+    const Plan p = plan_unit<MT>(a, unit);
+    __syncthreads();
+    for (int m = wave; m < a.unit_rows; m += kWaves) {
+      f32x2 ml = {-INFINITY, 0.f};
+      if (lane < p.splits && seen_by(a, p, p.m0 + m) > 0)
+        ml = a.ws_ml[((uint64_t)unit * a.n_splits + lane) * a.unit_rows + m];
+      const float top = wave_max(ml[0]);
+      float total = ml[1] * exp2_fast(ml[0] - (top == -INFINITY ? 0.f : top));
+#pragma unroll
+      for (int s = 32; s; s >>= 1) total += __shfl_xor(total, s);
+      if (lane == 0) s_f[m] = log_total(top, total);
+    }
+    __syncthreads();
+    if (page >= a.rows.max_pages) continue;
+    const int t1 = min(t0 + (1 << a.pool.tile_shift), p.tiles);
+    for (int m = 0; m < a.unit_rows; ++m) {
+      if (seen_by(a, p, p.m0 + m) == 0) continue;
+      const float* mass = a.ws_mass + ((uint64_t)unit * a.unit_rows + m) * a.cap_tiles;
+      for (int t = t0; t < t1; ++t) w += exp2_fast(mass[t] - s_f[m]);
+    }
+  }
+  if (page < a.rows.max_pages) {
+    const uint64_t at = (uint64_t)row * a.rows.max_pages + page;
+    a.w_out[at] = a.w_in[at] + w;
+  }
+}
+
+// ------------------------------------------------------------ eviction ----
+
+struct Evict {
+  const int32_t* pages;
+  const int32_t* lengths;
+  const float* weights;
+  int32_t* pages_out;
+  float* weights_out;
+  int32_t* lengths_out;
+  uint32_t max_pages;
+  int32_t capacity;
+  uint32_t page_shift;  // log2 of a page's tokens
+  uint32_t keep, sink, recent;
+};
+
+// Whole numbers in the order of the weights.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  uint32_t b = __builtin_bit_cast(uint32_t, w);
+  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return ~0u;
+  if (b == 0x80000000u) b = 0u;
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// One workgroup per row.  The weight of the last page to stay is found digit
+// by digit (8 bits at a time, from counts of the digits in LDS), then one pass in
+// order writes every page to its place.
+__global__ __launch_bounds__(kThreads) void evict_kernel(Evict e) {
+  __shared__ uint32_t s_count[256];
+  __shared__ uint32_t s_pick[2];
+  __shared__ uint32_t s_sum[2][kWaves];
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const uint32_t row = blockIdx.x;
+  const uint64_t at = (uint64_t)row * e.max_pages;
+  const float* weights = e.weights + at;
+  const int len = min(max(e.lengths[row], 0), e.capacity);
+  const uint32_t held = ((uint32_t)len + (1u << e.page_shift) - 1u) >> e.page_shift;
+  const bool full = held > e.keep;
+  const uint32_t left = full ? e.keep : held;
+  if (threadIdx.x == 0) e.lengths_out[row] = len - (int)((held - left) << e.page_shift);
+  const uint32_t lo = e.sink, hi = full ? held - e.recent : held;  // the pages to choose from
+
+  uint32_t key = 0, want = full ? e.keep - e.sink - e.recent : 0;
+  if (full && want) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      s_count[threadIdx.x] = 0;
+      __syncthreads();
+      for (uint32_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+        const uint32_t k = weight_key(weights[i]);
+        if (shift == 24 || (k ^ key) >> (shift + 8) == 0) atomicAdd(&s_count[(k >> shift) & 255u], 1u);
+      }
+      __syncthreads();
+      if (wave == 0) {  // lane l: digits 255 - 4 l down to 252 - 4 l
+        uint32_t c[4], mine = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mine += c[i] = s_count[255 - 4 * lane - i];
+        uint32_t before = mine;
+#pragma unroll
+        for (int s = 1; s < kWave; s <<= 1) {
+          const uint32_t y = __shfl_up(before, s);
+          if (lane >= s) before += y;
+        }
+        before -= mine;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (before < want && before + c[i] >= want) {
+            s_pick[0] = 255u - 4u * lane - i;
+            s_pick[1] = want - before;
+          }
+          before += c[i];
+        }
+      }
+      __syncthreads();
+      key |= s_pick[0] << shift;
+      want = s_pick[1];
+    }
+  }
+
+  // kept: above the key, the first `want` equal to it, and the protected ones
+  uint32_t above_before = 0, equal_before = 0;
+  for (uint32_t base = 0; base < e.max_pages; base += kThreads) {
+    const uint32_t i = base + threadIdx.x;
+    const bool in = i < e.max_pages;
+    const float w = in ? weights[i] : 0.f;
+    const int32_t id = in ? e.pages[at + i] : 0;
+    const bool middle = full && i >= lo && i < hi;
+    const uint32_t k = weight_key(w);
+    const bool above = i < held && (!middle || (want && k > key));
+    const bool equal = middle && want && k == key;
+    const uint64_t ba = __ballot(above), be = __ballot(equal);
+    if (lane == 0) {
+      s_sum[0][wave] = (uint32_t)__popcll(ba);
+      s_sum[1][wave] = (uint32_t)__popcll(be);
+    }
+    __syncthreads();
+    uint32_t a = above_before, q = equal_before;
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) {
+      if (x < wave) {
+        a += s_sum[0][x];
+        q += s_sum[1][x];
+      }
+      above_before += s_sum[0][x];
+      equal_before += s_sum[1][x];
+    }
+    __syncthreads();
+    const uint64_t under = (1ull << lane) - 1ull;
+    a += (uint32_t)__popcll(ba & under);
+    q += (uint32_t)__popcll(be & under);
+    if (in) {
+      const bool kept = above || (equal && q < want);
+      const uint32_t kept_before = a + min(q, want);
+      uint32_t to = i;
+      if (i < held) to = kept ? kept_before : left + (i - kept_before);
+      e.pages_out[at + to] = id;
+      e.weights_out[at + to] = i < held && !kept ? 0.f : w;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host ----
+
+thread_local int g_last_hip = 0;
+
+int hip_fail(hipError_t e) {
+  g_last_hip = (int)e;
+  return IBP_ERR_HIP;
+}
+
+int pending_hip_error() {
+  const hipError_t e = hipPeekAtLastError();
+  return e == hipSuccess ? IBP_OK : hip_fail(e);
+}
+
+int launched() {
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? IBP_OK : hip_fail(e);
+}
+
+bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
+
+constexpr uint64_t kMaxGrid = 0x7FFFFFFFull;
+
+int check_cache(const ibp_kv_cache* c) {
+  if (!c) return IBP_ERR_INVALID_ARGUMENT;
+  if (c->page_tokens != 16 && c->page_tokens != 32 && c->page_tokens != 64) return IBP_ERR_UNSUPPORTED;
+  if (c->head_dim == 0 || c->head_dim % 64 || c->head_dim > 256) return IBP_ERR_UNSUPPORTED;
+  if (c->n_pages == 0) return IBP_OK;  // every id is a hole
+  if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return IBP_ERR_INVALID_ARGUMENT;
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 4) ||
+      !aligned(c->v_scales, 4))
+    return IBP_ERR_LAYOUT;
+  return IBP_OK;
+}
+
+// 0 rows is no error; the caller returns at once.
+int check_table(const ibp_kv_table* t, uint64_t page_tokens, uint64_t* n_rows) {
+  if (!t) return IBP_ERR_INVALID_ARGUMENT;
+  if (t->n_seqs && t->kv_heads > (1ull << 30) / t->n_seqs) return IBP_ERR_INVALID_ARGUMENT;
+  *n_rows = t->n_seqs * t->kv_heads;
+  if (*n_rows == 0) return IBP_OK;
+  if (t->max_pages > 0x7FFFFFFFull / page_tokens) return IBP_ERR_INVALID_ARGUMENT;
+  if (!t->lengths || (t->max_pages && !t->pages)) return IBP_ERR_INVALID_ARGUMENT;
+  if (!aligned(t->lengths, 4) || !aligned(t->pages, 4)) return IBP_ERR_LAYOUT;
+  return IBP_OK;
+}
+
+int check_tensor(const ibp_kv_tensor* x) {
+  if (!x || !x->data) return IBP_ERR_INVALID_ARGUMENT;
+  return aligned(x->data, 2) ? IBP_OK : IBP_ERR_LAYOUT;
+}
+
+Pool make_pool(const ibp_kv_cache* c) {
+  Pool p;
+  p.k_codes = c->k_codes;
+  p.k_scales = c->k_scales;
+  p.v_codes = c->v_codes;
+  p.v_scales = c->v_scales;
+  p.n_pages = (uint32_t)std::min<uint64_t>(c->n_pages, 1ull << 31);
+  p.page_bytes = c->page_tokens * c->head_dim;
+  p.tile_shift = c->page_tokens == 16 ? 0 : c->page_tokens == 32 ? 1 : 2;
+  return p;
+}
+
+Rows make_rows(const ibp_kv_table* t, uint32_t page_tokens, uint64_t n_new, const int32_t* counts) {
+  Rows r;
+  r.pages = t->pages;
+  r.lengths = t->lengths;
+  r.counts = counts;
+  r.heads = (uint32_t)t->kv_heads;
+  r.max_pages = (uint32_t)t->max_pages;
+  r.capacity = (int32_t)(t->max_pages * page_tokens);
+  r.n_new = (int32_t)n_new;
+  return r;
+}
+
+Strided make_strided(const ibp_kv_tensor* x) {
+  Strided s;
+  s.data = (uint16_t*)x->data;
+  s.seq = x->seq_stride;
+  s.token = x->token_stride;
+  s.head = x->head_stride;
+  s.wide = aligned(x->data, 16) && x->seq_stride % 8 == 0 && x->token_stride % 8 == 0 &&
+           x->head_stride % 8 == 0;
+  return s;
+}
+
+template <int DJ, bool F16>
+void launch_append(const Pool& pool, const Rows& rows, const Strided& k, const Strided& v,
+                   uint32_t pages_per_row, uint64_t tasks, hipStream_t st) {
+  const uint64_t per_group = kWaves >> pool.tile_shift;
+  hipLaunchKernelGGL((append_kernel<DJ, F16>), dim3((uint32_t)((tasks + per_group - 1) / per_group)),
+                     dim3(kThreads), 0, st, pool, rows, k, v, pages_per_row, tasks);
+}
+
+// How the query rows of a head are cut: at most 64 to a unit, 32 where the
+// accumulators of wide heads would not fit the registers.
+struct Shape {
+  int mt;
+  int32_t m_rows, m_groups, unit_rows, cap_tiles;
+  uint32_t n_units, n_splits;
+  uint64_t mass_at, ml_at, bytes;  // in the workspace; the sums come first
+};
+
+// Compute units of the current device; 256 where a HIP error is pending, which
+// is not this library's to clear, and where there is no device.
+int compute_units() {
+  int dev = 0, n = 0;
+  if (hipPeekAtLastError() != hipSuccess) return 256;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) {
+    (void)hipGetLastError();
+    n = 0;
+  }
+  return n > 0 ? n : 256;
+}
+
+bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint32_t head_dim,
+                uint64_t group, uint64_t n_new, bool weights, int cus, Shape* s) {
+  if (n_new && group > (1ull << 24) / n_new) return false;
+  const uint64_t m = group * n_new;
+  s->m_rows = (int32_t)m;
+  s->mt = m <= 16 ? 1 : m <= 32 || head_dim > 128 ? 2 : 4;
+  const uint64_t per_unit = 16ull * s->mt;
+  s->m_groups = (int32_t)((m + per_unit - 1) / per_unit);
+  s->unit_rows = (int32_t)std::min<uint64_t>(m, per_unit);
+  s->cap_tiles = (int32_t)(max_pages * page_tokens / kTile);
+  const uint64_t units = n_rows * s->m_groups;
+  if (units > kMaxGrid / 64) return false;
+  s->n_units = (uint32_t)units;
+  // four workgroups a compute unit, and a step for each wave of a split
+  const uint64_t steps = ((uint64_t)max_pages * page_tokens + kStep - 1) / kStep;
+  uint64_t splits = units ? (4ull * cus + units - 1) / units : 1;
+  splits = std::min<uint64_t>(splits, (steps + kWaves - 1) / kWaves);
+  s->n_splits = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(splits, kMaxSplits));
+  const bool direct = s->n_splits == 1 && s->m_groups <= 1;
+  const uint64_t parts = direct ? 0 : units * s->n_splits * s->unit_rows;
+  s->ml_at = parts * head_dim * 4;
+  s->mass_at = (s->ml_at + parts * 8 + 15) / 16 * 16;
+  s->bytes = s->mass_at + (weights ? units * s->unit_rows * s->cap_tiles * 4 : 0);
+  if (units * s->unit_rows > kMaxGrid / 2) return false;
+  return true;
+}
+
+template <int DJ, bool F16, int MT>
+void launch_attention(const Attention& a, uint64_t n_rows, hipStream_t st) {
+  const bool direct = a.n_splits == 1 && a.m_groups == 1;
+  if (a.n_units)
+    hipLaunchKernelGGL((attention_kernel<DJ, F16, MT>), dim3(a.n_units * a.n_splits), dim3(kThreads),
+                       0, st, a);
+  if (direct) return;
+  const uint64_t blocks = (uint64_t)a.n_units * a.unit_rows + (a.w_out ? n_rows * a.weight_blocks : 0);
+  if (blocks)
+    hipLaunchKernelGGL((combine_kernel<DJ, F16, MT>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a);
+}
+
+template <int DJ, bool F16>
+void launch_attention_mt(const Attention& a, int mt, uint64_t n_rows, hipStream_t st) {
+  if (mt == 1) return launch_attention<DJ, F16, 1>(a, n_rows, st);
+  if (DJ > 2 || mt == 2) return launch_attention<DJ, F16, 2>(a, n_rows, st);
+  if constexpr (DJ <= 2) launch_attention<DJ, F16, 4>(a, n_rows, st);
+}
+
+bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return na && nb && x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ibp_kv_last_hip_error(void) { return g_last_hip; }
+
+const char* ibp_kv_status_string(int status) {
+  switch (status) {
+    case IBP_OK: return "ok";
+    case IBP_ERR_INVALID_ARGUMENT: return "invalid argument";
+    case IBP_ERR_UNSUPPORTED: return "unsupported page size, head size or type";
+    case IBP_ERR_LAYOUT: return "misaligned pointer";
+    case IBP_ERR_HIP: return "HIP error";
+    default: return "unknown status";
+  }
+}
+
+int ibp_kv_append(const ibp_kv_cache* cache, const ibp_kv_table* table, uint32_t dtype,
+                  uint64_t n_new, const ibp_kv_tensor* k, const ibp_kv_tensor* v,
+                  const int32_t* counts, void* stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (dtype > IBP_KV_FP16) return IBP_ERR_UNSUPPORTED;
+  uint64_t n_rows = 0;
+  rc = check_table(table, cache->page_tokens, &n_rows);
+  if (rc || n_rows == 0 || n_new == 0 || table->max_pages == 0 || cache->n_pages == 0) return rc;
+  if (n_new > 0x7FFFFFFFull) return IBP_ERR_INVALID_ARGUMENT;
+  if ((rc = check_tensor(k)) || (rc = check_tensor(v))) return rc;
+  if (!aligned(counts, 4)) return IBP_ERR_LAYOUT;
+  const uint64_t pt = cache->page_tokens;
+  const uint64_t per_row = std::min<uint64_t>((n_new + pt - 2) / pt + 1, table->max_pages);
+  if (per_row > kMaxGrid / n_rows) return IBP_ERR_INVALID_ARGUMENT;
+  rc = pending_hip_error();
+  if (rc) return rc;
+  const Pool pool = make_pool(cache);
+  const Rows rows = make_rows(table, cache->page_tokens, n_new, counts);
+  const Strided ks = make_strided(k), vs = make_strided(v);
+  hipStream_t st = (hipStream_t)stream;
+  const uint64_t tasks = n_rows * per_row;
+  switch (cache->head_dim / 64 * 2 + dtype) {
+    case 2: launch_append<1, false>(pool, rows, ks, vs, (uint32_t)per_row, tasks, st); break;
+    case 3: launch_append<1, true>(pool, rows, ks, vs, (uint32_t)per_row, tasks, st); break;
+    case 4: launch_append<2, false>(pool, rows, ks, vs, (uint32_t)per_row, tasks, st); break;
+    case 5: launch_append<2, true>(pool, rows, ks, vs, (uint32_t)per_row, tasks, st); break;
+    case 6: launch_append<3, false>(pool, rows, ks, vs, (uint32_t)per_row, tasks, st); break;
+    case 7: launch_append<3, true>(pool, rows, ks, vs, (uint32_t)per_row, tasks, st); break;
+    case 8: launch_append<4, false>(pool, rows, ks, vs, (uint32_t)per_row, tasks, st); break;
+    default: launch_append<4, true>(pool, rows, ks, vs, (uint32_t)per_row, tasks, st); break;
+  }
+  return launched();
+}
+
+uint64_t ibp_kv_attention_workspace_bytes(const ibp_kv_cache* cache, const ibp_kv_table* table,
+                                          uint64_t q_heads, uint64_t n_new, int with_weights) {
+  uint64_t n_rows = 0;
+  if (check_cache(cache) || !table || table->kv_heads == 0 || q_heads % table->kv_heads) return 0;
+  if (table->n_seqs && table->kv_heads > (1ull << 30) / table->n_seqs) return 0;
+  if (table->max_pages > 0x7FFFFFFFull / cache->page_tokens) return 0;
+  n_rows = table->n_seqs * table->kv_heads;
+  Shape s;
+  if (!make_shape(n_rows, table->max_pages, cache->page_tokens, cache->head_dim,
+                  q_heads / table->kv_heads, n_new, with_weights != 0, compute_units(), &s))
+    return 0;
+  return s.bytes;
+}
+
+int ibp_kv_attention(const ibp_kv_cache* cache, const ibp_kv_table* table, uint32_t dtype,
+                     uint64_t q_heads, uint64_t n_new, const ibp_kv_tensor* q,
+                     const ibp_kv_tensor* out, const int32_t* counts, float scale,
+                     const float* weights, float* weights_out, void* workspace,
+                     uint64_t workspace_bytes, void* stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (dtype > IBP_KV_FP16) return IBP_ERR_UNSUPPORTED;
+  uint64_t n_rows = 0;
+  rc = check_table(table, cache->page_tokens, &n_rows);
+  if (rc || n_rows == 0) return rc;
+  if (q_heads == 0 || q_heads % table->kv_heads || !weights != !weights_out || !(scale - scale == 0.f))
+    return IBP_ERR_INVALID_ARGUMENT;
+  if (n_new && ((rc = check_tensor(q)) || (rc = check_tensor(out)))) return rc;
+  if (!aligned(counts, 4) || !aligned(weights, 4) || !aligned(weights_out, 4)) return IBP_ERR_LAYOUT;
+  if (!aligned(workspace, 16)) return IBP_ERR_LAYOUT;
+  Shape s;
+  if (!make_shape(n_rows, table->max_pages, cache->page_tokens, cache->head_dim,
+                  q_heads / table->kv_heads, n_new, weights != nullptr, compute_units(), &s))
+    return IBP_ERR_INVALID_ARGUMENT;
+  if (s.bytes && (!workspace || workspace_bytes < s.bytes)) return IBP_ERR_INVALID_ARGUMENT;
+  rc = pending_hip_error();
+  if (rc) return rc;
+  Attention a{};
+  a.pool = make_pool(cache);
+  a.rows = make_rows(table, cache->page_tokens, n_new, counts);
+  if (n_new) {
+    a.q = make_strided(q);
+    a.out = make_strided(out);
+  }
+  a.w_in = weights;
+  a.w_out = weights_out;
+  a.ws_o = (float*)workspace;
+  a.ws_ml = (f32x2*)((char*)workspace + s.ml_at);
+  a.ws_mass = (float*)((char*)workspace + s.mass_at);
+  a.scale = scale * 1.44269504088896340736f;
+  a.group = (int32_t)(q_heads / table->kv_heads);
+  a.m_rows = s.m_rows;
+  a.m_groups = s.m_groups;
+  a.unit_rows = s.unit_rows;
+  a.cap_tiles = s.cap_tiles;
+  a.n_units = s.n_units;
+  a.n_splits = s.n_splits;
+  a.weight_blocks = (a.rows.max_pages + kThreads - 1) / kThreads;
+  hipStream_t st = (hipStream_t)stream;
+  switch (cache->head_dim / 64 * 2 + dtype) {
+    case 2: launch_attention_mt<1, false>(a, s.mt, n_rows, st); break;
+    case 3: launch_attention_mt<1, true>(a, s.mt, n_rows, st); break;
+    case 4: launch_attention_mt<2, false>(a, s.mt, n_rows, st); break;
+    case 5: launch_attention_mt<2, true>(a, s.mt, n_rows, st); break;
+    case 6: launch_attention_mt<3, false>(a, s.mt, n_rows, st); break;
+    case 7: launch_attention_mt<3, true>(a, s.mt, n_rows, st); break;
+    case 8: launch_attention_mt<4, false>(a, s.mt, n_rows, st); break;
+    default: launch_attention_mt<4, true>(a, s.mt, n_rows, st); break;
+  }
+  return launched();
+}
+
+int ibp_kv_evict(const ibp_kv_table* table, uint32_t page_tokens, uint64_t keep_pages,
+                 uint64_t sink_pages, uint64_t recent_pages, const float* weights,
+                 int32_t* pages_out, float* weights_out, int32_t* lengths_out, void* stream) {
+  if (page_tokens != 16 && page_tokens != 32 && page_tokens != 64) return IBP_ERR_UNSUPPORTED;
+  uint64_t n_rows = 0;
+  int rc = check_table(table, page_tokens, &n_rows);
+  if (rc) return rc;
+  if (recent_pages == 0 || sink_pages > keep_pages || recent_pages > keep_pages - sink_pages)
+    return IBP_ERR_INVALID_ARGUMENT;
+  if (n_rows == 0) return IBP_OK;
+  const uint64_t n = n_rows * table->max_pages * 4, nl = n_rows * 4;
+  if (!lengths_out || (n && (!weights || !pages_out || !weights_out))) return IBP_ERR_INVALID_ARGUMENT;
+  if (!aligned(weights, 4) || !aligned(pages_out, 4) || !aligned(weights_out, 4) || !aligned(lengths_out, 4))
+    return IBP_ERR_LAYOUT;
+  const void* in[3] = {table->pages, weights, table->lengths};
+  void* outs[3] = {pages_out, weights_out, lengths_out};
+  const uint64_t size[3] = {n, n, nl};
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < 3; ++j)
+      if (overlap(in[i], size[i], outs[j], size[j]) || (i < j && overlap(outs[i], size[i], outs[j], size[j])))
+        return IBP_ERR_INVALID_ARGUMENT;
+  if (n_rows > kMaxGrid) return IBP_ERR_INVALID_ARGUMENT;
+  rc = pending_hip_error();
+  if (rc) return rc;
+  Evict e;
+  e.pages = table->pages;
+  e.lengths = table->lengths;
+  e.weights = weights;
+  e.pages_out = pages_out;
+  e.weights_out = weights_out;
+  e.lengths_out = lengths_out;
+  e.max_pages = (uint32_t)table->max_pages;
+  e.capacity = (int32_t)(table->max_pages * page_tokens);
+  e.page_shift = page_tokens == 16 ? 4 : page_tokens == 32 ? 5 : 6;
+  e.keep = (uint32_t)std::min<uint64_t>(keep_pages, 0xFFFFFFFFull);
+  e.sink = (uint32_t)std::min<uint64_t>(sink_pages, 0xFFFFFFFFull);
+  e.recent = (uint32_t)std::min<uint64_t>(recent_pages, 0xFFFFFFFFull);
+  hipLaunchKernelGGL(evict_kernel, dim3((uint32_t)n_rows), dim3(kThreads), 0, (hipStream_t)stream, e);
+  return launched();
+}
+
+}  // extern "C"
