@@ -15,8 +15,9 @@ constexpr int kWave = 64;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kTile = 16;       // tokens of a tile
-constexpr int kStepTiles = 4;   // tiles a wave takes at a time
-constexpr int kStep = kTile * kStepTiles;
+// Tiles that a wave takes at a time: 64 tokens, 32 of wide heads, whose tiles
+// and accumulators take twice the registers.
+constexpr int step_tiles(int dj, int mt) { return dj * mt <= 2 ? 4 : 2; }
 constexpr int kUnit = 1024;     // bytes of a tile that one wide load of a wave takes
 constexpr int kMaxSplits = 64;
 constexpr int kExpMin = -126, kExpMax = 119;  // exponents of a page's scale
@@ -392,7 +393,7 @@ struct Attention {
 };
 
 // What a unit (some query rows of a head) reads: the tiles up to what its
-// last query sees, cut into steps of 64 tokens, cut into splits.
+// last query sees, cut into steps, cut into splits.
 struct Plan {
   uint32_t row, seq, head;
   int m0;      // first query row
@@ -403,7 +404,7 @@ struct Plan {
   int tiles, steps, split_steps, splits;
 };
 
-template <int MT>
+template <int DJ, int MT>
 __device__ __forceinline__ Plan plan_unit(const Attention& a, uint32_t unit) {
   Plan p;
   p.row = unit / a.m_groups;
@@ -418,7 +419,7 @@ __device__ __forceinline__ Plan plan_unit(const Attention& a, uint32_t unit) {
   p.end = t_high >= t_low ? max(p.origin + t_high + 1, 0) : 0;
   p.full = max(p.origin + t_low + 1, 1);
   p.tiles = (p.end + kTile - 1) / kTile;
-  p.steps = (p.end + kStep - 1) / kStep;
+  p.steps = (p.tiles + step_tiles(DJ, MT) - 1) / step_tiles(DJ, MT);
   // a split has a step for each of its waves at least
   p.split_steps = max((p.steps + (int)a.n_splits - 1) / (int)a.n_splits, kWaves);
   p.splits = (p.steps + p.split_steps - 1) / p.split_steps;
@@ -439,173 +440,226 @@ __device__ __forceinline__ uint16_t* row_of(const Strided& x, const Attention& a
 template <int DJ, int MT>
 struct State {
   f32x4 o[MT][4 * DJ];  // o[h * 4 + c][r]: dim 64 h + 16 c + 4 (lane / 16) + r of query lane % 16
-  float m[MT], l[MT];   // running maximum (log2) and sum of query lane % 16
+  float m[MT];          // running maximum (log2) of query lane % 16
+  float l[MT];          // the lane's part of the running sum
 };
 
-template <int DJ>
-struct Tiles {
-  u32x4 k[kStepTiles][DJ], v[kStepTiles][DJ];
-  float ks[kStepTiles], vs[kStepTiles];
-  bool ok[kStepTiles];
-};
-
-template <int DJ>
-__device__ __forceinline__ void load_step(const Attention& a, const Plan& p, int step, int lane,
-                                          Tiles<DJ>& x) {
-#pragma unroll
-  for (int t = 0; t < kStepTiles; ++t) {
-    const int tile = step * kStepTiles + t;
-    int32_t id = -1;
-    if (tile < p.tiles)
-      id = a.rows.pages[(uint64_t)p.row * a.rows.max_pages + (tile >> a.pool.tile_shift)];
-    x.ok[t] = (uint32_t)id < a.pool.n_pages;
-    if (x.ok[t]) {
-      const uint64_t base = (uint64_t)(uint32_t)id * a.pool.page_bytes +
-                            (uint32_t)((tile & ((1 << a.pool.tile_shift) - 1)) * (DJ * kUnit));
-#pragma unroll
-      for (int j = 0; j < DJ; ++j)
-        x.k[t][j] = *(const u32x4*)(a.pool.k_codes + base + j * kUnit + lane * 16);
-#pragma unroll
-      for (int j = 0; j < DJ; ++j)
-        x.v[t][j] = *(const u32x4*)(a.pool.v_codes + base + j * kUnit + lane * 16);
-      x.ks[t] = a.pool.k_scales[id];
-      x.vs[t] = a.pool.v_scales[id];
-    } else {
-#pragma unroll
-      for (int j = 0; j < DJ; ++j) x.k[t][j] = x.v[t][j] = u32x4{0, 0, 0, 0};
-      x.ks[t] = x.vs[t] = 0.f;
-    }
-  }
+// Read-only data at an address that is the same for the whole wave: scalar
+// loads, which the compiler does not choose by itself next to stores.
+template <class T>
+__device__ __forceinline__ T scalar(const T* p) {
+  return *(const __attribute__((address_space(4))) T*)p;
 }
 
-// One step of a wave: 64 tokens against its 16 MT query rows.
+// The pages of a step's tiles.  Tiles that are holes or past the row's end
+// have `ok` unset and the id of a page that can be read all the same.
+template <int ST>
+struct Where {
+  uint64_t at[ST];  // byte of the tile in the pool
+  float ks[ST], vs[ST];
+  bool ok[ST];
+};
+
+template <int DJ, int ST>
+__device__ __forceinline__ Where<ST> find_step(const Attention& a, const Plan& p, int step) {
+  const int32_t* pages = a.rows.pages + (uint64_t)p.row * a.rows.max_pages;
+  Where<ST> w;
+#pragma unroll
+  for (int t = 0; t < ST; ++t) {
+    const int tile = step * ST + t, there = min(tile, p.tiles - 1);
+    const uint32_t id = (uint32_t)scalar(pages + (there >> a.pool.tile_shift));
+    w.ok[t] = id < a.pool.n_pages && tile < p.tiles;
+    const uint32_t page = id < a.pool.n_pages ? id : 0u;
+    w.at[t] = (uint64_t)page * a.pool.page_bytes +
+              (uint32_t)((there & ((1 << a.pool.tile_shift) - 1)) * (DJ * kUnit));
+    w.ks[t] = scalar(a.pool.k_scales + page);
+    w.vs[t] = scalar(a.pool.v_scales + page);
+  }
+  return w;
+}
+
+template <int DJ, int ST>
+__device__ __forceinline__ void load_tiles(const uint8_t* codes, const Where<ST>& w, int lane,
+                                           u32x4 (&x)[ST][DJ]) {
+#pragma unroll
+  for (int t = 0; t < ST; ++t)
+#pragma unroll
+    for (int j = 0; j < DJ; ++j) x[t][j] = *(const u32x4*)(codes + w.at[t] + j * kUnit + lane * 16);
+}
+
+// The largest of the four lanes that hold a query.
+__device__ __forceinline__ float query_max(float x) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, x);
+  const auto y = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  const uint32_t z = __builtin_bit_cast(uint32_t, fmaxf(__builtin_bit_cast(float, (uint32_t)y[0]),
+                                                        __builtin_bit_cast(float, (uint32_t)y[1])));
+  const auto w = __builtin_amdgcn_permlane32_swap(z, z, false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)w[0]), __builtin_bit_cast(float, (uint32_t)w[1]));
+}
+
+// Sums over lanes l, l ^ 16 of x (for even lane / 16) and of y (for odd).
+__device__ __forceinline__ float pair_sum16(float x, float y) {
+  const auto z = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x),
+                                                  __builtin_bit_cast(uint32_t, y), false, false);
+  return __builtin_bit_cast(float, (uint32_t)z[0]) + __builtin_bit_cast(float, (uint32_t)z[1]);
+}
+
+// Sums over lanes l, l ^ 32 of x (for the lower half) and of y (for the upper).
+__device__ __forceinline__ float pair_sum32(float x, float y) {
+  const auto z = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x),
+                                                  __builtin_bit_cast(uint32_t, y), false, false);
+  return __builtin_bit_cast(float, (uint32_t)z[0]) + __builtin_bit_cast(float, (uint32_t)z[1]);
+}
+
+// A step of a wave is 16 ST tokens against its 16 MT query rows.
 //   S^T = K Q^T: the lane gets the scores of query lane % 16 with tokens
 //   4 (lane / 16) + r of each tile.  These are, without any exchange, the
 //   P^T operand of O^T = V^T P^T when the matrix instruction's index k is
 //   taken as (tile of the pair, r) within lane / 16, and the layout of a value
 //   tile gives V^T in the same order.
-// P times the page's scale goes in as two 16-bit terms (bf16, so that any
-// scale fits): the products keep 16 bits of P.
-template <int DJ, bool F16, int MT, bool MASKED>
-__device__ __forceinline__ void attend_step(const Attention& a, const Plan& p, int step, int lane,
-                                            const u32x4 (&q)[MT][DJ][2], const int (&seen)[MT],
-                                            Tiles<DJ>& x, float* mass_row, State<DJ, MT>& st) {
-  const int g = lane / 16;
-  f32x4 s[MT][kStepTiles];
+template <int DJ, bool F16, int MT, int ST>
+__device__ __forceinline__ void scores(const u32x4 (&k)[ST][DJ], const u32x4 (&q)[MT][DJ][2],
+                                       f32x4 (&s)[MT][ST]) {
 #pragma unroll
-  for (int t = 0; t < kStepTiles; ++t) {
+  for (int t = 0; t < ST; ++t) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) s[mt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < DJ; ++j)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const u32x4 kk = widen8<F16>(x.k[t][j][2 * half], x.k[t][j][2 * half + 1]);
+        const u32x4 kk = widen8<F16>(k[t][j][2 * half], k[t][j][2 * half + 1]);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) s[mt][t] = mfma<F16>(kk, q[mt][j][half], s[mt][t]);
       }
   }
+}
 
-  const int at = step * kStep + 4 * g;  // the lane's first token
-  u32x4 hi[MT][2], lo[MT][2], sees[MT][2];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    float top = -INFINITY;
-#pragma unroll
-    for (int t = 0; t < kStepTiles; ++t) {
-      const float c = x.ks[t] * a.scale;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float y = s[mt][t][r] * c;
-        if constexpr (MASKED)
-          if (!x.ok[t] || at + 16 * t + r >= seen[mt]) y = -INFINITY;
-        s[mt][t][r] = y;
-        top = fmaxf(top, y);
-      }
-    }
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const float m = fmaxf(st.m[mt], top);
-    const float base = m == -INFINITY ? 0.f : m;
-    const float keep = exp2_fast(st.m[mt] - base);
-    st.m[mt] = m;
-    float mass[kStepTiles], sum = 0.f;
-#pragma unroll
-    for (int t = 0; t < kStepTiles; ++t) {
-      float y[4], z[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        y[r] = exp2_fast(s[mt][t][r] - base);
-        z[r] = y[r] * x.vs[t];
-        if constexpr (MASKED) {
-          const bool on = x.ok[t] && at + 16 * t + r < seen[mt];
-          z[r] = on ? z[r] : 0.f;
-        }
-      }
-      mass[t] = (y[0] + y[1]) + (y[2] + y[3]);
-      const uint32_t h0 = pack_bf16(z[0], z[1]), h1 = pack_bf16(z[2], z[3]);
-      hi[mt][t / 2][t % 2 * 2] = h0;
-      hi[mt][t / 2][t % 2 * 2 + 1] = h1;
-      lo[mt][t / 2][t % 2 * 2] = pack_bf16(z[0] - bf16_low(h0), z[1] - bf16_high(h0));
-      lo[mt][t / 2][t % 2 * 2 + 1] = pack_bf16(z[2] - bf16_low(h1), z[3] - bf16_high(h1));
-      if constexpr (MASKED) {
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const int n = x.ok[t] ? seen[mt] - (at + 16 * t + 2 * w) : 0;
-          sees[mt][t / 2][t % 2 * 2 + w] = n <= 0 ? 0u : n == 1 ? 0x3F80u : 0x3F803F80u;
-        }
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < kStepTiles; ++t) {
-      mass[t] += __shfl_xor(mass[t], 16);
-      mass[t] += __shfl_xor(mass[t], 32);
-      sum += mass[t];
-    }
-    st.l[mt] = st.l[mt] * keep + sum;
-#pragma unroll
-    for (int i = 0; i < 4 * DJ; ++i) st.o[mt][i] *= keep;
-    if (mass_row) {
-      const float mine = g == 0 ? mass[0] : g == 1 ? mass[1] : g == 2 ? mass[2] : mass[3];
-      const int tile = step * kStepTiles + g, m_local = mt * 16 + lane % 16;
-      if (tile < p.tiles && m_local < a.unit_rows)
-        mass_row[(uint64_t)m_local * a.cap_tiles + tile] = base + log2_fast(mine);
-    }
-  }
+// P times the page's scale goes into the second product as two 16-bit terms
+// (bf16, so that any scale fits): the products keep 16 bits of P.
+template <int MT, int ST>
+struct Probs {
+  u32x4 hi[MT][ST / 2], lo[MT][ST / 2];
+};
 
+// Takes out of a step what its queries may not see: scores become minus
+// infinity, value bytes that no query sees (they may hold anything) 0.  A NaN
+// value that only some of the queries see is 0 to the products, and those that
+// see it get NaN here.
+template <int DJ, int MT, int ST>
+__device__ __forceinline__ void mask_step(const Plan& p, int step, int lane, const int (&seen)[MT],
+                                          Where<ST>& w, f32x4 (&s)[MT][ST], u32x4 (&v)[ST][DJ],
+                                          State<DJ, MT>& st) {
+  const int at = step * (kTile * ST) + 4 * (lane / 16);  // the lane's first token
 #pragma unroll
-  for (int pair = 0; pair < 2; ++pair)
+  for (int t = 0; t < ST; ++t) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (!w.ok[t] || at + 16 * t + r >= seen[mt]) s[mt][t][r] = -INFINITY;
+    if (!w.ok[t]) w.vs[t] = 0.f;
+    const uint32_t inside = w.ok[t] ? byte_mask(p.end - (at + 16 * t)) : 0u;
+    uint32_t any = 0;
 #pragma unroll
     for (int h = 0; h < DJ; ++h)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t v0 = x.v[2 * pair][h][c], v1 = x.v[2 * pair + 1][h][c];
-        if constexpr (MASKED) {
-          // bytes past what any query sees may hold anything
-          v0 &= byte_mask(p.end - (at + 32 * pair));
-          v1 &= byte_mask(p.end - (at + 32 * pair + 16));
-          // a NaN that only some of the queries see: those get NaN, the
-          // products get 0 in its place
-          const uint32_t n0 = nan_codes(v0), n1 = nan_codes(v1);
-          if (__ballot((n0 | n1) != 0)) {
-            const uint32_t b0 = (n0 >> 7) * 255u, b1 = (n1 >> 7) * 255u;
-            const u32x4 is = widen8<false>(b0 & 0x38383838u, b1 & 0x38383838u);  // 1.0 where NaN
-            v0 &= ~b0;
-            v1 &= ~b1;
+        v[t][h][c] &= inside;
+        any |= nan_codes(v[t][h][c]);
+      }
+    if (__ballot(any != 0)) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              const f32x4 found = mfma<false>(is, sees[mt][pair], f32x4{0.f, 0.f, 0.f, 0.f});
+      for (int h = 0; h < DJ; ++h)
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
-                if (found[r] > 0.f) st.o[mt][h * 4 + c][r] = NAN;
-            }
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t nan = (nan_codes(v[t][h][c]) >> 7) * 255u;
+          v[t][h][c] &= ~nan;
+          const u32x4 is = widen8<false>(nan & 0x38383838u, 0u);  // 1 where NaN
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const int n = seen[mt] - (at + 16 * t);
+            const u32x4 sees = {n <= 0 ? 0u : n == 1 ? 0x3F80u : 0x3F803F80u,
+                                n <= 2 ? 0u : n == 3 ? 0x3F80u : 0x3F803F80u, 0u, 0u};
+            const f32x4 found = mfma<false>(is, sees, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (found[r] > 0.f) st.o[mt][h * 4 + c][r] = NAN;
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        const u32x4 vv = widen8<false>(v0, v1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+template <int DJ, int MT, int ST>
+__device__ __forceinline__ void softmax(const Attention& a, const Plan& p, int step, int lane,
+                                        const Where<ST>& w, f32x4 (&s)[MT][ST], float* mass_row,
+                                        State<DJ, MT>& st, Probs<MT, ST>& out) {
+  const int g = lane / 16;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < ST; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) top = fmaxf(top, s[mt][t][r]);
+    if (__ballot(top > st.m[mt])) {  // a new maximum for some query, which is rare after some steps
+      const float m = fmaxf(st.m[mt], query_max(top));
+      const float keep = exp2_fast(st.m[mt] - (m == -INFINITY ? 0.f : m));
+      st.m[mt] = m;
+      st.l[mt] *= keep;
+#pragma unroll
+      for (int i = 0; i < 4 * DJ; ++i) st.o[mt][i] *= keep;
+    }
+    const float base = st.m[mt] == -INFINITY ? 0.f : st.m[mt];
+    float mass[ST];
+#pragma unroll
+    for (int t = 0; t < ST; ++t) {
+      float y[4], z[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        y[r] = exp2_fast(s[mt][t][r] - base);
+        z[r] = y[r] * w.vs[t];
+      }
+      mass[t] = (y[0] + y[1]) + (y[2] + y[3]);
+      const uint32_t h0 = pack_bf16(z[0], z[1]), h1 = pack_bf16(z[2], z[3]);
+      out.hi[mt][t / 2][t % 2 * 2] = h0;
+      out.hi[mt][t / 2][t % 2 * 2 + 1] = h1;
+      out.lo[mt][t / 2][t % 2 * 2] = pack_bf16(z[0] - bf16_low(h0), z[1] - bf16_high(h0));
+      out.lo[mt][t / 2][t % 2 * 2 + 1] = pack_bf16(z[2] - bf16_low(h1), z[3] - bf16_high(h1));
+    }
+    // lane / 16 = t gets the sum of tile t (with two tiles, of tile t % 2)
+    float mine = pair_sum16(mass[0], mass[1]);
+    if constexpr (ST == 4)
+      mine = pair_sum32(mine, pair_sum16(mass[2], mass[3]));
+    else
+      mine = pair_sum32(mine, mine);
+    const bool sole = ST == 4 || g < ST;
+    if (sole) st.l[mt] += mine;
+    if (mass_row) {
+      const int tile = step * ST + g, m_local = mt * 16 + lane % 16;
+      if (sole && tile < p.tiles && m_local < a.unit_rows)
+        mass_row[(uint64_t)m_local * a.cap_tiles + tile] = base + log2_fast(mine);
+    }
+  }
+}
+
+template <int DJ, int MT, int ST>
+__device__ __forceinline__ void gather_values(const u32x4 (&v)[ST][DJ], const Probs<MT, ST>& pr,
+                                              State<DJ, MT>& st) {
+#pragma unroll
+  for (int pair = 0; pair < ST / 2; ++pair)
+#pragma unroll
+    for (int h = 0; h < DJ; ++h)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const u32x4 vv = widen8<false>(v[2 * pair][h][c], v[2 * pair + 1][h][c]);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          st.o[mt][h * 4 + c] = mfma<false>(vv, hi[mt][pair], st.o[mt][h * 4 + c]);
-          st.o[mt][h * 4 + c] = mfma<false>(vv, lo[mt][pair], st.o[mt][h * 4 + c]);
+          st.o[mt][h * 4 + c] = mfma<false>(vv, pr.hi[mt][pair], st.o[mt][h * 4 + c]);
+          st.o[mt][h * 4 + c] = mfma<false>(vv, pr.lo[mt][pair], st.o[mt][h * 4 + c]);
         }
       }
 }
@@ -620,8 +674,9 @@ __device__ __forceinline__ float log_total(float m, float l) {
 // join at the end.  With one split and one unit a row the result is written
 // here, else it is left in the workspace for the combining kernel.
 template <int DJ, bool F16, int MT>
-__global__ __launch_bounds__(kThreads) void attention_kernel(Attention a) {
+__global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kernel(Attention a) {
   constexpr int D = 64 * DJ;
+  constexpr int ST = step_tiles(DJ, MT);
   constexpr int kPitch = 64 + 4;  // floats of a query row of 64 dims in LDS
   __shared__ __attribute__((aligned(16))) float s_o[kWaves][16][kPitch];
   __shared__ f32x2 s_ml[kWaves][MT * 16];
@@ -629,7 +684,7 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(Attention a) {
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const uint32_t unit = blockIdx.x % a.n_units, split = blockIdx.x / a.n_units;
   const bool direct = a.n_splits == 1 && a.m_groups == 1;
-  const Plan p = plan_unit<MT>(a, unit);
+  const Plan p = plan_unit<DJ, MT>(a, unit);
   const int first = (int)split * p.split_steps;
   const int last = min(first + p.split_steps, p.steps);
   if (first >= last && !direct) return;
@@ -664,13 +719,45 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(Attention a) {
   }
   float* mass_row = a.w_out ? a.ws_mass + (uint64_t)unit * a.unit_rows * a.cap_tiles : nullptr;
 
-  for (int step = first + wave; step < last; step += kWaves) {
-    Tiles<DJ> x;
-    load_step<DJ>(a, p, step, lane, x);
-    if (step * kStep + kStep <= p.full && x.ok[0] && x.ok[1] && x.ok[2] && x.ok[3])
-      attend_step<DJ, F16, MT, false>(a, p, step, lane, q, seen, x, mass_row, st);
-    else
-      attend_step<DJ, F16, MT, true>(a, p, step, lane, q, seen, x, mass_row, st);
+  // While a step is computed the next one's tiles are on their way: its keys
+  // take the registers of this one's as soon as the scores are done, its
+  // values once they have been summed.
+  int step = first + wave;
+  if (step < last) {
+    u32x4 k[ST][DJ], v[ST][DJ];
+    Where<ST> here = find_step<DJ, ST>(a, p, step);
+    load_tiles<DJ, ST>(a.pool.k_codes, here, lane, k);
+    load_tiles<DJ, ST>(a.pool.v_codes, here, lane, v);
+    while (true) {
+      const int next_step = step + kWaves;
+      const bool more = next_step < last;
+      Where<ST> next = find_step<DJ, ST>(a, p, more ? next_step : step);
+      f32x4 s[MT][ST];
+      scores<DJ, F16, MT, ST>(k, q, s);
+      if (more) load_tiles<DJ, ST>(a.pool.k_codes, next, lane, k);
+      bool plain = (step + 1) * (kTile * ST) <= p.full;
+#pragma unroll
+      for (int t = 0; t < ST; ++t) plain = plain && here.ok[t];
+#pragma unroll
+      for (int t = 0; t < ST; ++t) {
+        const float c = here.ks[t] * a.scale;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) s[mt][t] *= c;
+      }
+      if (!plain) mask_step<DJ, MT, ST>(p, step, lane, seen, here, s, v, st);
+      Probs<MT, ST> pr;
+      softmax<DJ, MT, ST>(a, p, step, lane, here, s, mass_row, st, pr);
+      gather_values<DJ, MT, ST>(v, pr, st);
+      if (!more) break;
+      load_tiles<DJ, ST>(a.pool.v_codes, next, lane, v);
+      here = next;
+      step = next_step;
+    }
+  }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    st.l[mt] = pair_sum16(st.l[mt], st.l[mt]);
+    st.l[mt] = pair_sum32(st.l[mt], st.l[mt]);
   }
 
   if (lane < 16) {
@@ -759,7 +846,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
   if (blockIdx.x < out_blocks) {
     const uint32_t unit = blockIdx.x / a.unit_rows;
     const int m_local = (int)(blockIdx.x % a.unit_rows);
-    const Plan p = plan_unit<MT>(a, unit);
+    const Plan p = plan_unit<DJ, MT>(a, unit);
     const int m = p.m0 + m_local;
     if (m >= a.m_rows) return;
     const bool any = seen_by(a, p, m) > 0;
@@ -806,7 +893,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
   float w = 0.f;
   for (int g = 0; g < a.m_groups; ++g) {
     const uint32_t unit = row * a.m_groups + g;
-    const Plan p = plan_unit<MT>(a, unit);
+    const Plan p = plan_unit<DJ, MT>(a, unit);
     __syncthreads();
     for (int m = wave; m < a.unit_rows; m += kWaves) {
       f32x2 ml = {-INFINITY, 0.f};
@@ -1082,9 +1169,9 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
   const uint64_t units = n_rows * s->m_groups;
   if (units > kMaxGrid / 64) return false;
   s->n_units = (uint32_t)units;
-  // four workgroups a compute unit, and a step for each wave of a split
-  const uint64_t steps = ((uint64_t)max_pages * page_tokens + kStep - 1) / kStep;
-  uint64_t splits = units ? (4ull * cus + units - 1) / units : 1;
+  // two workgroups a compute unit, which is what fits, and a step for each wave of a split
+  const uint64_t steps = (uint64_t)(s->cap_tiles + step_tiles((int)head_dim / 64, s->mt) - 1) / step_tiles((int)head_dim / 64, s->mt);
+  uint64_t splits = units ? (2ull * cus + units - 1) / units : 1;
   splits = std::min<uint64_t>(splits, (steps + kWaves - 1) / kWaves);
   s->n_splits = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(splits, kMaxSplits));
   const bool direct = s->n_splits == 1 && s->m_groups <= 1;
@@ -1212,6 +1299,7 @@ int ibp_kv_attention(const ibp_kv_cache* cache, const ibp_kv_table* table, uint3
   Attention a{};
   a.pool = make_pool(cache);
   a.rows = make_rows(table, cache->page_tokens, n_new, counts);
+  if (cache->n_pages == 0) a.rows.capacity = 0;  // holes only: nothing to see, and no page to read
   if (n_new) {
     a.q = make_strided(q);
     a.out = make_strided(out);
