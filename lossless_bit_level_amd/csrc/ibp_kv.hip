@@ -15,11 +15,14 @@ constexpr int kWave = 64;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kTile = 16;       // tokens of a tile
-// Tiles that a wave takes at a time: 64 tokens, 32 of wide heads, whose tiles
-// and accumulators take twice the registers.
-constexpr int step_tiles(int dj, int mt) { return dj * mt <= 2 ? 4 : 2; }
+// Tiles that a wave takes at a time: 64 tokens of narrow heads, 32 of wider
+// ones, whose tiles and accumulators take more registers (64 tokens of 128
+// dims measured the same at 40 registers more).
+constexpr int step_tiles(int dj, int mt) { return dj * mt <= 1 ? 4 : 2; }
+// The most groups of 16 query rows that a unit takes.
+constexpr int most_query_tiles(int dj) { return dj <= 2 ? 4 : 2; }
 constexpr int kUnit = 1024;     // bytes of a tile that one wide load of a wave takes
-constexpr int kMaxSplits = 64;
+constexpr int kMaxParts = 512;
 constexpr int kExpMin = -126, kExpMax = 119;  // exponents of a page's scale
 constexpr float kE4m3Max = 448.f;
 
@@ -149,6 +152,64 @@ __device__ __forceinline__ uint32_t byte_mask(int n) {  // the first n bytes of 
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
+// ---------------------------------------------------------------- waves ----
+
+template <int CTRL>
+__device__ __forceinline__ float row_rotate(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
+}
+
+// The two values that lanes l and l ^ 16 (l ^ 32) hold, the same in both.
+__device__ __forceinline__ f32x2 both16(float x) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, x);
+  const auto y = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  return f32x2{__builtin_bit_cast(float, (uint32_t)y[0]), __builtin_bit_cast(float, (uint32_t)y[1])};
+}
+__device__ __forceinline__ f32x2 both32(float x) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, x);
+  const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return f32x2{__builtin_bit_cast(float, (uint32_t)y[0]), __builtin_bit_cast(float, (uint32_t)y[1])};
+}
+
+// Maximum and sum over the wave, in every lane: rotations within 16 lanes, then
+// swaps of rows.
+__device__ __forceinline__ float wave_max(float x) {
+  x = fmaxf(x, row_rotate<0x121>(x));
+  x = fmaxf(x, row_rotate<0x122>(x));
+  x = fmaxf(x, row_rotate<0x124>(x));
+  x = fmaxf(x, row_rotate<0x128>(x));
+  f32x2 y = both16(x);
+  y = both32(fmaxf(y[0], y[1]));
+  return fmaxf(y[0], y[1]);
+}
+
+__device__ __forceinline__ float wave_sum(float x) {
+  x += row_rotate<0x121>(x);
+  x += row_rotate<0x122>(x);
+  x += row_rotate<0x124>(x);
+  x += row_rotate<0x128>(x);
+  f32x2 y = both16(x);
+  y = both32(y[0] + y[1]);
+  return y[0] + y[1];
+}
+
+// n plus the bits of `mask` that belong to lower lanes.
+__device__ __forceinline__ uint32_t lanes_below(uint64_t mask, uint32_t n) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, n));
+}
+
+// Sum over the lanes up to this one: shifts within 16 lanes, then the last lane
+// of a row to the rows after it.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xF, 0xF, false);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xF, 0xF, false);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xF, 0xF, false);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xF, 0xF, false);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xA, 0xF, false);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xC, 0xF, false);
+  return x;
+}
+
 // ---------------------------------------------------------------- rows ----
 
 struct Pool {
@@ -198,12 +259,6 @@ __device__ __forceinline__ void load8(const uint16_t* p, bool wide, float* x) {
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = to_float<F16>(h[i]);
-}
-
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int s = 32; s; s >>= 1) x = fmaxf(x, __shfl_xor(x, s));
-  return x;
 }
 
 // One wave per 16-token tile of a page that receives new tokens; the waves of
@@ -378,9 +433,10 @@ struct Attention {
   Strided q, out;
   const float* w_in;
   float* w_out;
-  float* ws_o;     // [unit][split][unit_rows][D] sums of p v
-  f32x2* ws_ml;    // [unit][split][unit_rows] maximum and sum
+  float* ws_o;     // [part][unit_rows][D] sums of p v
+  f32x2* ws_ml;    // [part][unit_rows] maximum and sum
   float* ws_mass;  // [unit][unit_rows][cap_tiles] log2 of a tile's share of exp2(s)
+  int32_t* ws_of;  // [unit][2] first part and number of parts, of units that have a token
   float scale;     // scale * log2(e)
   int32_t group;
   int32_t m_rows;      // group * n_new: query rows of a key/value head
@@ -388,12 +444,22 @@ struct Attention {
   int32_t unit_rows;   // query rows of a unit
   int32_t cap_tiles;
   uint32_t n_units;
-  uint32_t n_splits;
+  uint32_t n_rows;
+  uint32_t n_parts;  // workgroups that the units are spread over; n_units: one each
   uint32_t weight_blocks;  // of a row, in the combining kernel
 };
 
-// What a unit (some query rows of a head) reads: the tiles up to what its
-// last query sees, cut into steps, cut into splits.
+// Which part of which unit a workgroup takes.
+struct Part {
+  uint32_t row;
+  int group;       // of the head's query rows
+  int index, of;   // the unit is cut into `of` parts
+  uint32_t first;  // part 0 of the unit; the next ones are m_groups apart
+  bool idle;
+};
+
+// A unit (some query rows of a head) reads the tiles up to what its last query
+// sees, in steps.
 struct Plan {
   uint32_t row, seq, head;
   int m0;      // first query row
@@ -401,16 +467,103 @@ struct Plan {
   int count;
   int end;     // tokens that some query sees
   int full;    // tokens that every query with any sees
-  int tiles, steps, split_steps, splits;
+  int tiles, steps;
+  int part_steps, parts;
 };
 
-template <int DJ, int MT>
-__device__ __forceinline__ Plan plan_unit(const Attention& a, uint32_t unit) {
+constexpr int kRowsPerLane = 4;  // of the rows that share out the workgroups
+
+// Shares the workgroups out: with C = ceil(all steps / (n_parts - n_units)) a
+// row of s steps gets ceil(s / C) workgroups for each of its units, n_parts at
+// most together.  Long rows get more than short ones, so that no workgroup
+// works long after the others.  Every wave works it out from the lengths.
+//   lane l: rows 4 l .. 4 l + 3, `share` workgroups a unit each, `before` those
+//   of the rows before them.
+template <int ST>
+__device__ __forceinline__ void share_out(const Attention& a, int lane, int (&share)[kRowsPerLane],
+                                          int& before) {
+  int total = 0;
+#pragma unroll
+  for (int i = 0; i < kRowsPerLane; ++i) {
+    const uint32_t row = lane * kRowsPerLane + i;
+    const int len = row < a.n_rows ? row_length(a.rows, row) : 0;
+    share[i] = (int)(((uint32_t)len + kTile * ST - 1) / (kTile * ST));
+    total += share[i];
+  }
+  const uint32_t all = (uint32_t)__builtin_amdgcn_readlane((int)wave_scan((uint32_t)total), kWave - 1) *
+                       (uint32_t)a.m_groups;
+  const uint32_t room = a.n_parts - a.n_units;
+  const uint32_t c = max((all + room - 1) / room, (uint32_t)kWaves);
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < kRowsPerLane; ++i) {
+    share[i] = (int)(((uint32_t)share[i] + c - 1) / c);
+    mine += share[i];
+  }
+  before = (int)wave_scan((uint32_t)mine) - mine;
+}
+
+template <int ST>
+__device__ __forceinline__ Part part_of_workgroup(const Attention& a, uint32_t w, int lane) {
+  Part t;
+  if (a.n_parts == a.n_units) {
+    t.row = w / a.m_groups;
+    t.group = (int)(w % a.m_groups);
+    t.index = 0;
+    t.of = 1;
+    t.first = w;
+    t.idle = false;
+    return t;
+  }
+  int share[kRowsPerLane], before;
+  share_out<ST>(a, lane, share, before);
+  const int x = (int)(w / a.m_groups);
+  t.group = (int)(w % a.m_groups);
+  int row = 0, index = 0, of = 0, first = 0;
+#pragma unroll
+  for (int i = 0; i < kRowsPerLane; ++i) {
+    if (x >= before && x < before + share[i]) {
+      row = lane * kRowsPerLane + i;
+      index = x - before;
+      of = share[i];
+      first = before;
+    }
+    before += share[i];
+  }
+  const uint64_t who = __ballot(of != 0);
+  t.idle = who == 0;
+  const int src = t.idle ? 0 : __builtin_ctzll(who);
+  t.row = (uint32_t)__builtin_amdgcn_readlane(row, src);
+  t.index = __builtin_amdgcn_readlane(index, src);
+  t.of = __builtin_amdgcn_readlane(of, src);
+  t.first = (uint32_t)__builtin_amdgcn_readlane(first, src) * (uint32_t)a.m_groups + t.group;
+  return t;
+}
+
+// The parts of a unit, as its part 0 left them.
+__device__ __forceinline__ Part parts_of_unit(const Attention& a, uint32_t row, int group) {
+  Part t;
+  t.row = row;
+  t.group = group;
+  t.index = 0;
+  t.idle = false;
+  const uint32_t unit = row * (uint32_t)a.m_groups + group;
+  t.first = unit;
+  t.of = 1;
+  if (a.n_parts != a.n_units && row_length(a.rows, row) > 0) {
+    t.first = (uint32_t)a.ws_of[2 * unit];
+    t.of = a.ws_of[2 * unit + 1];
+  }
+  return t;
+}
+
+template <int MT, int ST>
+__device__ __forceinline__ Plan plan_unit(const Attention& a, const Part& t) {
   Plan p;
-  p.row = unit / a.m_groups;
+  p.row = t.row;
   p.seq = p.row / a.rows.heads;
   p.head = p.row % a.rows.heads;
-  p.m0 = (int)(unit % a.m_groups) * (MT * 16);
+  p.m0 = t.group * (MT * 16);
   const int len = row_length(a.rows, p.row);
   p.count = new_count(a.rows, p.seq);
   p.origin = len - p.count;
@@ -419,10 +572,9 @@ __device__ __forceinline__ Plan plan_unit(const Attention& a, uint32_t unit) {
   p.end = t_high >= t_low ? max(p.origin + t_high + 1, 0) : 0;
   p.full = max(p.origin + t_low + 1, 1);
   p.tiles = (p.end + kTile - 1) / kTile;
-  p.steps = (p.tiles + step_tiles(DJ, MT) - 1) / step_tiles(DJ, MT);
-  // a split has a step for each of its waves at least
-  p.split_steps = max((p.steps + (int)a.n_splits - 1) / (int)a.n_splits, kWaves);
-  p.splits = (p.steps + p.split_steps - 1) / p.split_steps;
+  p.steps = (p.tiles + ST - 1) / ST;
+  p.part_steps = t.of > 1 ? (p.steps + t.of - 1) / t.of : max(p.steps, 1);
+  p.parts = p.steps ? (p.steps + p.part_steps - 1) / p.part_steps : 0;
   return p;
 }
 
@@ -478,23 +630,29 @@ __device__ __forceinline__ Where<ST> find_step(const Attention& a, const Plan& p
   return w;
 }
 
-template <int DJ, int ST>
+// Non-temporal where a unit has all of its head's query rows, so that no other
+// workgroup of the call comes back for the tiles: 16 x 32 heads x 4096 tokens
+// take 88.4 us so (6.1 TB/s), 102.7 us with plain loads.
+template <int DJ, int ST, bool ONCE>
 __device__ __forceinline__ void load_tiles(const uint8_t* codes, const Where<ST>& w, int lane,
                                            u32x4 (&x)[ST][DJ]) {
 #pragma unroll
   for (int t = 0; t < ST; ++t)
 #pragma unroll
-    for (int j = 0; j < DJ; ++j) x[t][j] = *(const u32x4*)(codes + w.at[t] + j * kUnit + lane * 16);
+    for (int j = 0; j < DJ; ++j) {
+      const u32x4* p = (const u32x4*)(codes + w.at[t] + j * kUnit + lane * 16);
+      if constexpr (ONCE)
+        x[t][j] = __builtin_nontemporal_load(p);
+      else
+        x[t][j] = *p;
+    }
 }
 
 // The largest of the four lanes that hold a query.
 __device__ __forceinline__ float query_max(float x) {
-  const uint32_t b = __builtin_bit_cast(uint32_t, x);
-  const auto y = __builtin_amdgcn_permlane16_swap(b, b, false, false);
-  const uint32_t z = __builtin_bit_cast(uint32_t, fmaxf(__builtin_bit_cast(float, (uint32_t)y[0]),
-                                                        __builtin_bit_cast(float, (uint32_t)y[1])));
-  const auto w = __builtin_amdgcn_permlane32_swap(z, z, false, false);
-  return fmaxf(__builtin_bit_cast(float, (uint32_t)w[0]), __builtin_bit_cast(float, (uint32_t)w[1]));
+  f32x2 y = both16(x);
+  y = both32(fmaxf(y[0], y[1]));
+  return fmaxf(y[0], y[1]);
 }
 
 // Sums over lanes l, l ^ 16 of x (for even lane / 16) and of y (for odd).
@@ -670,23 +828,58 @@ __device__ __forceinline__ float log_total(float m, float l) {
   return l == 0.f ? INFINITY : (m == -INFINITY ? 0.f : m) + log2_fast(l);
 }
 
-// A workgroup takes one split of one unit; its waves take steps in turn and
-// join at the end.  With one split and one unit a row the result is written
+// The weight that tile `tile` got from a unit's query rows, lse their
+// log_total (+inf for rows that see nothing, whose shares are not written).
+__device__ __forceinline__ float tile_weight(const Attention& a, const float* mass, const float* lse,
+                                             int tile) {
+  float w = 0.f;
+  int m = 0;
+  for (; m + 8 <= a.unit_rows; m += 8) {  // eight loads in flight
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = mass[(uint64_t)(m + i) * a.cap_tiles + tile];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w += lse[m + i] == INFINITY ? 0.f : exp2_fast(x[i] - lse[m + i]);
+  }
+  for (; m < a.unit_rows; ++m)
+    w += lse[m] == INFINITY ? 0.f : exp2_fast(mass[(uint64_t)m * a.cap_tiles + tile] - lse[m]);
+  return w;
+}
+
+// Adds up the tiles of a page, which neighbouring lanes hold, and writes it.
+__device__ __forceinline__ void write_weight(const Attention& a, uint32_t row, int tile, float w) {
+  const int shift = (int)a.pool.tile_shift;
+  if (shift >= 1) w += __shfl_xor(w, 1);
+  if (shift == 2) w += __shfl_xor(w, 2);
+  if (tile >= a.cap_tiles || (tile & ((1 << shift) - 1))) return;
+  const uint64_t at = (uint64_t)row * a.rows.max_pages + (uint32_t)(tile >> shift);
+  a.w_out[at] = a.w_in[at] + w;
+}
+
+// A workgroup takes one part of one unit; its waves take steps in turn and
+// join at the end.  With one part and one unit a row the result is written
 // here, else it is left in the workspace for the combining kernel.
 template <int DJ, bool F16, int MT>
 __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kernel(Attention a) {
   constexpr int D = 64 * DJ;
   constexpr int ST = step_tiles(DJ, MT);
+  constexpr bool kOnce = MT < most_query_tiles(DJ);
   constexpr int kPitch = 64 + 4;  // floats of a query row of 64 dims in LDS
   __shared__ __attribute__((aligned(16))) float s_o[kWaves][16][kPitch];
   __shared__ f32x2 s_ml[kWaves][MT * 16];
   __shared__ float s_lse[MT * 16];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const uint32_t unit = blockIdx.x % a.n_units, split = blockIdx.x / a.n_units;
-  const bool direct = a.n_splits == 1 && a.m_groups == 1;
-  const Plan p = plan_unit<DJ, MT>(a, unit);
-  const int first = (int)split * p.split_steps;
-  const int last = min(first + p.split_steps, p.steps);
+  const bool direct = a.n_parts == a.n_units && a.m_groups == 1;
+  const Part part = part_of_workgroup<ST>(a, blockIdx.x, lane);
+  if (part.idle) return;
+  const uint32_t unit = part.row * (uint32_t)a.m_groups + part.group;
+  const Plan p = plan_unit<MT, ST>(a, part);
+  const int first = part.index * p.part_steps;
+  const int last = min(first + p.part_steps, p.steps);
+  if (part.index == 0 && threadIdx.x == 0 && a.n_parts != a.n_units) {
+    a.ws_of[2 * unit] = (int32_t)part.first;
+    a.ws_of[2 * unit + 1] = part.of;
+  }
   if (first >= last && !direct) return;
 
   u32x4 q[MT][DJ][2];
@@ -726,15 +919,15 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
   if (step < last) {
     u32x4 k[ST][DJ], v[ST][DJ];
     Where<ST> here = find_step<DJ, ST>(a, p, step);
-    load_tiles<DJ, ST>(a.pool.k_codes, here, lane, k);
-    load_tiles<DJ, ST>(a.pool.v_codes, here, lane, v);
+    load_tiles<DJ, ST, kOnce>(a.pool.k_codes, here, lane, k);
+    load_tiles<DJ, ST, kOnce>(a.pool.v_codes, here, lane, v);
     while (true) {
       const int next_step = step + kWaves;
       const bool more = next_step < last;
       Where<ST> next = find_step<DJ, ST>(a, p, more ? next_step : step);
       f32x4 s[MT][ST];
       scores<DJ, F16, MT, ST>(k, q, s);
-      if (more) load_tiles<DJ, ST>(a.pool.k_codes, next, lane, k);
+      if (more) load_tiles<DJ, ST, kOnce>(a.pool.k_codes, next, lane, k);
       bool plain = (step + 1) * (kTile * ST) <= p.full;
 #pragma unroll
       for (int t = 0; t < ST; ++t) plain = plain && here.ok[t];
@@ -749,7 +942,7 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
       softmax<DJ, MT, ST>(a, p, step, lane, here, s, mass_row, st, pr);
       gather_values<DJ, MT, ST>(v, pr, st);
       if (!more) break;
-      load_tiles<DJ, ST>(a.pool.v_codes, next, lane, v);
+      load_tiles<DJ, ST, kOnce>(a.pool.v_codes, next, lane, v);
       here = next;
       step = next_step;
     }
@@ -778,15 +971,15 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
       f[w] = exp2_fast(s_ml[w][m_local][0] - base);
       total += s_ml[w][m_local][1] * f[w];
     }
-    const uint64_t part = ((uint64_t)unit * a.n_splits + split) * a.unit_rows + m_local;
+    const uint64_t slot = (uint64_t)blockIdx.x * a.unit_rows + m_local;
     const bool here = m_local < a.unit_rows && m < a.m_rows;
     const float share = total == 0.f ? 0.f : 1.f / total;
     const bool any = seen_by(a, p, m) > 0;
     if (d4 == 0) {
       if (direct)
-        s_lse[m_local] = log_total(top, total);
+        s_lse[m_local] = any ? log_total(top, total) : INFINITY;
       else if (here)
-        a.ws_ml[part] = f32x2{top, total};
+        a.ws_ml[slot] = f32x2{top, total};
     }
 #pragma unroll
     for (int h = 0; h < DJ; ++h) {
@@ -812,61 +1005,74 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
           for (int r = 0; r < 4; ++r) dst[r] = y[r];
         }
       } else {
-        *(f32x4*)(a.ws_o + part * D + d) = o;
+        *(f32x4*)(a.ws_o + slot * D + d) = o;
       }
     }
   }
   if (!direct || !a.w_out) return;
   __syncthreads();
-  const uint64_t w_at = (uint64_t)p.row * a.rows.max_pages;
-  for (uint32_t page = threadIdx.x; page < a.rows.max_pages; page += kThreads) {
-    float w = 0.f;
-    const int t0 = (int)(page << a.pool.tile_shift);
-    const int t1 = min(t0 + (1 << a.pool.tile_shift), p.tiles);
-    for (int m = 0; m < a.unit_rows; ++m) {
-      if (seen_by(a, p, p.m0 + m) == 0) continue;
-      for (int t = t0; t < t1; ++t)
-        w += exp2_fast(mass_row[(uint64_t)m * a.cap_tiles + t] - s_lse[m]);
-    }
-    a.w_out[w_at + page] = a.w_in[w_at + page] + w;
+  for (int base = 0; base < a.cap_tiles; base += kThreads) {  // whole waves: lanes add to each other
+    const int tile = base + (int)threadIdx.x;
+    write_weight(a, p.row, tile, tile < p.tiles ? tile_weight(a, mass_row, s_lse, tile) : 0.f);
   }
 }
 
-// Joins the splits.  Workgroups below n_units * unit_rows take one query row
-// each; the others take 256 pages of a row each and sum their weights.
+// Maximum and sum of a query row over the parts of its unit (up to kMaxParts),
+// and each part's factor, in LDS, where asked for.
+__device__ __forceinline__ float join_parts(const Attention& a, const Part& t, int parts, int m_local,
+                                            int lane, float* factors) {
+  f32x2 ml[kMaxParts / kWave];
+  float top = -INFINITY, total = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxParts / kWave; ++i) {
+    ml[i] = f32x2{-INFINITY, 0.f};
+    const int n = i * kWave + lane;
+    if (n < parts) ml[i] = a.ws_ml[((uint64_t)t.first + (uint64_t)n * a.m_groups) * a.unit_rows + m_local];
+    top = fmaxf(top, ml[i][0]);
+  }
+  top = wave_max(top);
+#pragma unroll
+  for (int i = 0; i < kMaxParts / kWave; ++i) {
+    ml[i][0] = exp2_fast(ml[i][0] - (top == -INFINITY ? 0.f : top));
+    total += ml[i][0] * ml[i][1];
+  }
+  total = wave_sum(total);
+  if (factors) {
+#pragma unroll
+    for (int i = 0; i < kMaxParts / kWave; ++i)
+      if (i * kWave < parts) factors[i * kWave + lane] = total == 0.f ? 0.f : ml[i][0] / total;
+  }
+  return log_total(top, total);
+}
+
+// Joins the parts.  Workgroups below n_units * unit_rows take one query row
+// each; the others take 256 tiles of a row each and sum their weights.
 template <int DJ, bool F16, int MT>
 __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
   constexpr int D = 64 * DJ;
+  constexpr int ST = step_tiles(DJ, MT);
   constexpr int kVec = D / 4;                 // threads of a row of the output
-  constexpr int kGroups = kThreads / kVec;    // splits summed at a time
+  constexpr int kGroups = kThreads / kVec;    // parts summed at a time
   __shared__ __attribute__((aligned(16))) f32x4 s_sum[kGroups][kVec];
-  __shared__ float s_f[kThreads];
+  __shared__ float s_f[kMaxParts];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const uint32_t out_blocks = a.n_units * (uint32_t)a.unit_rows;
   if (blockIdx.x < out_blocks) {
     const uint32_t unit = blockIdx.x / a.unit_rows;
     const int m_local = (int)(blockIdx.x % a.unit_rows);
-    const Plan p = plan_unit<DJ, MT>(a, unit);
+    const Part t = parts_of_unit(a, unit / a.m_groups, (int)(unit % a.m_groups));
+    const Plan p = plan_unit<MT, ST>(a, t);
     const int m = p.m0 + m_local;
     if (m >= a.m_rows) return;
-    const bool any = seen_by(a, p, m) > 0;
-    const int splits = any ? p.splits : 0;
-    // kMaxSplits is a wave's lanes
-    f32x2 ml = {-INFINITY, 0.f};
-    if (lane < splits) ml = a.ws_ml[((uint64_t)unit * a.n_splits + lane) * a.unit_rows + m_local];
-    const float top = wave_max(ml[0]);
-    const float base = top == -INFINITY ? 0.f : top;
-    const float f = exp2_fast(ml[0] - base);
-    float total = ml[1] * f;
-#pragma unroll
-    for (int s = 32; s; s >>= 1) total += __shfl_xor(total, s);
-    if (wave == 0) s_f[lane] = total == 0.f ? 0.f : f / total;
+    const int parts = seen_by(a, p, m) > 0 ? p.parts : 0;
+    if (wave == 0) (void)join_parts(a, t, parts, m_local, lane, s_f);
     __syncthreads();
     const int d4 = threadIdx.x % kVec, group = threadIdx.x / kVec;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
     if (group < kGroups) {
-      for (int s = group; s < splits; s += kGroups)
-        o += *(const f32x4*)(a.ws_o + (((uint64_t)unit * a.n_splits + s) * a.unit_rows + m_local) * D + 4 * d4) * s_f[s];
+#pragma unroll 4
+      for (int n = group; n < parts; n += kGroups)
+        o += *(const f32x4*)(a.ws_o + (((uint64_t)t.first + (uint64_t)n * a.m_groups) * a.unit_rows + m_local) * D + 4 * d4) * s_f[n];
       s_sum[group][d4] = o;
     }
     __syncthreads();
@@ -888,36 +1094,21 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
 
   const uint32_t b = blockIdx.x - out_blocks;
   const uint32_t row = b / a.weight_blocks;
-  const uint32_t page = b % a.weight_blocks * kThreads + threadIdx.x;
-  const int t0 = (int)(page << a.pool.tile_shift);
+  const int tile = (int)(b % a.weight_blocks * kThreads + threadIdx.x);
   float w = 0.f;
   for (int g = 0; g < a.m_groups; ++g) {
-    const uint32_t unit = row * a.m_groups + g;
-    const Plan p = plan_unit<DJ, MT>(a, unit);
+    const Part t = parts_of_unit(a, row, g);
+    const Plan p = plan_unit<MT, ST>(a, t);
     __syncthreads();
     for (int m = wave; m < a.unit_rows; m += kWaves) {
-      f32x2 ml = {-INFINITY, 0.f};
-      if (lane < p.splits && seen_by(a, p, p.m0 + m) > 0)
-        ml = a.ws_ml[((uint64_t)unit * a.n_splits + lane) * a.unit_rows + m];
-      const float top = wave_max(ml[0]);
-      float total = ml[1] * exp2_fast(ml[0] - (top == -INFINITY ? 0.f : top));
-#pragma unroll
-      for (int s = 32; s; s >>= 1) total += __shfl_xor(total, s);
-      if (lane == 0) s_f[m] = log_total(top, total);
+      const float lse = join_parts(a, t, seen_by(a, p, p.m0 + m) > 0 ? p.parts : 0, m, lane, nullptr);
+      if (lane == 0) s_f[m] = lse;
     }
     __syncthreads();
-    if (page >= a.rows.max_pages) continue;
-    const int t1 = min(t0 + (1 << a.pool.tile_shift), p.tiles);
-    for (int m = 0; m < a.unit_rows; ++m) {
-      if (seen_by(a, p, p.m0 + m) == 0) continue;
-      const float* mass = a.ws_mass + ((uint64_t)unit * a.unit_rows + m) * a.cap_tiles;
-      for (int t = t0; t < t1; ++t) w += exp2_fast(mass[t] - s_f[m]);
-    }
+    const uint64_t unit = (uint64_t)row * a.m_groups + g;
+    if (tile < p.tiles) w += tile_weight(a, a.ws_mass + unit * a.unit_rows * a.cap_tiles, s_f, tile);
   }
-  if (page < a.rows.max_pages) {
-    const uint64_t at = (uint64_t)row * a.rows.max_pages + page;
-    a.w_out[at] = a.w_in[at] + w;
-  }
+  write_weight(a, row, tile, w);
 }
 
 // ------------------------------------------------------------ eviction ----
@@ -935,33 +1126,212 @@ struct Evict {
   uint32_t keep, sink, recent;
 };
 
-// Whole numbers in the order of the weights.
+// Whole numbers above 0 in the order of the weights.
 __device__ __forceinline__ uint32_t weight_key(float w) {
   uint32_t b = __builtin_bit_cast(uint32_t, w);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return ~0u;
+  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0xFF800001u;  // NaN: one above infinity
   if (b == 0x80000000u) b = 0u;
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// One workgroup per row.  The weight of the last page to stay is found digit
-// by digit (8 bits at a time, from counts of the digits in LDS), then one pass in
-// order writes every page to its place.
-__global__ __launch_bounds__(kThreads) void evict_kernel(Evict e) {
+// What a row's workgroup does: keep the protected pages and, of pages lo .. hi
+// - 1, the `want` heaviest.
+struct Choice {
+  uint64_t at;  // the row's place in the tables
+  int len;
+  uint32_t held, left, lo, hi, want;
+  bool full;
+};
+
+__device__ __forceinline__ Choice choice_of(const Evict& e, uint32_t row) {
+  Choice c;
+  c.at = (uint64_t)row * e.max_pages;
+  c.len = min(max(e.lengths[row], 0), e.capacity);
+  c.held = ((uint32_t)c.len + (1u << e.page_shift) - 1u) >> e.page_shift;
+  c.full = c.held > e.keep;
+  c.left = c.full ? e.keep : c.held;
+  c.lo = e.sink;
+  c.hi = c.full ? c.held - e.recent : c.held;
+  c.want = c.full ? e.keep - e.sink - e.recent : 0;
+  return c;
+}
+
+// One workgroup per row of up to THREADS * R pages, the weights in LDS.
+// The weight of the last page to stay is found from counts in LDS: the keys
+// between the smallest and the largest are counted in 256 equal ranges, the
+// range that holds the wanted one is cut into 256 again, and so on.  (Bisecting
+// with one count a round takes 25 rounds where this takes 3: 16,384 pages x
+// 768 rows spent 47 us on it.)  With the counts of every 64 pages in LDS each
+// page then knows its place.
+template <int THREADS, int R>
+__global__ __launch_bounds__(THREADS, 8) void evict_kernel(Evict e) {
+  constexpr int kW = THREADS / kWave;
+  constexpr int kUnroll = R < 8 ? R : 8;
+  constexpr int kChunks = R * kW;  // of 64 pages, chunk i * kW + wave
+  constexpr uint32_t kStays = 0xFFFFFFFFu;  // above every weight's key; 0 is below
+  static_assert(kChunks <= 256, "a wave scans them, four to a lane");
+  static_assert(THREADS * R < 65536, "two counts to a word");
+  __shared__ uint32_t s_count[2][256];
+  __shared__ uint32_t s_bound[2][kW];
+  __shared__ uint32_t s_chunk[256];      // pages that stay, and ties in the upper half
+  __shared__ uint32_t s_key[R][THREADS];  // a thread reads its own only
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const Choice c = choice_of(e, blockIdx.x);
+  if (threadIdx.x == 0) e.lengths_out[blockIdx.x] = c.len - (int)((c.held - c.left) << e.page_shift);
+  const float* weights = e.weights + c.at;
+  const int32_t* pages = e.pages + c.at;
+  float* weights_out = e.weights_out + c.at;
+  int32_t* pages_out = e.pages_out + c.at;
+  // everything is asked for at once; the ids arrive while the places are worked out
+  float w[R];
+  int32_t id[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const uint32_t p = (uint32_t)i * THREADS + threadIdx.x;
+    w[i] = p < e.max_pages ? weights[p] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const uint32_t p = (uint32_t)i * THREADS + threadIdx.x;
+    id[i] = p < e.max_pages ? pages[p] : 0;
+  }
+  uint32_t low = 0xFFFFFFFFu, high = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const uint32_t p = (uint32_t)i * THREADS + threadIdx.x;
+    uint32_t key = p < c.held ? kStays : 0u;
+    if (c.full && p - c.lo < c.hi - c.lo) {
+      key = weight_key(w[i]);
+      low = min(low, key);
+      high = max(high, key);
+    }
+    s_key[i][threadIdx.x] = key;
+  }
+  uint32_t last = kStays - 1u, ties = 0;  // stay: keys above `last` and the first `ties` equal to it
+  if (c.want) {
+#pragma unroll
+    for (int s = 32; s; s >>= 1) {
+      low = min(low, (uint32_t)__shfl_xor((int)low, s));
+      high = max(high, (uint32_t)__shfl_xor((int)high, s));
+    }
+    if (lane == 0) {
+      s_bound[0][wave] = low;
+      s_bound[1][wave] = high;
+    }
+    if (threadIdx.x < 256) s_count[0][threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kW; ++x) {
+      low = min(low, s_bound[0][x]);
+      high = max(high, s_bound[1][x]);
+    }
+    low = (uint32_t)uniform((int)low);
+    high = (uint32_t)uniform((int)high);
+    // the key is in low .. high; `over` < want keys are above high
+    uint32_t over = 0;
+    last = low;
+    for (int round = 0; low < high; round ^= 1) {
+      const int shift = max(24 - (int)__builtin_clz(high - low), 0);
+      uint32_t* count = s_count[round];
+#pragma unroll kUnroll
+      for (int i = 0; i < R; ++i) {
+        const uint32_t above_low = s_key[i][threadIdx.x] - low;
+        if (above_low <= high - low) atomicAdd(&count[above_low >> shift], 1u);
+      }
+      __syncthreads();
+      // every wave reads them all; lane l has ranges 255 - 4 l down to 252 - 4 l
+      uint32_t n[4], mine = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mine += n[i] = count[255 - 4 * lane - i];
+      uint32_t before = over + wave_scan(mine) - mine;
+      uint32_t found = 0, over_found = 0, n_found = 0;
+      bool here = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (before < c.want && before + n[i] >= c.want) {
+          here = true;
+          found = 255u - 4u * lane - i;
+          over_found = before;
+          n_found = n[i];
+        }
+        before += n[i];
+      }
+      const int src = __builtin_ctzll(__ballot(here));
+      found = (uint32_t)__builtin_amdgcn_readlane((int)found, src);
+      over = (uint32_t)__builtin_amdgcn_readlane((int)over_found, src);
+      const bool exact = over + (uint32_t)__builtin_amdgcn_readlane((int)n_found, src) == c.want;
+      low += found << shift;
+      if (high - low >= 1u << shift) high = low + ((1u << shift) - 1u);  // no sum past 32 bits
+      last = low;
+      if (exact) {  // the whole range stays
+        last = low - 1u;
+        over = c.want;
+        break;
+      }
+      if (threadIdx.x < 256) s_count[round ^ 1][threadIdx.x] = 0;
+      __syncthreads();
+    }
+    ties = c.want - over;
+  }
+
+#pragma unroll kUnroll
+  for (int i = 0; i < R; ++i) {
+    const uint32_t key = s_key[i][threadIdx.x];
+    uint32_t n = (uint32_t)__popcll(__ballot(key > last));
+    if (ties) n += (uint32_t)__popcll(__ballot(key == last)) << 16;
+    if (lane == 0) s_chunk[i * kW + wave] = n;
+  }
+  __syncthreads();
+  if (wave == 0) {  // counts before each chunk
+    uint32_t x[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = 4 * lane + i < kChunks ? s_chunk[4 * lane + i] : 0u;
+      sum += x[i];
+    }
+    uint32_t before = wave_scan(sum) - sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (4 * lane + i < kChunks) s_chunk[4 * lane + i] = before;
+      before += x[i];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const uint32_t p = (uint32_t)i * THREADS + threadIdx.x;
+    const uint32_t key = s_key[i][threadIdx.x], chunk = s_chunk[i * kW + wave];
+    uint32_t before = lanes_below(__ballot(key > last), chunk & 0xFFFFu);  // pages that stay before this one
+    bool stays = key > last;
+    if (ties) {
+      const uint32_t tie = lanes_below(__ballot(key == last), chunk >> 16);
+      stays = stays || (key == last && tie < ties);
+      before += min(tie, ties);
+    }
+    // past the row's pages `before` is `left`, so that they keep their places
+    const uint32_t to = stays ? before : c.left + p - before;
+    if (p < e.max_pages) {
+      pages_out[to] = id[i];
+      weights_out[to] = p < c.held && !stays ? 0.f : w[i];
+    }
+  }
+}
+
+// Rows of any length: the weight is found digit by digit (8 bits at a time,
+// from counts in LDS), the weights read again for each.
+__global__ __launch_bounds__(kThreads) void evict_long_kernel(Evict e) {
   __shared__ uint32_t s_count[256];
   __shared__ uint32_t s_pick[2];
   __shared__ uint32_t s_sum[2][kWaves];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const uint32_t row = blockIdx.x;
-  const uint64_t at = (uint64_t)row * e.max_pages;
+  const Choice ch = choice_of(e, blockIdx.x);
+  const uint64_t at = ch.at;
   const float* weights = e.weights + at;
-  const int len = min(max(e.lengths[row], 0), e.capacity);
-  const uint32_t held = ((uint32_t)len + (1u << e.page_shift) - 1u) >> e.page_shift;
-  const bool full = held > e.keep;
-  const uint32_t left = full ? e.keep : held;
-  if (threadIdx.x == 0) e.lengths_out[row] = len - (int)((held - left) << e.page_shift);
-  const uint32_t lo = e.sink, hi = full ? held - e.recent : held;  // the pages to choose from
+  const uint32_t held = ch.held, left = ch.left, lo = ch.lo, hi = ch.hi;
+  const bool full = ch.full;
+  if (threadIdx.x == 0) e.lengths_out[blockIdx.x] = ch.len - (int)((held - left) << e.page_shift);
 
-  uint32_t key = 0, want = full ? e.keep - e.sink - e.recent : 0;
+  uint32_t key = 0, want = ch.want;
   if (full && want) {
     for (int shift = 24; shift >= 0; shift -= 8) {
       s_count[threadIdx.x] = 0;
@@ -975,13 +1345,7 @@ __global__ __launch_bounds__(kThreads) void evict_kernel(Evict e) {
         uint32_t c[4], mine = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) mine += c[i] = s_count[255 - 4 * lane - i];
-        uint32_t before = mine;
-#pragma unroll
-        for (int s = 1; s < kWave; s <<= 1) {
-          const uint32_t y = __shfl_up(before, s);
-          if (lane >= s) before += y;
-        }
-        before -= mine;
+        uint32_t before = wave_scan(mine) - mine;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (before < want && before + c[i] >= want) {
@@ -1139,8 +1503,8 @@ void launch_append(const Pool& pool, const Rows& rows, const Strided& k, const S
 struct Shape {
   int mt;
   int32_t m_rows, m_groups, unit_rows, cap_tiles;
-  uint32_t n_units, n_splits;
-  uint64_t mass_at, ml_at, bytes;  // in the workspace; the sums come first
+  uint32_t n_units, n_parts;
+  uint64_t of_at, mass_at, ml_at, bytes;  // in the workspace; the sums come first
 };
 
 // Compute units of the current device; 256 where a HIP error is pending, which
@@ -1161,7 +1525,7 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
   if (n_new && group > (1ull << 24) / n_new) return false;
   const uint64_t m = group * n_new;
   s->m_rows = (int32_t)m;
-  s->mt = m <= 16 ? 1 : m <= 32 || head_dim > 128 ? 2 : 4;
+  s->mt = m <= 16 ? 1 : m <= 32 ? 2 : most_query_tiles((int)head_dim / 64);
   const uint64_t per_unit = 16ull * s->mt;
   s->m_groups = (int32_t)((m + per_unit - 1) / per_unit);
   s->unit_rows = (int32_t)std::min<uint64_t>(m, per_unit);
@@ -1169,15 +1533,22 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
   const uint64_t units = n_rows * s->m_groups;
   if (units > kMaxGrid / 64) return false;
   s->n_units = (uint32_t)units;
-  // two workgroups a compute unit, which is what fits, and a step for each wave of a split
-  const uint64_t steps = (uint64_t)(s->cap_tiles + step_tiles((int)head_dim / 64, s->mt) - 1) / step_tiles((int)head_dim / 64, s->mt);
-  uint64_t splits = units ? (2ull * cus + units - 1) / units : 1;
-  splits = std::min<uint64_t>(splits, (steps + kWaves - 1) / kWaves);
-  s->n_splits = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(splits, kMaxSplits));
-  const bool direct = s->n_splits == 1 && s->m_groups <= 1;
-  const uint64_t parts = direct ? 0 : units * s->n_splits * s->unit_rows;
+  // As many parts as keep all workgroups on the chip at once, two to a compute
+  // unit: what comes after them would start over with an empty pipeline.  Rows
+  // of up to four steps a wave are not worth the second launch, which costs
+  // about as much as those, and units that fill half the chip are not cut.
+  const int st = step_tiles((int)head_dim / 64, s->mt);
+  const uint64_t steps = (uint64_t)(s->cap_tiles + st - 1) / st;
+  const uint64_t slots = std::min<uint64_t>(2ull * cus, kMaxParts);
+  s->n_parts = s->n_units;
+  if (units && units <= slots / 2 && n_rows <= (uint64_t)kWave * kRowsPerLane && steps > 4 * kWaves &&
+      steps * units < (1ull << 31))  // the sums of share_out
+    s->n_parts = (uint32_t)std::min<uint64_t>(slots, units * ((steps + kWaves - 1) / kWaves + 1));
+  const bool direct = s->n_parts == s->n_units && s->m_groups <= 1;
+  const uint64_t parts = direct ? 0 : (uint64_t)s->n_parts * s->unit_rows;
   s->ml_at = parts * head_dim * 4;
-  s->mass_at = (s->ml_at + parts * 8 + 15) / 16 * 16;
+  s->of_at = s->ml_at + parts * 8;
+  s->mass_at = (s->of_at + (s->n_parts != s->n_units ? units * 8 : 0) + 15) / 16 * 16;
   s->bytes = s->mass_at + (weights ? units * s->unit_rows * s->cap_tiles * 4 : 0);
   if (units * s->unit_rows > kMaxGrid / 2) return false;
   return true;
@@ -1185,9 +1556,9 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
 
 template <int DJ, bool F16, int MT>
 void launch_attention(const Attention& a, uint64_t n_rows, hipStream_t st) {
-  const bool direct = a.n_splits == 1 && a.m_groups == 1;
+  const bool direct = a.n_parts == a.n_units && a.m_groups == 1;
   if (a.n_units)
-    hipLaunchKernelGGL((attention_kernel<DJ, F16, MT>), dim3(a.n_units * a.n_splits), dim3(kThreads),
+    hipLaunchKernelGGL((attention_kernel<DJ, F16, MT>), dim3(a.n_parts), dim3(kThreads),
                        0, st, a);
   if (direct) return;
   const uint64_t blocks = (uint64_t)a.n_units * a.unit_rows + (a.w_out ? n_rows * a.weight_blocks : 0);
@@ -1309,6 +1680,7 @@ int ibp_kv_attention(const ibp_kv_cache* cache, const ibp_kv_table* table, uint3
   a.ws_o = (float*)workspace;
   a.ws_ml = (f32x2*)((char*)workspace + s.ml_at);
   a.ws_mass = (float*)((char*)workspace + s.mass_at);
+  a.ws_of = (int32_t*)((char*)workspace + s.of_at);
   a.scale = scale * 1.44269504088896340736f;
   a.group = (int32_t)(q_heads / table->kv_heads);
   a.m_rows = s.m_rows;
@@ -1316,8 +1688,9 @@ int ibp_kv_attention(const ibp_kv_cache* cache, const ibp_kv_table* table, uint3
   a.unit_rows = s.unit_rows;
   a.cap_tiles = s.cap_tiles;
   a.n_units = s.n_units;
-  a.n_splits = s.n_splits;
-  a.weight_blocks = (a.rows.max_pages + kThreads - 1) / kThreads;
+  a.n_rows = (uint32_t)n_rows;
+  a.n_parts = s.n_parts;
+  a.weight_blocks = (uint32_t)(s.cap_tiles + kThreads - 1) / kThreads;
   hipStream_t st = (hipStream_t)stream;
   switch (cache->head_dim / 64 * 2 + dtype) {
     case 2: launch_attention_mt<1, false>(a, s.mt, n_rows, st); break;
@@ -1369,7 +1742,16 @@ int ibp_kv_evict(const ibp_kv_table* table, uint32_t page_tokens, uint64_t keep_
   e.keep = (uint32_t)std::min<uint64_t>(keep_pages, 0xFFFFFFFFull);
   e.sink = (uint32_t)std::min<uint64_t>(sink_pages, 0xFFFFFFFFull);
   e.recent = (uint32_t)std::min<uint64_t>(recent_pages, 0xFFFFFFFFull);
-  hipLaunchKernelGGL(evict_kernel, dim3((uint32_t)n_rows), dim3(kThreads), 0, (hipStream_t)stream, e);
+  const dim3 grid((uint32_t)n_rows);
+  hipStream_t st = (hipStream_t)stream;
+  if (table->max_pages <= 1024)
+    hipLaunchKernelGGL((evict_kernel<256, 4>), grid, dim3(256), 0, st, e);
+  else if (table->max_pages <= 4096)
+    hipLaunchKernelGGL((evict_kernel<1024, 4>), grid, dim3(1024), 0, st, e);
+  else if (table->max_pages <= 16384)
+    hipLaunchKernelGGL((evict_kernel<1024, 16>), grid, dim3(1024), 0, st, e);
+  else
+    hipLaunchKernelGGL(evict_long_kernel, grid, dim3(kThreads), 0, st, e);
   return launched();
 }
 

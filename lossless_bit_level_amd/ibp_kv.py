@@ -115,8 +115,9 @@ def _check(fn: str, status: int):
         raise IBPKVError(fn, status)
 
 
-def _stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _stream(stream, t: torch.Tensor) -> int:
+    """The given stream, or the current one of t's device."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else stream.cuda_stream
 
 
 def _need(t: torch.Tensor, dtype: torch.dtype, name: str, shape=None):
@@ -177,7 +178,7 @@ def ibp_kv_append(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Tenso
     kt, vt = _tensor(k, "k", k.dtype, shape), _tensor(v, "v", k.dtype, shape)
     _check("ibp_kv_append",
            lib().ibp_kv_append(cache, table, dtype, k.shape[1], kt, vt,
-                               _counts(counts, table.n_seqs), _stream(stream)))
+                               _counts(counts, table.n_seqs), _stream(stream, pages)))
 
 
 def ibp_kv_attention_workspace_bytes(cache: ibp_kv_cache, pages: torch.Tensor,
@@ -233,7 +234,7 @@ def ibp_kv_attention(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Te
            L.ibp_kv_attention(cache, table, dtype, q_heads, n_new, qt, ot,
                               _counts(counts, table.n_seqs),
                               1.0 / math.sqrt(cache.head_dim) if scale is None else scale,
-                              w, wo, ws, ws_bytes, _stream(stream)))
+                              w, wo, ws, ws_bytes, _stream(stream, q)))
     return out, weights_out
 
 
@@ -260,5 +261,5 @@ def ibp_kv_evict(pages: torch.Tensor, weights: torch.Tensor, lengths: torch.Tens
     _check("ibp_kv_evict",
            lib().ibp_kv_evict(table, page_tokens, keep_pages, sink_pages, recent_pages,
                               weights.data_ptr(), pages_out.data_ptr(), weights_out.data_ptr(),
-                              lengths_out.data_ptr(), _stream(stream)))
+                              lengths_out.data_ptr(), _stream(stream, pages)))
     return pages_out, weights_out, lengths_out
