@@ -23,6 +23,7 @@ constexpr int step_tiles(int dj, int mt) { return dj * mt <= 1 ? 4 : 2; }
 constexpr int most_query_tiles(int dj) { return dj <= 2 ? 4 : 2; }
 constexpr int kUnit = 1024;     // bytes of a tile that one wide load of a wave takes
 constexpr int kMaxParts = 512;
+constexpr int kLdsMass = 4096;  // shares of tiles that a workgroup that works alone keeps in LDS
 constexpr int kExpMin = -126, kExpMax = 119;  // exponents of a page's scale
 constexpr float kE4m3Max = 448.f;
 
@@ -248,17 +249,55 @@ __device__ __forceinline__ int new_count(const Rows& r, uint32_t seq) {
 
 // -------------------------------------------------------------- append ----
 
-template <bool F16>
-__device__ __forceinline__ void load8(const uint16_t* p, bool wide, float* x) {
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ u32x4 load8(const uint16_t* p, bool wide) {
+  if (wide) return *(const u32x4*)p;
   u16x8 h;
-  if (wide) {
-    h = *(const u16x8*)p;
-  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = p[i];
+  for (int i = 0; i < 8; ++i) h[i] = p[i];
+  return __builtin_bit_cast(u32x4, h);
+}
+
+// Largest magnitude of the 16-bit numbers so far, in each half: as whole
+// numbers, which order magnitudes, infinity and NaN at the top.
+__device__ __forceinline__ uint32_t magnitude_max(uint32_t m, uint32_t x) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m),
+                                                                __builtin_bit_cast(u16x2, x & 0x7FFF7FFFu)));
+}
+
+template <bool F16>
+__device__ __forceinline__ bool not_finite(uint32_t half) {
+  return (half & 0x7FFFu) >= (F16 ? 0x7C00u : 0x7F80u);
+}
+
+// The lane's largest finite magnitude: 0 in place of what is not finite.
+template <bool F16>
+__device__ __forceinline__ uint32_t finite_max(uint32_t m, uint32_t x) {
+  if (not_finite<F16>(x)) x &= 0xFFFF0000u;
+  if (not_finite<F16>(x >> 16)) x &= 0xFFFFu;
+  return magnitude_max(m, x);
+}
+
+// Codes of the pairs a and b at the scale 2^e.  `plain`: all are finite and
+// within the scale, which the conversion of pairs then does as it is (it
+// rounds to nearest, ties to even).
+template <bool F16>
+__device__ __forceinline__ uint32_t codes_of(uint32_t a, uint32_t b, bool plain, float scale, float inv) {
+  if (plain) {
+    i16x2 r = {0, 0};
+    if constexpr (F16) {
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(r, __builtin_bit_cast(f16x2, a), scale, false);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(r, __builtin_bit_cast(f16x2, b), scale, true);
+    } else {
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, a), scale, false);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, b), scale, true);
+    }
+    return __builtin_bit_cast(uint32_t, r);
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = to_float<F16>(h[i]);
+  return codes4(code_value(to_float<F16>((uint16_t)a), inv), code_value(to_float<F16>((uint16_t)(a >> 16)), inv),
+                code_value(to_float<F16>((uint16_t)b), inv), code_value(to_float<F16>((uint16_t)(b >> 16)), inv));
 }
 
 // One wave per 16-token tile of a page that receives new tokens; the waves of
@@ -266,7 +305,9 @@ __device__ __forceinline__ void load8(const uint16_t* p, bool wide, float* x) {
 // key unit are 16 dims of one token, so keys go straight from the loads to
 // the store.  A lane's 16 bytes of a value unit are 4 tokens x 4 dims: the
 // lane that loads 8 dims of 4 tokens writes 8 words of 4 codes to LDS, from
-// which units are read back.
+// which units are read back.  Bound by HBM: 4 prompts of 4096 tokens x 32 heads
+// x 128 dims (403 MB moved) take 75 us, 5.3 TB/s; with plain stores 78 us, with
+// non-temporal loads as well 76 us.
 template <int DJ, bool F16>
 __global__ __launch_bounds__(kThreads) void append_kernel(Pool pool, Rows rows, Strided k,
                                                           Strided v, uint32_t pages_per_row,
@@ -280,34 +321,31 @@ __global__ __launch_bounds__(kThreads) void append_kernel(Pool pool, Rows rows, 
   const int tiles = 1 << pool.tile_shift;
   const uint64_t task = (uint64_t)blockIdx.x * (kWaves >> pool.tile_shift) + (wave >> pool.tile_shift);
   const int tile = wave & (tiles - 1);
-  const uint32_t row = (uint32_t)(min(task, n_tasks - 1) / pages_per_row);
-  const uint32_t seq = row / rows.heads, head = row % rows.heads;
+  // heads first: what neighbouring workgroups read lies together in [seq][token][head]
+  const uint32_t line = (uint32_t)(min(task, n_tasks - 1) / rows.heads);
+  const uint32_t head = (uint32_t)(min(task, n_tasks - 1) % rows.heads);
+  const uint32_t seq = line / pages_per_row, row = seq * rows.heads + head;
   const int end = row_length(rows, row), count = new_count(rows, seq);
   const int first = max(end - count, 0);      // position of the first new token that exists
   const int origin = end - count;             // position of token 0
-  const int page_tokens = kTile << pool.tile_shift;
-  const int page = first / page_tokens + (int)(min(task, n_tasks - 1) % pages_per_row);
-  const int page_at = page * page_tokens, at = page_at + tile * kTile;
-  bool live = task < n_tasks && count > 0 && page_at < end;
+  const int page_shift = 4 + (int)pool.tile_shift;
+  const int page = (first >> page_shift) + (int)(line % pages_per_row);
+  const int page_at = page << page_shift, at = page_at + tile * kTile;
+  const bool reached = task < n_tasks && count > 0 && page < (int)rows.max_pages && page_at < end;
   int32_t id = -1;
-  if (live) id = rows.pages[(uint64_t)row * rows.max_pages + page];
-  live = live && (uint32_t)id < pool.n_pages;
+  if (reached) id = rows.pages[(uint64_t)row * rows.max_pages + page];
 
   // keys: token at + lane % 16, dims 64 j + 16 (lane / 16) + 0..15
-  float kx[DJ][16], vx[kPasses][4][8];
+  u32x4 kx[DJ][2], vx[kPasses][4];
   const int kt = at + lane % 16, kg = lane / 16;
-  const bool k_new = live && kt >= first && kt < end;
-  float k_max = 0.f, v_max = 0.f;
 #pragma unroll
-  for (int j = 0; j < DJ; ++j)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) kx[j][i] = 0.f;
-  if (k_new) {
+  for (int j = 0; j < DJ; ++j) kx[j][0] = kx[j][1] = u32x4{0, 0, 0, 0};
+  if (reached && kt >= first && kt < end) {
     const uint16_t* p = k.data + seq * k.seq + (int64_t)(kt - origin) * k.token + head * k.head + 16 * kg;
 #pragma unroll
     for (int j = 0; j < DJ; ++j) {
-      load8<F16>(p + 64 * j, k.wide, kx[j]);
-      load8<F16>(p + 64 * j + 8, k.wide, kx[j] + 8);
+      kx[j][0] = load8(p + 64 * j, k.wide);
+      kx[j][1] = load8(p + 64 * j + 8, k.wide);
     }
   }
   // values: octet `item % kOctets` of dims, tokens at + 4 (item / kOctets) + 0..3
@@ -318,27 +356,39 @@ __global__ __launch_bounds__(kThreads) void append_kernel(Pool pool, Rows rows, 
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = at + 4 * g + r;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) vx[p][r][i] = 0.f;
-      if (live && g < 4 && t >= first && t < end)
-        load8<F16>(v.data + seq * v.seq + (int64_t)(t - origin) * v.token + head * v.head + 8 * o,
-                   v.wide, vx[p][r]);
+      vx[p][r] = u32x4{0, 0, 0, 0};
+      if (reached && g < 4 && t >= first && t < end)
+        vx[p][r] = load8(v.data + seq * v.seq + (int64_t)(t - origin) * v.token + head * v.head + 8 * o, v.wide);
     }
   }
+  const bool live = (uint32_t)id < pool.n_pages;
+  uint32_t km = 0, vm = 0;
 #pragma unroll
   for (int j = 0; j < DJ; ++j)
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (finite(kx[j][i])) k_max = fmaxf(k_max, fabsf(kx[j][i]));
+    for (int i = 0; i < 8; ++i) km = magnitude_max(km, kx[j][i / 4][i % 4]);
 #pragma unroll
   for (int p = 0; p < kPasses; ++p)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int i = 0; i < 16; ++i) vm = magnitude_max(vm, vx[p][i / 4][i % 4]);
+  const bool k_odd = __ballot(not_finite<F16>(km) || not_finite<F16>(km >> 16)) != 0;
+  const bool v_odd = __ballot(not_finite<F16>(vm) || not_finite<F16>(vm >> 16)) != 0;
+  if (k_odd) {
+    km = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (finite(vx[p][r][i])) v_max = fmaxf(v_max, fabsf(vx[p][r][i]));
-  k_max = wave_max(k_max);
-  v_max = wave_max(v_max);
+    for (int j = 0; j < DJ; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) km = finite_max<F16>(km, kx[j][i / 4][i % 4]);
+  }
+  if (v_odd) {
+    vm = 0;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) vm = finite_max<F16>(vm, vx[p][i / 4][i % 4]);
+  }
+  float k_max = wave_max(to_float<F16>((uint16_t)max(km & 0xFFFFu, km >> 16)));
+  float v_max = wave_max(to_float<F16>((uint16_t)max(vm & 0xFFFFu, vm >> 16)));
   // a page that held tokens keeps a larger scale
   const bool held = live && page_at < first;
   float k_was = 0.f, v_was = 0.f;
@@ -363,11 +413,15 @@ __global__ __launch_bounds__(kThreads) void append_kernel(Pool pool, Rows rows, 
     ke = max(ke, held_exponent(k_was));
     ve = max(ve, held_exponent(v_was));
   }
+  ke = uniform(ke);
+  ve = uniform(ve);
+  const float k_scale = power2(ke), v_scale = power2(ve);
   const float k_inv = power2(-ke), v_inv = power2(-ve);
   const float k_ratio = k_was * k_inv, v_ratio = v_was * v_inv;
+  const bool k_plain = !k_odd && ke > kExpMin && ke < kExpMax, v_plain = !v_odd && ve > kExpMin && ve < kExpMax;
   if (tile == 0 && lane == 0) {
-    pool.k_scales[id] = power2(ke);
-    pool.v_scales[id] = power2(ve);
+    pool.k_scales[id] = k_scale;
+    pool.v_scales[id] = v_scale;
   }
   const uint64_t base = (uint64_t)(uint32_t)id * pool.page_bytes + (uint32_t)(tile * kTile * D);
   uint8_t* kp = pool.k_codes + base + lane * 16;
@@ -379,8 +433,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(Pool pool, Rows rows, 
     u32x4 c;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      c[i] = codes4(code_value(kx[j][4 * i], k_inv), code_value(kx[j][4 * i + 1], k_inv),
-                    code_value(kx[j][4 * i + 2], k_inv), code_value(kx[j][4 * i + 3], k_inv));
+      c[i] = codes_of<F16>(kx[j][i / 2][i % 2 * 2], kx[j][i / 2][i % 2 * 2 + 1], k_plain, k_scale, k_inv);
     if (k_old) {
       c = *(const u32x4*)(kp + j * kUnit);
       if (k_ratio != 1.f) {
@@ -388,7 +441,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(Pool pool, Rows rows, 
         for (int i = 0; i < 4; ++i) c[i] = rescale4(c[i], k_ratio);
       }
     }
-    *(u32x4*)(kp + j * kUnit) = c;
+    __builtin_nontemporal_store(c, (u32x4*)(kp + j * kUnit));
   }
 
   uint32_t* tile_words = s_tile[wave];
@@ -398,11 +451,14 @@ __global__ __launch_bounds__(kThreads) void append_kernel(Pool pool, Rows rows, 
     const int g = item / kOctets, o = item % kOctets;
     if (g < 4) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int d = 8 * o + i;
-        tile_words[(d / 64) * 256 + g * 64 + (d % 16) * 4 + d % 64 / 16] =
-            codes4(code_value(vx[p][0][i], v_inv), code_value(vx[p][1][i], v_inv),
-                   code_value(vx[p][2][i], v_inv), code_value(vx[p][3][i], v_inv));
+      for (int i = 0; i < 4; ++i) {
+        // dims d and d + 1 of tokens 0, 1 and of tokens 2, 3
+        const uint32_t a = codes_of<F16>(vx[p][0][i], vx[p][1][i], v_plain, v_scale, v_inv);
+        const uint32_t b = codes_of<F16>(vx[p][2][i], vx[p][3][i], v_plain, v_scale, v_inv);
+        const int d = 8 * o + 2 * i;
+        uint32_t* word = tile_words + (d / 64) * 256 + g * 64 + (d % 16) * 4 + d % 64 / 16;
+        word[0] = __builtin_amdgcn_perm(b, a, 0x06040200u);
+        word[4] = __builtin_amdgcn_perm(b, a, 0x07050301u);
       }
     }
   }
@@ -421,7 +477,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(Pool pool, Rows rows, 
         c[i] = (c[i] & ~old) | (w & old);
       }
     }
-    *(u32x4*)(vp + j * kUnit) = c;
+    __builtin_nontemporal_store(c, (u32x4*)(vp + j * kUnit));
   }
 }
 
@@ -443,6 +499,7 @@ struct Attention {
   int32_t m_groups;    // units a head's query rows are cut into
   int32_t unit_rows;   // query rows of a unit
   int32_t cap_tiles;
+  uint32_t mass_in_lds;  // the unit's shares fit kLdsMass, and no other workgroup needs them
   uint32_t n_units;
   uint32_t n_rows;
   uint32_t n_parts;  // workgroups that the units are spread over; n_units: one each
@@ -754,7 +811,7 @@ __device__ __forceinline__ void mask_step(const Plan& p, int step, int lane, con
 template <int DJ, int MT, int ST>
 __device__ __forceinline__ void softmax(const Attention& a, const Plan& p, int step, int lane,
                                         const Where<ST>& w, f32x4 (&s)[MT][ST], float* mass_row,
-                                        State<DJ, MT>& st, Probs<MT, ST>& out) {
+                                        float* mass_lds, State<DJ, MT>& st, Probs<MT, ST>& out) {
   const int g = lane / 16;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
@@ -796,10 +853,15 @@ __device__ __forceinline__ void softmax(const Attention& a, const Plan& p, int s
       mine = pair_sum32(mine, mine);
     const bool sole = ST == 4 || g < ST;
     if (sole) st.l[mt] += mine;
-    if (mass_row) {
+    if (a.w_out) {
       const int tile = step * ST + g, m_local = mt * 16 + lane % 16;
-      if (sole && tile < p.tiles && m_local < a.unit_rows)
-        mass_row[(uint64_t)m_local * a.cap_tiles + tile] = base + log2_fast(mine);
+      if (sole && tile < p.tiles && m_local < a.unit_rows) {
+        const float share = base + log2_fast(mine);
+        if (a.mass_in_lds)
+          mass_lds[m_local * a.cap_tiles + tile] = share;
+        else
+          mass_row[(uint64_t)m_local * a.cap_tiles + tile] = share;
+      }
     }
   }
 }
@@ -868,6 +930,7 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
   __shared__ __attribute__((aligned(16))) float s_o[kWaves][16][kPitch];
   __shared__ f32x2 s_ml[kWaves][MT * 16];
   __shared__ float s_lse[MT * 16];
+  __shared__ float s_mass[kLdsMass];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const bool direct = a.n_parts == a.n_units && a.m_groups == 1;
   const Part part = part_of_workgroup<ST>(a, blockIdx.x, lane);
@@ -910,7 +973,7 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
 #pragma unroll
     for (int i = 0; i < 4 * DJ; ++i) st.o[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  float* mass_row = a.w_out ? a.ws_mass + (uint64_t)unit * a.unit_rows * a.cap_tiles : nullptr;
+  float* mass_row = a.ws_mass + (uint64_t)unit * a.unit_rows * a.cap_tiles;
 
   // While a step is computed the next one's tiles are on their way: its keys
   // take the registers of this one's as soon as the scores are done, its
@@ -939,7 +1002,7 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
       }
       if (!plain) mask_step<DJ, MT, ST>(p, step, lane, seen, here, s, v, st);
       Probs<MT, ST> pr;
-      softmax<DJ, MT, ST>(a, p, step, lane, here, s, mass_row, st, pr);
+      softmax<DJ, MT, ST>(a, p, step, lane, here, s, mass_row, s_mass, st, pr);
       gather_values<DJ, MT, ST>(v, pr, st);
       if (!more) break;
       load_tiles<DJ, ST, kOnce>(a.pool.v_codes, next, lane, v);
@@ -1013,7 +1076,10 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
   __syncthreads();
   for (int base = 0; base < a.cap_tiles; base += kThreads) {  // whole waves: lanes add to each other
     const int tile = base + (int)threadIdx.x;
-    write_weight(a, p.row, tile, tile < p.tiles ? tile_weight(a, mass_row, s_lse, tile) : 0.f);
+    float w = 0.f;
+    if (tile < p.tiles)
+      w = a.mass_in_lds ? tile_weight(a, s_mass, s_lse, tile) : tile_weight(a, mass_row, s_lse, tile);
+    write_weight(a, p.row, tile, w);
   }
 }
 
@@ -1504,6 +1570,7 @@ struct Shape {
   int mt;
   int32_t m_rows, m_groups, unit_rows, cap_tiles;
   uint32_t n_units, n_parts;
+  bool mass_in_lds;
   uint64_t of_at, mass_at, ml_at, bytes;  // in the workspace; the sums come first
 };
 
@@ -1549,7 +1616,8 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
   s->ml_at = parts * head_dim * 4;
   s->of_at = s->ml_at + parts * 8;
   s->mass_at = (s->of_at + (s->n_parts != s->n_units ? units * 8 : 0) + 15) / 16 * 16;
-  s->bytes = s->mass_at + (weights ? units * s->unit_rows * s->cap_tiles * 4 : 0);
+  s->mass_in_lds = direct && (uint64_t)s->unit_rows * s->cap_tiles <= (uint64_t)kLdsMass;
+  s->bytes = s->mass_at + (weights && !s->mass_in_lds ? units * s->unit_rows * s->cap_tiles * 4 : 0);
   if (units * s->unit_rows > kMaxGrid / 2) return false;
   return true;
 }
@@ -1687,6 +1755,7 @@ int ibp_kv_attention(const ibp_kv_cache* cache, const ibp_kv_table* table, uint3
   a.m_groups = s.m_groups;
   a.unit_rows = s.unit_rows;
   a.cap_tiles = s.cap_tiles;
+  a.mass_in_lds = s.mass_in_lds;
   a.n_units = s.n_units;
   a.n_rows = (uint32_t)n_rows;
   a.n_parts = s.n_parts;

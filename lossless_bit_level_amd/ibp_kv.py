@@ -211,7 +211,7 @@ def ibp_kv_attention(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Te
     shape = (table.n_seqs, n_new, q_heads, cache.head_dim)
     qt = _tensor(q, "q", q.dtype, shape)
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     ot = _tensor(out, "out", q.dtype, shape)
     w = wo = None
     if weights is not None:

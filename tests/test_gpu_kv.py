@@ -286,6 +286,27 @@ def test_attention_many_splits(kv):
     close(out, wo, expect(p, [[n]], q, w))
 
 
+@pytest.mark.parametrize("group,new", [(16, 1), (16, 5)])
+def test_attention_many_rows(kv, group, new):
+    """More rows than the chip holds workgroups at once, so that none is cut,
+    over tables with room for long rows; with 80 query rows a head, units of
+    one head meet in the joining kernel."""
+    seqs, heads, pt, d, m = 40, 8, 64, 64, 70
+    lens = [(17 * i) % 101 for i in range(seqs)]
+    lens[3] = 700
+    p = Pages(kv, seqs, heads, m, pt, d, n_pages=seqs * heads * m)
+    rng = np.random.default_rng(1)
+    for pool in (p.k, p.v):
+        pool[0][:] = rng.integers(0, 0x58, pool[0].shape, dtype=np.uint8) | (rng.integers(0, 2, pool[0].shape, dtype=np.uint8) << 7)
+        pool[1][:] = 2.0 ** rng.integers(-3, 2, pool[1].shape)
+    p.upload()
+    q = torch.randn(seqs, new, heads * group, d, generator=torch.Generator().manual_seed(new)).bfloat16()
+    w = rng.random((seqs, heads, m), dtype=np.float32)
+    lengths = grid(seqs, heads, lens)
+    out, wo = run_attention(kv, p, lengths, q, w)
+    close(out, wo, expect(p, lengths, q, w))
+
+
 def test_attention_large_scores(kv):
     """Scores of some hundreds: the statistics must be those of the whole row."""
     p = filled(kv, 2, 2, 40, 16, 128, [600, 500], seed=8, amp=30.0)
