@@ -558,3 +558,20 @@ def test_graph_of_a_decoding_step(kv):
         for x, y in zip(other["t"], eager["t"]):
             assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), i
     assert int(eager["lengths"].max()) <= 6 * pt
+
+
+def test_example_runs_them_together(kv):
+    """The example with small sizes: what evicted pages held comes back from
+    the archive bit for bit (asserted inside), rows end within the budget."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "kv_decode.py")
+    spec = importlib.util.spec_from_file_location("kv_decode", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    out, lengths, weights = example.main(seqs=2, heads=3, group=2, prompt=320, steps=20, keep=12, quiet=True)
+    torch.cuda.synchronize()
+    assert torch.isfinite(out).all() and int(lengths.max()) <= 12 * 16
+    # weights of pages that are not held are 0
+    held = -(-lengths.long() // 16)
+    assert not weights[torch.arange(weights.shape[2], device="cuda") >= held[..., None]].any()
