@@ -184,6 +184,17 @@ __device__ __forceinline__ float wave_max(float x) {
   return fmaxf(y[0], y[1]);
 }
 
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x121, 0xF, 0xF, false));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x122, 0xF, 0xF, false));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x124, 0xF, 0xF, false));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xF, 0xF, false));
+  const auto y = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  x = max((uint32_t)y[0], (uint32_t)y[1]);
+  const auto z = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return max((uint32_t)z[0], (uint32_t)z[1]);
+}
+
 __device__ __forceinline__ float wave_sum(float x) {
   x += row_rotate<0x121>(x);
   x += row_rotate<0x122>(x);
@@ -223,11 +234,22 @@ struct Pool {
   uint32_t tile_shift;  // log2 of a page's tiles
 };
 
+// Division of numbers below 2^31 by one that the host knows: with 2^l >= d the
+// multiplier ceil(2^(31 + l) / d) is off by less than 2^l / d, too little to
+// show.  (A division by a number in a register takes some 30 instructions.)
+struct Divisor {
+  uint32_t d, mul, shift;
+};
+
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const Divisor& x) {
+  return (uint32_t)(((uint64_t)n * x.mul) >> x.shift);
+}
+
 struct Rows {
   const int32_t* pages;
   const int32_t* lengths;
   const int32_t* counts;
-  uint32_t heads;
+  Divisor heads;
   uint32_t max_pages;
   int32_t capacity;  // tokens
   int32_t n_new;
@@ -310,8 +332,8 @@ __device__ __forceinline__ uint32_t codes_of(uint32_t a, uint32_t b, bool plain,
 // non-temporal loads as well 76 us.
 template <int DJ, bool F16>
 __global__ __launch_bounds__(kThreads) void append_kernel(Pool pool, Rows rows, Strided k,
-                                                          Strided v, uint32_t pages_per_row,
-                                                          uint64_t n_tasks) {
+                                                          Strided v, Divisor pages_per_row,
+                                                          uint32_t n_tasks) {
   constexpr int D = 64 * DJ;
   constexpr int kOctets = D / 8;
   constexpr int kPasses = (kOctets * 4 + kWave - 1) / kWave;
@@ -319,17 +341,17 @@ __global__ __launch_bounds__(kThreads) void append_kernel(Pool pool, Rows rows, 
   __shared__ float s_max[2][kWaves];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int tiles = 1 << pool.tile_shift;
-  const uint64_t task = (uint64_t)blockIdx.x * (kWaves >> pool.tile_shift) + (wave >> pool.tile_shift);
+  const uint32_t task = blockIdx.x * (kWaves >> pool.tile_shift) + (wave >> pool.tile_shift);
   const int tile = wave & (tiles - 1);
   // heads first: what neighbouring workgroups read lies together in [seq][token][head]
-  const uint32_t line = (uint32_t)(min(task, n_tasks - 1) / rows.heads);
-  const uint32_t head = (uint32_t)(min(task, n_tasks - 1) % rows.heads);
-  const uint32_t seq = line / pages_per_row, row = seq * rows.heads + head;
+  const uint32_t line = quotient(min(task, n_tasks - 1), rows.heads);
+  const uint32_t head = min(task, n_tasks - 1) - line * rows.heads.d;
+  const uint32_t seq = quotient(line, pages_per_row), row = seq * rows.heads.d + head;
   const int end = row_length(rows, row), count = new_count(rows, seq);
   const int first = max(end - count, 0);      // position of the first new token that exists
   const int origin = end - count;             // position of token 0
   const int page_shift = 4 + (int)pool.tile_shift;
-  const int page = (first >> page_shift) + (int)(line % pages_per_row);
+  const int page = (first >> page_shift) + (int)(line - seq * pages_per_row.d);
   const int page_at = page << page_shift, at = page_at + tile * kTile;
   const bool reached = task < n_tasks && count > 0 && page < (int)rows.max_pages && page_at < end;
   int32_t id = -1;
@@ -494,21 +516,22 @@ struct Attention {
   float* ws_mass;  // [unit][unit_rows][cap_tiles] log2 of a tile's share of exp2(s)
   int32_t* ws_of;  // [unit][2] first part and number of parts, of units that have a token
   float scale;     // scale * log2(e)
-  int32_t group;
+  Divisor group;
+  Divisor m_groups;    // units a head's query rows are cut into
+  Divisor unit_rows;   // query rows of a unit
   int32_t m_rows;      // group * n_new: query rows of a key/value head
-  int32_t m_groups;    // units a head's query rows are cut into
-  int32_t unit_rows;   // query rows of a unit
   int32_t cap_tiles;
   uint32_t mass_in_lds;  // the unit's shares fit kLdsMass, and no other workgroup needs them
   uint32_t n_units;
   uint32_t n_rows;
   uint32_t n_parts;  // workgroups that the units are spread over; n_units: one each
-  uint32_t weight_blocks;  // of a row, in the combining kernel
+  Divisor weight_blocks;  // of a row, in the joining kernel
 };
 
 // Which part of which unit a workgroup takes.
 struct Part {
   uint32_t row;
+  int len;         // tokens of the row
   int group;       // of the head's query rows
   int index, of;   // the unit is cut into `of` parts
   uint32_t first;  // part 0 of the unit; the next ones are m_groups apart
@@ -537,18 +560,18 @@ constexpr int kRowsPerLane = 4;  // of the rows that share out the workgroups
 //   lane l: rows 4 l .. 4 l + 3, `share` workgroups a unit each, `before` those
 //   of the rows before them.
 template <int ST>
-__device__ __forceinline__ void share_out(const Attention& a, int lane, int (&share)[kRowsPerLane],
-                                          int& before) {
+__device__ __forceinline__ void share_out(const Attention& a, int lane, int (&len)[kRowsPerLane],
+                                          int (&share)[kRowsPerLane], int& before) {
   int total = 0;
 #pragma unroll
   for (int i = 0; i < kRowsPerLane; ++i) {
     const uint32_t row = lane * kRowsPerLane + i;
-    const int len = row < a.n_rows ? row_length(a.rows, row) : 0;
-    share[i] = (int)(((uint32_t)len + kTile * ST - 1) / (kTile * ST));
+    len[i] = row < a.n_rows ? row_length(a.rows, row) : 0;
+    share[i] = (int)(((uint32_t)len[i] + kTile * ST - 1) / (kTile * ST));
     total += share[i];
   }
   const uint32_t all = (uint32_t)__builtin_amdgcn_readlane((int)wave_scan((uint32_t)total), kWave - 1) *
-                       (uint32_t)a.m_groups;
+                       a.m_groups.d;
   const uint32_t room = a.n_parts - a.n_units;
   const uint32_t c = max((all + room - 1) / room, (uint32_t)kWaves);
   int mine = 0;
@@ -563,25 +586,26 @@ __device__ __forceinline__ void share_out(const Attention& a, int lane, int (&sh
 template <int ST>
 __device__ __forceinline__ Part part_of_workgroup(const Attention& a, uint32_t w, int lane) {
   Part t;
+  const uint32_t x = quotient(w, a.m_groups);
+  t.group = (int)(w - x * a.m_groups.d);
   if (a.n_parts == a.n_units) {
-    t.row = w / a.m_groups;
-    t.group = (int)(w % a.m_groups);
+    t.row = x;
+    t.len = row_length(a.rows, x);
     t.index = 0;
     t.of = 1;
     t.first = w;
     t.idle = false;
     return t;
   }
-  int share[kRowsPerLane], before;
-  share_out<ST>(a, lane, share, before);
-  const int x = (int)(w / a.m_groups);
-  t.group = (int)(w % a.m_groups);
-  int row = 0, index = 0, of = 0, first = 0;
+  int lens[kRowsPerLane], share[kRowsPerLane], before;
+  share_out<ST>(a, lane, lens, share, before);
+  int row = 0, len = 0, index = 0, of = 0, first = 0;
 #pragma unroll
   for (int i = 0; i < kRowsPerLane; ++i) {
-    if (x >= before && x < before + share[i]) {
+    if ((int)x >= before && (int)x < before + share[i]) {
       row = lane * kRowsPerLane + i;
-      index = x - before;
+      len = lens[i];
+      index = (int)x - before;
       of = share[i];
       first = before;
     }
@@ -591,25 +615,29 @@ __device__ __forceinline__ Part part_of_workgroup(const Attention& a, uint32_t w
   t.idle = who == 0;
   const int src = t.idle ? 0 : __builtin_ctzll(who);
   t.row = (uint32_t)__builtin_amdgcn_readlane(row, src);
+  t.len = __builtin_amdgcn_readlane(len, src);
   t.index = __builtin_amdgcn_readlane(index, src);
   t.of = __builtin_amdgcn_readlane(of, src);
-  t.first = (uint32_t)__builtin_amdgcn_readlane(first, src) * (uint32_t)a.m_groups + t.group;
+  t.first = (uint32_t)__builtin_amdgcn_readlane(first, src) * a.m_groups.d + t.group;
   return t;
 }
 
-// The parts of a unit, as its part 0 left them.
+// The parts of a unit, as its part 0 left them (a row without a token has none,
+// and what is read for it is not used).
 __device__ __forceinline__ Part parts_of_unit(const Attention& a, uint32_t row, int group) {
   Part t;
   t.row = row;
   t.group = group;
   t.index = 0;
   t.idle = false;
-  const uint32_t unit = row * (uint32_t)a.m_groups + group;
+  const uint32_t unit = row * a.m_groups.d + group;
+  t.len = row_length(a.rows, row);
   t.first = unit;
   t.of = 1;
-  if (a.n_parts != a.n_units && row_length(a.rows, row) > 0) {
-    t.first = (uint32_t)a.ws_of[2 * unit];
-    t.of = a.ws_of[2 * unit + 1];
+  if (a.n_parts != a.n_units) {
+    const int first = a.ws_of[2 * unit], of = a.ws_of[2 * unit + 1];
+    t.first = t.len > 0 ? (uint32_t)first : 0u;
+    t.of = t.len > 0 ? of : 1;
   }
   return t;
 }
@@ -618,14 +646,13 @@ template <int MT, int ST>
 __device__ __forceinline__ Plan plan_unit(const Attention& a, const Part& t) {
   Plan p;
   p.row = t.row;
-  p.seq = p.row / a.rows.heads;
-  p.head = p.row % a.rows.heads;
+  p.seq = quotient(p.row, a.rows.heads);
+  p.head = p.row - p.seq * a.rows.heads.d;
   p.m0 = t.group * (MT * 16);
-  const int len = row_length(a.rows, p.row);
   p.count = new_count(a.rows, p.seq);
-  p.origin = len - p.count;
-  const int t_low = p.m0 / a.group;
-  const int t_high = min((min(p.m0 + MT * 16, a.m_rows) - 1) / a.group, p.count - 1);
+  p.origin = t.len - p.count;
+  const int t_low = (int)quotient(p.m0, a.group);
+  const int t_high = min((int)quotient(min(p.m0 + MT * 16, a.m_rows) - 1, a.group), p.count - 1);
   p.end = t_high >= t_low ? max(p.origin + t_high + 1, 0) : 0;
   p.full = max(p.origin + t_low + 1, 1);
   p.tiles = (p.end + kTile - 1) / kTile;
@@ -637,13 +664,14 @@ __device__ __forceinline__ Plan plan_unit(const Attention& a, const Part& t) {
 
 // Tokens of the row that query row m sees; 0: none, or no such row.
 __device__ __forceinline__ int seen_by(const Attention& a, const Plan& p, int m) {
-  const int t = m / a.group;
+  const int t = (int)quotient(m, a.group);
   return m < a.m_rows && t < p.count ? max(p.origin + t + 1, 0) : 0;
 }
 
 __device__ __forceinline__ uint16_t* row_of(const Strided& x, const Attention& a, const Plan& p, int m) {
-  return x.data + p.seq * x.seq + (int64_t)(m / a.group) * x.token +
-         ((int64_t)p.head * a.group + m % a.group) * x.head;
+  const int t = (int)quotient(m, a.group);
+  return x.data + p.seq * x.seq + (int64_t)t * x.token +
+         ((int64_t)p.head * a.group.d + (m - t * (int)a.group.d)) * x.head;
 }
 
 template <int DJ, int MT>
@@ -855,7 +883,7 @@ __device__ __forceinline__ void softmax(const Attention& a, const Plan& p, int s
     if (sole) st.l[mt] += mine;
     if (a.w_out) {
       const int tile = step * ST + g, m_local = mt * 16 + lane % 16;
-      if (sole && tile < p.tiles && m_local < a.unit_rows) {
+      if (sole && tile < p.tiles && m_local < (int)a.unit_rows.d) {
         const float share = base + log2_fast(mine);
         if (a.mass_in_lds)
           mass_lds[m_local * a.cap_tiles + tile] = share;
@@ -890,21 +918,26 @@ __device__ __forceinline__ float log_total(float m, float l) {
   return l == 0.f ? INFINITY : (m == -INFINITY ? 0.f : m) + log2_fast(l);
 }
 
-// The weight that tile `tile` got from a unit's query rows, lse their
-// log_total (+inf for rows that see nothing, whose shares are not written).
-__device__ __forceinline__ float tile_weight(const Attention& a, const float* mass, const float* lse,
-                                             int tile) {
+// The shares that tile `tile` got from eight query rows of a unit, and their sum
+// as weights: lse is the rows' log_total (+inf for rows that see nothing, whose
+// shares are not written).
+struct Shares {
+  float x[8];
+};
+
+__device__ __forceinline__ Shares load_shares(const Attention& a, const float* mass, int m, int tile) {
+  Shares s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    s.x[i] = m + i < (int)a.unit_rows.d ? mass[(uint64_t)(m + i) * a.cap_tiles + tile] : 0.f;
+  return s;
+}
+
+__device__ __forceinline__ float sum_shares(const Attention& a, const Shares& s, const float* lse, int m) {
   float w = 0.f;
-  int m = 0;
-  for (; m + 8 <= a.unit_rows; m += 8) {  // eight loads in flight
-    float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = mass[(uint64_t)(m + i) * a.cap_tiles + tile];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w += lse[m + i] == INFINITY ? 0.f : exp2_fast(x[i] - lse[m + i]);
-  }
-  for (; m < a.unit_rows; ++m)
-    w += lse[m] == INFINITY ? 0.f : exp2_fast(mass[(uint64_t)m * a.cap_tiles + tile] - lse[m]);
+  for (int i = 0; i < 8; ++i)
+    if (m + i < (int)a.unit_rows.d) w += lse[m + i] == INFINITY ? 0.f : exp2_fast(s.x[i] - lse[m + i]);
   return w;
 }
 
@@ -932,10 +965,10 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
   __shared__ float s_lse[MT * 16];
   __shared__ float s_mass[kLdsMass];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const bool direct = a.n_parts == a.n_units && a.m_groups == 1;
+  const bool direct = a.n_parts == a.n_units && a.m_groups.d == 1;
   const Part part = part_of_workgroup<ST>(a, blockIdx.x, lane);
   if (part.idle) return;
-  const uint32_t unit = part.row * (uint32_t)a.m_groups + part.group;
+  const uint32_t unit = part.row * a.m_groups.d + part.group;
   const Plan p = plan_unit<MT, ST>(a, part);
   const int first = part.index * p.part_steps;
   const int last = min(first + p.part_steps, p.steps);
@@ -973,7 +1006,7 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
 #pragma unroll
     for (int i = 0; i < 4 * DJ; ++i) st.o[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  float* mass_row = a.ws_mass + (uint64_t)unit * a.unit_rows * a.cap_tiles;
+  float* mass_row = a.ws_mass + (uint64_t)unit * a.unit_rows.d * a.cap_tiles;
 
   // While a step is computed the next one's tiles are on their way: its keys
   // take the registers of this one's as soon as the scores are done, its
@@ -1034,8 +1067,8 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
       f[w] = exp2_fast(s_ml[w][m_local][0] - base);
       total += s_ml[w][m_local][1] * f[w];
     }
-    const uint64_t slot = (uint64_t)blockIdx.x * a.unit_rows + m_local;
-    const bool here = m_local < a.unit_rows && m < a.m_rows;
+    const uint64_t slot = (uint64_t)blockIdx.x * a.unit_rows.d + m_local;
+    const bool here = m_local < (int)a.unit_rows.d && m < a.m_rows;
     const float share = total == 0.f ? 0.f : 1.f / total;
     const bool any = seen_by(a, p, m) > 0;
     if (d4 == 0) {
@@ -1078,7 +1111,8 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
     const int tile = base + (int)threadIdx.x;
     float w = 0.f;
     if (tile < p.tiles)
-      w = a.mass_in_lds ? tile_weight(a, s_mass, s_lse, tile) : tile_weight(a, mass_row, s_lse, tile);
+      for (int m = 0; m < (int)a.unit_rows.d; m += 8)
+        w += sum_shares(a, load_shares(a, a.mass_in_lds ? s_mass : mass_row, m, tile), s_lse, m);
     write_weight(a, p.row, tile, w);
   }
 }
@@ -1087,26 +1121,22 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
 // and each part's factor, in LDS, where asked for.
 __device__ __forceinline__ float join_parts(const Attention& a, const Part& t, int parts, int m_local,
                                             int lane, float* factors) {
-  f32x2 ml[kMaxParts / kWave];
-  float top = -INFINITY, total = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMaxParts / kWave; ++i) {
-    ml[i] = f32x2{-INFINITY, 0.f};
-    const int n = i * kWave + lane;
-    if (n < parts) ml[i] = a.ws_ml[((uint64_t)t.first + (uint64_t)n * a.m_groups) * a.unit_rows + m_local];
-    top = fmaxf(top, ml[i][0]);
-  }
+  auto part = [&](int n) {
+    return a.ws_ml[((uint64_t)t.first + (uint64_t)n * a.m_groups.d) * a.unit_rows.d + m_local];
+  };
+  const f32x2 mine = lane < parts ? part(lane) : f32x2{-INFINITY, 0.f};
+  float top = mine[0];
+  for (int n = lane + kWave; n < parts; n += kWave) top = fmaxf(top, part(n)[0]);
   top = wave_max(top);
-#pragma unroll
-  for (int i = 0; i < kMaxParts / kWave; ++i) {
-    ml[i][0] = exp2_fast(ml[i][0] - (top == -INFINITY ? 0.f : top));
-    total += ml[i][0] * ml[i][1];
-  }
+  const float base = top == -INFINITY ? 0.f : top;
+  const float f = exp2_fast(mine[0] - base);
+  float total = f * mine[1];
+  for (int n = lane + kWave; n < parts; n += kWave) total += exp2_fast(part(n)[0] - base) * part(n)[1];
   total = wave_sum(total);
   if (factors) {
-#pragma unroll
-    for (int i = 0; i < kMaxParts / kWave; ++i)
-      if (i * kWave < parts) factors[i * kWave + lane] = total == 0.f ? 0.f : ml[i][0] / total;
+    const float share = total == 0.f ? 0.f : 1.f / total;
+    factors[lane] = f * share;
+    for (int n = lane + kWave; n < parts; n += kWave) factors[n] = exp2_fast(part(n)[0] - base) * share;
   }
   return log_total(top, total);
 }
@@ -1119,26 +1149,39 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
   constexpr int ST = step_tiles(DJ, MT);
   constexpr int kVec = D / 4;                 // threads of a row of the output
   constexpr int kGroups = kThreads / kVec;    // parts summed at a time
+  constexpr int kAhead = 4;
   __shared__ __attribute__((aligned(16))) f32x4 s_sum[kGroups][kVec];
   __shared__ float s_f[kMaxParts];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const uint32_t out_blocks = a.n_units * (uint32_t)a.unit_rows;
+  const uint32_t out_blocks = a.n_units * a.unit_rows.d;
   if (blockIdx.x < out_blocks) {
-    const uint32_t unit = blockIdx.x / a.unit_rows;
-    const int m_local = (int)(blockIdx.x % a.unit_rows);
-    const Part t = parts_of_unit(a, unit / a.m_groups, (int)(unit % a.m_groups));
+    const uint32_t unit = quotient(blockIdx.x, a.unit_rows);
+    const int m_local = (int)(blockIdx.x - unit * a.unit_rows.d);
+    const uint32_t row = quotient(unit, a.m_groups);
+    const Part t = parts_of_unit(a, row, (int)(unit - row * a.m_groups.d));
     const Plan p = plan_unit<MT, ST>(a, t);
     const int m = p.m0 + m_local;
     if (m >= a.m_rows) return;
     const int parts = seen_by(a, p, m) > 0 ? p.parts : 0;
+    const int d4 = threadIdx.x % kVec, group = threadIdx.x / kVec;
+    auto sums_of = [&](int n) {
+      return *(const f32x4*)(a.ws_o + (((uint64_t)t.first + (uint64_t)n * a.m_groups.d) * a.unit_rows.d + m_local) * D + 4 * d4);
+    };
+    // the first parts' sums are on their way while the factors are worked out
+    f32x4 o = {0.f, 0.f, 0.f, 0.f}, ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int n = group + i * kGroups;
+      ahead[i] = group < kGroups && n < parts ? sums_of(n) : o;
+    }
     if (wave == 0) (void)join_parts(a, t, parts, m_local, lane, s_f);
     __syncthreads();
-    const int d4 = threadIdx.x % kVec, group = threadIdx.x / kVec;
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
     if (group < kGroups) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (group + i * kGroups < parts) o += ahead[i] * s_f[group + i * kGroups];
 #pragma unroll 4
-      for (int n = group; n < parts; n += kGroups)
-        o += *(const f32x4*)(a.ws_o + (((uint64_t)t.first + (uint64_t)n * a.m_groups) * a.unit_rows + m_local) * D + 4 * d4) * s_f[n];
+      for (int n = group + kAhead * kGroups; n < parts; n += kGroups) o += sums_of(n) * s_f[n];
       s_sum[group][d4] = o;
     }
     __syncthreads();
@@ -1159,20 +1202,25 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
   }
 
   const uint32_t b = blockIdx.x - out_blocks;
-  const uint32_t row = b / a.weight_blocks;
-  const int tile = (int)(b % a.weight_blocks * kThreads + threadIdx.x);
+  const uint32_t row = quotient(b, a.weight_blocks);
+  const int tile = (int)((b - row * a.weight_blocks.d) * kThreads + threadIdx.x);
   float w = 0.f;
-  for (int g = 0; g < a.m_groups; ++g) {
+  for (int g = 0; g < (int)a.m_groups.d; ++g) {
     const Part t = parts_of_unit(a, row, g);
     const Plan p = plan_unit<MT, ST>(a, t);
+    const float* mass = a.ws_mass + ((uint64_t)row * a.m_groups.d + g) * a.unit_rows.d * a.cap_tiles;
+    Shares first;
+    if (tile < p.tiles) first = load_shares(a, mass, 0, tile);
     __syncthreads();
-    for (int m = wave; m < a.unit_rows; m += kWaves) {
+    for (int m = wave; m < (int)a.unit_rows.d; m += kWaves) {
       const float lse = join_parts(a, t, seen_by(a, p, p.m0 + m) > 0 ? p.parts : 0, m, lane, nullptr);
       if (lane == 0) s_f[m] = lse;
     }
     __syncthreads();
-    const uint64_t unit = (uint64_t)row * a.m_groups + g;
-    if (tile < p.tiles) w += tile_weight(a, a.ws_mass + unit * a.unit_rows * a.cap_tiles, s_f, tile);
+    if (tile < p.tiles) {
+      w += sum_shares(a, first, s_f, 0);
+      for (int m = 8; m < (int)a.unit_rows.d; m += 8) w += sum_shares(a, load_shares(a, mass, m, tile), s_f, m);
+    }
   }
   write_weight(a, row, tile, w);
 }
@@ -1224,9 +1272,9 @@ __device__ __forceinline__ Choice choice_of(const Evict& e, uint32_t row) {
 
 // One workgroup per row of up to THREADS * R pages, the weights in LDS.
 // The weight of the last page to stay is found from counts in LDS: the keys
-// between the smallest and the largest are counted in 256 equal ranges, the
-// range that holds the wanted one is cut into 256 again, and so on.  (Bisecting
-// with one count a round takes 25 rounds where this takes 3: 16,384 pages x
+// between the smallest and the largest are counted in 1024 equal ranges, the
+// range that holds the wanted one is cut into 1024 again, and so on.  (Bisecting
+// with one count a round takes 25 rounds where this takes 2 or 3: 16,384 pages x
 // 768 rows spent 47 us on it.)  With the counts of every 64 pages in LDS each
 // page then knows its place.
 template <int THREADS, int R>
@@ -1234,11 +1282,14 @@ __global__ __launch_bounds__(THREADS, 8) void evict_kernel(Evict e) {
   constexpr int kW = THREADS / kWave;
   constexpr int kUnroll = R < 8 ? R : 8;
   constexpr int kChunks = R * kW;  // of 64 pages, chunk i * kW + wave
+  constexpr int kRanges = 1024, kMine = kRanges / kWave;  // of a lane that adds them up
   constexpr uint32_t kStays = 0xFFFFFFFFu;  // above every weight's key; 0 is below
   static_assert(kChunks <= 256, "a wave scans them, four to a lane");
+  static_assert(THREADS > kWave && R <= 32);
   static_assert(THREADS * R < 65536, "two counts to a word");
-  __shared__ uint32_t s_count[2][256];
+  __shared__ __attribute__((aligned(16))) uint32_t s_count[2][kRanges];
   __shared__ uint32_t s_bound[2][kW];
+  __shared__ uint32_t s_pick[3];
   __shared__ uint32_t s_chunk[256];      // pages that stay, and ties in the upper half
   __shared__ uint32_t s_key[R][THREADS];  // a thread reads its own only
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
@@ -1275,16 +1326,13 @@ __global__ __launch_bounds__(THREADS, 8) void evict_kernel(Evict e) {
   }
   uint32_t last = kStays - 1u, ties = 0;  // stay: keys above `last` and the first `ties` equal to it
   if (c.want) {
-#pragma unroll
-    for (int s = 32; s; s >>= 1) {
-      low = min(low, (uint32_t)__shfl_xor((int)low, s));
-      high = max(high, (uint32_t)__shfl_xor((int)high, s));
-    }
+    low = ~wave_max(~low);
+    high = wave_max(high);
     if (lane == 0) {
       s_bound[0][wave] = low;
       s_bound[1][wave] = high;
     }
-    if (threadIdx.x < 256) s_count[0][threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < kRanges; i += THREADS) s_count[0][i] = 0;
     __syncthreads();
 #pragma unroll
     for (int x = 0; x < kW; ++x) {
@@ -1295,47 +1343,65 @@ __global__ __launch_bounds__(THREADS, 8) void evict_kernel(Evict e) {
     high = (uint32_t)uniform((int)high);
     // the key is in low .. high; `over` < want keys are above high
     uint32_t over = 0;
+    uint32_t within = 0;  // which of the thread's keys are, from the second round on
     last = low;
-    for (int round = 0; low < high; round ^= 1) {
-      const int shift = max(24 - (int)__builtin_clz(high - low), 0);
-      uint32_t* count = s_count[round];
-#pragma unroll kUnroll
-      for (int i = 0; i < R; ++i) {
-        const uint32_t above_low = s_key[i][threadIdx.x] - low;
-        if (above_low <= high - low) atomicAdd(&count[above_low >> shift], 1u);
+    for (int round = 0; low < high; ++round) {
+      const int shift = max(22 - (int)__builtin_clz(high - low), 0);
+      uint32_t* count = s_count[round & 1];
+      if (round < 2) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const uint32_t above_low = s_key[i][threadIdx.x] - low;
+          if (above_low <= high - low) {
+            atomicAdd(&count[above_low >> shift], 1u);
+            within |= 1u << i;
+          }
+        }
+        if (round == 0) within = 0;
+      } else {  // few are left
+        for (uint32_t left = within; left; left &= left - 1) {
+          const int i = __builtin_ctz(left);
+          const uint32_t above_low = s_key[i][threadIdx.x] - low;
+          if (above_low <= high - low)
+            atomicAdd(&count[above_low >> shift], 1u);
+          else
+            within &= ~(1u << i);
+        }
       }
       __syncthreads();
-      // every wave reads them all; lane l has ranges 255 - 4 l down to 252 - 4 l
-      uint32_t n[4], mine = 0;
+      if (wave == 0) {
+        // lane l adds up ranges from kMine (63 - l); the lane that holds the
+        // wanted one has its ranges looked at one to a lane
+        uint32_t mine = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) mine += n[i] = count[255 - 4 * lane - i];
-      uint32_t before = over + wave_scan(mine) - mine;
-      uint32_t found = 0, over_found = 0, n_found = 0;
-      bool here = false;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (before < c.want && before + n[i] >= c.want) {
-          here = true;
-          found = 255u - 4u * lane - i;
-          over_found = before;
-          n_found = n[i];
+        for (int i = 0; i < kMine; i += 4) {
+          const u32x4 four = *(const u32x4*)&count[kMine * (kWave - 1 - lane) + i];
+          mine += (four[0] + four[1]) + (four[2] + four[3]);
         }
-        before += n[i];
+        uint32_t before = over + wave_scan(mine) - mine;
+        const int src = __builtin_ctzll(__ballot(before < c.want && before + mine >= c.want));
+        before = (uint32_t)__builtin_amdgcn_readlane((int)before, src);
+        const int range = kMine * (kWave - src) - 1 - lane;
+        const uint32_t n = lane < kMine ? count[range] : 0u;
+        before += wave_scan(n) - n;
+        if (before < c.want && before + n >= c.want) {
+          s_pick[0] = (uint32_t)range;
+          s_pick[1] = before;
+          s_pick[2] = before + n;
+        }
+      } else {
+        for (int i = (int)threadIdx.x - kWave; i < kRanges; i += THREADS - kWave) s_count[(round & 1) ^ 1][i] = 0;
       }
-      const int src = __builtin_ctzll(__ballot(here));
-      found = (uint32_t)__builtin_amdgcn_readlane((int)found, src);
-      over = (uint32_t)__builtin_amdgcn_readlane((int)over_found, src);
-      const bool exact = over + (uint32_t)__builtin_amdgcn_readlane((int)n_found, src) == c.want;
-      low += found << shift;
+      __syncthreads();
+      low += (uint32_t)uniform((int)s_pick[0]) << shift;
+      over = (uint32_t)uniform((int)s_pick[1]);
       if (high - low >= 1u << shift) high = low + ((1u << shift) - 1u);  // no sum past 32 bits
       last = low;
-      if (exact) {  // the whole range stays
+      if ((uint32_t)uniform((int)s_pick[2]) == c.want) {  // the whole range stays
         last = low - 1u;
         over = c.want;
         break;
       }
-      if (threadIdx.x < 256) s_count[round ^ 1][threadIdx.x] = 0;
-      __syncthreads();
     }
     ties = c.want - over;
   }
@@ -1533,12 +1599,19 @@ Pool make_pool(const ibp_kv_cache* c) {
   return p;
 }
 
+Divisor make_divisor(uint32_t d) {
+  Divisor x = {d, 0, 31};
+  while ((1ull << (x.shift - 31)) < d) ++x.shift;
+  x.mul = (uint32_t)(((1ull << x.shift) + d - 1) / std::max<uint32_t>(d, 1));
+  return x;
+}
+
 Rows make_rows(const ibp_kv_table* t, uint32_t page_tokens, uint64_t n_new, const int32_t* counts) {
   Rows r;
   r.pages = t->pages;
   r.lengths = t->lengths;
   r.counts = counts;
-  r.heads = (uint32_t)t->kv_heads;
+  r.heads = make_divisor((uint32_t)t->kv_heads);
   r.max_pages = (uint32_t)t->max_pages;
   r.capacity = (int32_t)(t->max_pages * page_tokens);
   r.n_new = (int32_t)n_new;
@@ -1558,10 +1631,10 @@ Strided make_strided(const ibp_kv_tensor* x) {
 
 template <int DJ, bool F16>
 void launch_append(const Pool& pool, const Rows& rows, const Strided& k, const Strided& v,
-                   uint32_t pages_per_row, uint64_t tasks, hipStream_t st) {
-  const uint64_t per_group = kWaves >> pool.tile_shift;
-  hipLaunchKernelGGL((append_kernel<DJ, F16>), dim3((uint32_t)((tasks + per_group - 1) / per_group)),
-                     dim3(kThreads), 0, st, pool, rows, k, v, pages_per_row, tasks);
+                   uint32_t pages_per_row, uint32_t tasks, hipStream_t st) {
+  const uint32_t per_group = kWaves >> pool.tile_shift;
+  hipLaunchKernelGGL((append_kernel<DJ, F16>), dim3((tasks + per_group - 1) / per_group),
+                     dim3(kThreads), 0, st, pool, rows, k, v, make_divisor(pages_per_row), tasks);
 }
 
 // How the query rows of a head are cut: at most 64 to a unit, 32 where the
@@ -1624,12 +1697,12 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
 
 template <int DJ, bool F16, int MT>
 void launch_attention(const Attention& a, uint64_t n_rows, hipStream_t st) {
-  const bool direct = a.n_parts == a.n_units && a.m_groups == 1;
+  const bool direct = a.n_parts == a.n_units && a.m_groups.d == 1;
   if (a.n_units)
     hipLaunchKernelGGL((attention_kernel<DJ, F16, MT>), dim3(a.n_parts), dim3(kThreads),
                        0, st, a);
   if (direct) return;
-  const uint64_t blocks = (uint64_t)a.n_units * a.unit_rows + (a.w_out ? n_rows * a.weight_blocks : 0);
+  const uint64_t blocks = (uint64_t)a.n_units * a.unit_rows.d + (a.w_out ? n_rows * a.weight_blocks.d : 0);
   if (blocks)
     hipLaunchKernelGGL((combine_kernel<DJ, F16, MT>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a);
 }
@@ -1684,7 +1757,7 @@ int ibp_kv_append(const ibp_kv_cache* cache, const ibp_kv_table* table, uint32_t
   const Rows rows = make_rows(table, cache->page_tokens, n_new, counts);
   const Strided ks = make_strided(k), vs = make_strided(v);
   hipStream_t st = (hipStream_t)stream;
-  const uint64_t tasks = n_rows * per_row;
+  const uint32_t tasks = (uint32_t)(n_rows * per_row);
   switch (cache->head_dim / 64 * 2 + dtype) {
     case 2: launch_append<1, false>(pool, rows, ks, vs, (uint32_t)per_row, tasks, st); break;
     case 3: launch_append<1, true>(pool, rows, ks, vs, (uint32_t)per_row, tasks, st); break;
@@ -1750,16 +1823,16 @@ int ibp_kv_attention(const ibp_kv_cache* cache, const ibp_kv_table* table, uint3
   a.ws_mass = (float*)((char*)workspace + s.mass_at);
   a.ws_of = (int32_t*)((char*)workspace + s.of_at);
   a.scale = scale * 1.44269504088896340736f;
-  a.group = (int32_t)(q_heads / table->kv_heads);
+  a.group = make_divisor((uint32_t)(q_heads / table->kv_heads));
   a.m_rows = s.m_rows;
-  a.m_groups = s.m_groups;
-  a.unit_rows = s.unit_rows;
+  a.m_groups = make_divisor((uint32_t)s.m_groups);
+  a.unit_rows = make_divisor((uint32_t)s.unit_rows);
   a.cap_tiles = s.cap_tiles;
   a.mass_in_lds = s.mass_in_lds;
   a.n_units = s.n_units;
   a.n_rows = (uint32_t)n_rows;
   a.n_parts = s.n_parts;
-  a.weight_blocks = (uint32_t)(s.cap_tiles + kThreads - 1) / kThreads;
+  a.weight_blocks = make_divisor((uint32_t)(s.cap_tiles + kThreads - 1) / kThreads);
   hipStream_t st = (hipStream_t)stream;
   switch (cache->head_dim / 64 * 2 + dtype) {
     case 2: launch_attention_mt<1, false>(a, s.mt, n_rows, st); break;
