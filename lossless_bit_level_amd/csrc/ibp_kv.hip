@@ -19,10 +19,14 @@ constexpr int kTile = 16;       // tokens of a tile
 // ones, whose tiles and accumulators take more registers (64 tokens of 128
 // dims measured the same at 40 registers more).
 constexpr int step_tiles(int dj, int mt) { return dj * mt <= 1 ? 4 : 2; }
+// Workgroups of the attention kernel that a compute unit holds at once: their
+// accumulators, queries and tiles on the way fill the registers.
+constexpr int workgroups_per_unit(int dj, int mt) { return dj * mt <= 4 ? 2 : 1; }
 // The most groups of 16 query rows that a unit takes.
 constexpr int most_query_tiles(int dj) { return dj <= 2 ? 4 : 2; }
 constexpr int kUnit = 1024;     // bytes of a tile that one wide load of a wave takes
 constexpr int kMaxParts = 512;
+constexpr int kFewRows = 16;    // query rows of a unit that one thread adds up for its tile
 constexpr int kLdsMass = 4096;  // shares of tiles that a workgroup that works alone keeps in LDS
 constexpr int kExpMin = -126, kExpMax = 119;  // exponents of a page's scale
 constexpr float kE4m3Max = 448.f;
@@ -551,13 +555,13 @@ struct Plan {
   int part_steps, parts;
 };
 
-constexpr int kRowsPerLane = 4;  // of the rows that share out the workgroups
+constexpr int kRowsPerLane = 6;  // of the rows that share out the workgroups
 
 // Shares the workgroups out: with C = ceil(all steps / (n_parts - n_units)) a
 // row of s steps gets ceil(s / C) workgroups for each of its units, n_parts at
 // most together.  Long rows get more than short ones, so that no workgroup
 // works long after the others.  Every wave works it out from the lengths.
-//   lane l: rows 4 l .. 4 l + 3, `share` workgroups a unit each, `before` those
+//   lane l: rows 6 l .. 6 l + 5, `share` workgroups a unit each, `before` those
 //   of the rows before them.
 template <int ST>
 __device__ __forceinline__ void share_out(const Attention& a, int lane, int (&len)[kRowsPerLane],
@@ -717,7 +721,8 @@ __device__ __forceinline__ Where<ST> find_step(const Attention& a, const Plan& p
 
 // Non-temporal where a unit has all of its head's query rows, so that no other
 // workgroup of the call comes back for the tiles: 16 x 32 heads x 4096 tokens
-// take 88.4 us so (6.1 TB/s), 102.7 us with plain loads.
+// take 85.6 us so (6.3 TB/s), 95.8 us with plain loads.  (By a template: of two
+// branches with one kind each the compiler makes plain loads.)
 template <int DJ, int ST, bool ONCE>
 __device__ __forceinline__ void load_tiles(const uint8_t* codes, const Where<ST>& w, int lane,
                                            u32x4 (&x)[ST][DJ]) {
@@ -918,26 +923,30 @@ __device__ __forceinline__ float log_total(float m, float l) {
   return l == 0.f ? INFINITY : (m == -INFINITY ? 0.f : m) + log2_fast(l);
 }
 
-// The shares that tile `tile` got from eight query rows of a unit, and their sum
-// as weights: lse is the rows' log_total (+inf for rows that see nothing, whose
+// The shares that tile `tile` got from eight query rows of a unit (m, m + stride,
+// ...), and their sum as weights: lse is the rows' log_total (+inf for rows that see nothing, whose
 // shares are not written).
 struct Shares {
   float x[8];
 };
 
-__device__ __forceinline__ Shares load_shares(const Attention& a, const float* mass, int m, int tile) {
+__device__ __forceinline__ Shares load_shares(const Attention& a, const float* mass, int m, int stride,
+                                              int tile) {
   Shares s;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    s.x[i] = m + i < (int)a.unit_rows.d ? mass[(uint64_t)(m + i) * a.cap_tiles + tile] : 0.f;
+    s.x[i] = m + i * stride < (int)a.unit_rows.d ? mass[(uint64_t)(m + i * stride) * a.cap_tiles + tile] : 0.f;
   return s;
 }
 
-__device__ __forceinline__ float sum_shares(const Attention& a, const Shares& s, const float* lse, int m) {
+__device__ __forceinline__ float sum_shares(const Attention& a, const Shares& s, const float* lse, int m,
+                                            int stride) {
   float w = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (m + i < (int)a.unit_rows.d) w += lse[m + i] == INFINITY ? 0.f : exp2_fast(s.x[i] - lse[m + i]);
+  for (int i = 0; i < 8; ++i) {
+    const int row = m + i * stride;
+    if (row < (int)a.unit_rows.d) w += lse[row] == INFINITY ? 0.f : exp2_fast(s.x[i] - lse[row]);
+  }
   return w;
 }
 
@@ -954,11 +963,11 @@ __device__ __forceinline__ void write_weight(const Attention& a, uint32_t row, i
 // A workgroup takes one part of one unit; its waves take steps in turn and
 // join at the end.  With one part and one unit a row the result is written
 // here, else it is left in the workspace for the combining kernel.
-template <int DJ, bool F16, int MT>
-__global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kernel(Attention a) {
+// ONCE: the unit has all query rows of its head.
+template <int DJ, bool F16, int MT, bool ONCE>
+__global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, MT)) void attention_kernel(Attention a) {
   constexpr int D = 64 * DJ;
   constexpr int ST = step_tiles(DJ, MT);
-  constexpr bool kOnce = MT < most_query_tiles(DJ);
   constexpr int kPitch = 64 + 4;  // floats of a query row of 64 dims in LDS
   __shared__ __attribute__((aligned(16))) float s_o[kWaves][16][kPitch];
   __shared__ f32x2 s_ml[kWaves][MT * 16];
@@ -1015,15 +1024,15 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
   if (step < last) {
     u32x4 k[ST][DJ], v[ST][DJ];
     Where<ST> here = find_step<DJ, ST>(a, p, step);
-    load_tiles<DJ, ST, kOnce>(a.pool.k_codes, here, lane, k);
-    load_tiles<DJ, ST, kOnce>(a.pool.v_codes, here, lane, v);
+    load_tiles<DJ, ST, ONCE>(a.pool.k_codes, here, lane, k);
+    load_tiles<DJ, ST, ONCE>(a.pool.v_codes, here, lane, v);
     while (true) {
       const int next_step = step + kWaves;
       const bool more = next_step < last;
       Where<ST> next = find_step<DJ, ST>(a, p, more ? next_step : step);
       f32x4 s[MT][ST];
       scores<DJ, F16, MT, ST>(k, q, s);
-      if (more) load_tiles<DJ, ST, kOnce>(a.pool.k_codes, next, lane, k);
+      if (more) load_tiles<DJ, ST, ONCE>(a.pool.k_codes, next, lane, k);
       bool plain = (step + 1) * (kTile * ST) <= p.full;
 #pragma unroll
       for (int t = 0; t < ST; ++t) plain = plain && here.ok[t];
@@ -1038,7 +1047,7 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
       softmax<DJ, MT, ST>(a, p, step, lane, here, s, mass_row, s_mass, st, pr);
       gather_values<DJ, MT, ST>(v, pr, st);
       if (!more) break;
-      load_tiles<DJ, ST, kOnce>(a.pool.v_codes, next, lane, v);
+      load_tiles<DJ, ST, ONCE>(a.pool.v_codes, next, lane, v);
       here = next;
       step = next_step;
     }
@@ -1112,15 +1121,15 @@ __global__ __launch_bounds__(kThreads, MT * DJ <= 4 ? 2 : 1) void attention_kern
     float w = 0.f;
     if (tile < p.tiles)
       for (int m = 0; m < (int)a.unit_rows.d; m += 8)
-        w += sum_shares(a, load_shares(a, a.mass_in_lds ? s_mass : mass_row, m, tile), s_lse, m);
+        w += sum_shares(a, load_shares(a, a.mass_in_lds ? s_mass : mass_row, m, 1, tile), s_lse, m, 1);
     write_weight(a, p.row, tile, w);
   }
 }
 
-// Maximum and sum of a query row over the parts of its unit (up to kMaxParts),
-// and each part's factor, in LDS, where asked for.
-__device__ __forceinline__ float join_parts(const Attention& a, const Part& t, int parts, int m_local,
-                                            int lane, float* factors) {
+// The factors, in LDS, that the sums of a unit's parts (up to kMaxParts) take for
+// a query row.
+__device__ __forceinline__ void join_parts(const Attention& a, const Part& t, int parts, int m_local,
+                                           int lane, float* factors) {
   auto part = [&](int n) {
     return a.ws_ml[((uint64_t)t.first + (uint64_t)n * a.m_groups.d) * a.unit_rows.d + m_local];
   };
@@ -1133,16 +1142,13 @@ __device__ __forceinline__ float join_parts(const Attention& a, const Part& t, i
   float total = f * mine[1];
   for (int n = lane + kWave; n < parts; n += kWave) total += exp2_fast(part(n)[0] - base) * part(n)[1];
   total = wave_sum(total);
-  if (factors) {
-    const float share = total == 0.f ? 0.f : 1.f / total;
-    factors[lane] = f * share;
-    for (int n = lane + kWave; n < parts; n += kWave) factors[n] = exp2_fast(part(n)[0] - base) * share;
-  }
-  return log_total(top, total);
+  const float share = total == 0.f ? 0.f : 1.f / total;
+  factors[lane] = f * share;
+  for (int n = lane + kWave; n < parts; n += kWave) factors[n] = exp2_fast(part(n)[0] - base) * share;
 }
 
 // Joins the parts.  Workgroups below n_units * unit_rows take one query row
-// each; the others take 256 tiles of a row each and sum their weights.
+// each; the others take 256 or 64 tiles of a row each and sum their weights.
 template <int DJ, bool F16, int MT>
 __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
   constexpr int D = 64 * DJ;
@@ -1174,7 +1180,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
       const int n = group + i * kGroups;
       ahead[i] = group < kGroups && n < parts ? sums_of(n) : o;
     }
-    if (wave == 0) (void)join_parts(a, t, parts, m_local, lane, s_f);
+    if (wave == 0) join_parts(a, t, parts, m_local, lane, s_f);
     __syncthreads();
     if (group < kGroups) {
 #pragma unroll
@@ -1201,27 +1207,55 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
     return;
   }
 
+  // With few query rows 256 tiles, each thread with all rows of its tile; with
+  // many 64, wave w with rows w, w + 4, ..
   const uint32_t b = blockIdx.x - out_blocks;
   const uint32_t row = quotient(b, a.weight_blocks);
-  const int tile = (int)((b - row * a.weight_blocks.d) * kThreads + threadIdx.x);
+  const int stride = a.unit_rows.d > kFewRows ? kWaves : 1, start = stride == 1 ? 0 : wave;
+  const int tile = (int)((b - row * a.weight_blocks.d) * (kThreads / stride)) +
+                   (stride == 1 ? (int)threadIdx.x : lane);
+  int spread = 1;  // lanes that hold a query row each; the others share its parts
+  while (spread * kWaves < (int)a.unit_rows.d) spread *= 2;
   float w = 0.f;
   for (int g = 0; g < (int)a.m_groups.d; ++g) {
     const Part t = parts_of_unit(a, row, g);
     const Plan p = plan_unit<MT, ST>(a, t);
     const float* mass = a.ws_mass + ((uint64_t)row * a.m_groups.d + g) * a.unit_rows.d * a.cap_tiles;
     Shares first;
-    if (tile < p.tiles) first = load_shares(a, mass, 0, tile);
-    __syncthreads();
-    for (int m = wave; m < (int)a.unit_rows.d; m += kWaves) {
-      const float lse = join_parts(a, t, seen_by(a, p, p.m0 + m) > 0 ? p.parts : 0, m, lane, nullptr);
-      if (lane == 0) s_f[m] = lse;
+    if (tile < p.tiles) first = load_shares(a, mass, start, stride, tile);
+    const int m = lane % spread * kWaves + wave;
+    float top = -INFINITY, total = 0.f;
+    if (m < (int)a.unit_rows.d && seen_by(a, p, p.m0 + m) > 0) {
+#pragma unroll 4
+      for (int n = lane / spread; n < p.parts; n += kWave / spread) {
+        const f32x2 ml = a.ws_ml[((uint64_t)t.first + (uint64_t)n * a.m_groups.d) * a.unit_rows.d + m];
+        const float higher = fmaxf(top, ml[0]), base = higher == -INFINITY ? 0.f : higher;
+        total = total * exp2_fast(top - base) + ml[1] * exp2_fast(ml[0] - base);
+        top = higher;
+      }
     }
+    for (int x = spread; x < kWave; x *= 2) {
+      const float other = __shfl_xor(top, x), rest = __shfl_xor(total, x);
+      const float higher = fmaxf(top, other), base = higher == -INFINITY ? 0.f : higher;
+      total = total * exp2_fast(top - base) + rest * exp2_fast(other - base);
+      top = higher;
+    }
+    if (lane < spread) s_f[m] = log_total(top, total);
     __syncthreads();
     if (tile < p.tiles) {
-      w += sum_shares(a, first, s_f, 0);
-      for (int m = 8; m < (int)a.unit_rows.d; m += 8) w += sum_shares(a, load_shares(a, mass, m, tile), s_f, m);
+      w += sum_shares(a, first, s_f, start, stride);
+      for (int i = start + 8 * stride; i < (int)a.unit_rows.d; i += 8 * stride)
+        w += sum_shares(a, load_shares(a, mass, i, stride, tile), s_f, i, stride);
     }
+    __syncthreads();
   }
+  if (stride == 1) return write_weight(a, row, tile, w);
+  float* sums = (float*)s_sum;
+  sums[threadIdx.x] = w;
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i) w += sums[i * kWave + lane];
   write_weight(a, row, tile, w);
 }
 
@@ -1673,15 +1707,15 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
   const uint64_t units = n_rows * s->m_groups;
   if (units > kMaxGrid / 64) return false;
   s->n_units = (uint32_t)units;
-  // As many parts as keep all workgroups on the chip at once, two to a compute
-  // unit: what comes after them would start over with an empty pipeline.  Rows
+  // As many parts as keep all workgroups on the chip at once: what comes after them would start over with an empty pipeline.  Rows
   // of up to four steps a wave are not worth the second launch, which costs
-  // about as much as those, and units that fill half the chip are not cut.
+  // about as much as those.  Units that nearly fill the chip are not cut either:
+  // 264 ragged rows of up to 4538 tokens took 48.8 us whole.
   const int st = step_tiles((int)head_dim / 64, s->mt);
   const uint64_t steps = (uint64_t)(s->cap_tiles + st - 1) / st;
-  const uint64_t slots = std::min<uint64_t>(2ull * cus, kMaxParts);
+  const uint64_t slots = std::min<uint64_t>((uint64_t)workgroups_per_unit((int)head_dim / 64, s->mt) * cus, kMaxParts);
   s->n_parts = s->n_units;
-  if (units && units <= slots / 2 && n_rows <= (uint64_t)kWave * kRowsPerLane && steps > 4 * kWaves &&
+  if (units && units <= slots / 4 * 3 && n_rows <= (uint64_t)kWave * kRowsPerLane && steps > 4 * kWaves &&
       steps * units < (1ull << 31))  // the sums of share_out
     s->n_parts = (uint32_t)std::min<uint64_t>(slots, units * ((steps + kWaves - 1) / kWaves + 1));
   const bool direct = s->n_parts == s->n_units && s->m_groups <= 1;
@@ -1691,16 +1725,20 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
   s->mass_at = (s->of_at + (s->n_parts != s->n_units ? units * 8 : 0) + 15) / 16 * 16;
   s->mass_in_lds = direct && (uint64_t)s->unit_rows * s->cap_tiles <= (uint64_t)kLdsMass;
   s->bytes = s->mass_at + (weights && !s->mass_in_lds ? units * s->unit_rows * s->cap_tiles * 4 : 0);
-  if (units * s->unit_rows > kMaxGrid / 2) return false;
+  if (units * s->unit_rows > kMaxGrid / 2 ||
+      (weights && n_rows * (((uint64_t)s->cap_tiles + kWave - 1) / kWave) > kMaxGrid / 2))
+    return false;
   return true;
 }
 
 template <int DJ, bool F16, int MT>
 void launch_attention(const Attention& a, uint64_t n_rows, hipStream_t st) {
   const bool direct = a.n_parts == a.n_units && a.m_groups.d == 1;
-  if (a.n_units)
-    hipLaunchKernelGGL((attention_kernel<DJ, F16, MT>), dim3(a.n_parts), dim3(kThreads),
-                       0, st, a);
+  if (a.n_units && a.m_groups.d == 1)
+    hipLaunchKernelGGL((attention_kernel<DJ, F16, MT, true>), dim3(a.n_parts), dim3(kThreads), 0, st, a);
+  if constexpr (MT == most_query_tiles(DJ))  // only such units are one of several
+    if (a.m_groups.d > 1)
+      hipLaunchKernelGGL((attention_kernel<DJ, F16, MT, false>), dim3(a.n_parts), dim3(kThreads), 0, st, a);
   if (direct) return;
   const uint64_t blocks = (uint64_t)a.n_units * a.unit_rows.d + (a.w_out ? n_rows * a.weight_blocks.d : 0);
   if (blocks)
@@ -1832,7 +1870,8 @@ int ibp_kv_attention(const ibp_kv_cache* cache, const ibp_kv_table* table, uint3
   a.n_units = s.n_units;
   a.n_rows = (uint32_t)n_rows;
   a.n_parts = s.n_parts;
-  a.weight_blocks = make_divisor((uint32_t)(s.cap_tiles + kThreads - 1) / kThreads);
+  const uint32_t block_tiles = s.unit_rows > kFewRows ? kWave : kThreads;
+  a.weight_blocks = make_divisor(((uint32_t)s.cap_tiles + block_tiles - 1) / block_tiles);
   hipStream_t st = (hipStream_t)stream;
   switch (cache->head_dim / 64 * 2 + dtype) {
     case 2: launch_attention_mt<1, false>(a, s.mt, n_rows, st); break;
