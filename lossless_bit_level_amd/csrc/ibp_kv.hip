@@ -525,6 +525,7 @@ struct Attention {
   Divisor unit_rows;   // query rows of a unit
   int32_t m_rows;      // group * n_new: query rows of a key/value head
   int32_t cap_tiles;
+  uint32_t wave_rows;    // the joining kernel has a query row for each wave
   uint32_t mass_in_lds;  // the unit's shares fit kLdsMass, and no other workgroup needs them
   uint32_t n_units;
   uint32_t n_rows;
@@ -1147,8 +1148,9 @@ __device__ __forceinline__ void join_parts(const Attention& a, const Part& t, in
   for (int n = lane + kWave; n < parts; n += kWave) factors[n] = exp2_fast(part(n)[0] - base) * share;
 }
 
-// Joins the parts.  Workgroups below n_units * unit_rows take one query row
-// each; the others take 256 or 64 tiles of a row each and sum their weights.
+// Joins the parts.  The first workgroups take a query row each, or one for each
+// of their waves where the units have few parts on average (264 units x 14 rows
+// in 2 parts: 11.4 us by workgroups); the others take 256 or 64 tiles of a row each and sum their weights.
 template <int DJ, bool F16, int MT>
 __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
   constexpr int D = 64 * DJ;
@@ -1157,9 +1159,38 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
   constexpr int kGroups = kThreads / kVec;    // parts summed at a time
   constexpr int kAhead = 4;
   __shared__ __attribute__((aligned(16))) f32x4 s_sum[kGroups][kVec];
-  __shared__ float s_f[kMaxParts];
+  __shared__ float s_f[kWaves][kMaxParts];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const uint32_t out_blocks = a.n_units * a.unit_rows.d;
+  const uint32_t out_rows = a.n_units * a.unit_rows.d;
+  const uint32_t out_blocks = a.wave_rows ? (out_rows + kWaves - 1) / kWaves : out_rows;
+  if (blockIdx.x < out_blocks && a.wave_rows) {
+    const uint32_t x = blockIdx.x * kWaves + wave, unit = quotient(x, a.unit_rows);
+    if (x >= out_rows) return;
+    const int m_local = (int)(x - unit * a.unit_rows.d);
+    const uint32_t row = quotient(unit, a.m_groups);
+    const Part t = parts_of_unit(a, row, (int)(unit - row * a.m_groups.d));
+    const Plan p = plan_unit<MT, ST>(a, t);
+    const int m = p.m0 + m_local;
+    if (m >= a.m_rows) return;
+    const int parts = seen_by(a, p, m) > 0 ? p.parts : 0;
+    join_parts(a, t, parts, m_local, lane, s_f[wave]);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    float o[DJ];  // dims 64 j + lane
+#pragma unroll
+    for (int j = 0; j < DJ; ++j) o[j] = 0.f;
+#pragma unroll 4
+    for (int n = 0; n < parts; ++n) {
+      const float* sums = a.ws_o + (((uint64_t)t.first + (uint64_t)n * a.m_groups.d) * a.unit_rows.d + m_local) * D;
+      const float f = s_f[wave][n];
+#pragma unroll
+      for (int j = 0; j < DJ; ++j) o[j] += sums[64 * j + lane] * f;
+    }
+    uint16_t* dst = row_of(a.out, a, p, m);
+#pragma unroll
+    for (int j = 0; j < DJ; ++j) dst[64 * j + lane] = to_half<F16>(o[j]);
+    return;
+  }
   if (blockIdx.x < out_blocks) {
     const uint32_t unit = quotient(blockIdx.x, a.unit_rows);
     const int m_local = (int)(blockIdx.x - unit * a.unit_rows.d);
@@ -1180,14 +1211,14 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
       const int n = group + i * kGroups;
       ahead[i] = group < kGroups && n < parts ? sums_of(n) : o;
     }
-    if (wave == 0) join_parts(a, t, parts, m_local, lane, s_f);
+    if (wave == 0) join_parts(a, t, parts, m_local, lane, s_f[0]);
     __syncthreads();
     if (group < kGroups) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
-        if (group + i * kGroups < parts) o += ahead[i] * s_f[group + i * kGroups];
+        if (group + i * kGroups < parts) o += ahead[i] * s_f[0][group + i * kGroups];
 #pragma unroll 4
-      for (int n = group + kAhead * kGroups; n < parts; n += kGroups) o += sums_of(n) * s_f[n];
+      for (int n = group + kAhead * kGroups; n < parts; n += kGroups) o += sums_of(n) * s_f[0][n];
       s_sum[group][d4] = o;
     }
     __syncthreads();
@@ -1240,12 +1271,12 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
       total = total * exp2_fast(top - base) + rest * exp2_fast(other - base);
       top = higher;
     }
-    if (lane < spread) s_f[m] = log_total(top, total);
+    if (lane < spread) s_f[0][m] = log_total(top, total);
     __syncthreads();
     if (tile < p.tiles) {
-      w += sum_shares(a, first, s_f, start, stride);
+      w += sum_shares(a, first, s_f[0], start, stride);
       for (int i = start + 8 * stride; i < (int)a.unit_rows.d; i += 8 * stride)
-        w += sum_shares(a, load_shares(a, mass, i, stride, tile), s_f, i, stride);
+        w += sum_shares(a, load_shares(a, mass, i, stride, tile), s_f[0], i, stride);
     }
     __syncthreads();
   }
@@ -1740,7 +1771,8 @@ void launch_attention(const Attention& a, uint64_t n_rows, hipStream_t st) {
     if (a.m_groups.d > 1)
       hipLaunchKernelGGL((attention_kernel<DJ, F16, MT, false>), dim3(a.n_parts), dim3(kThreads), 0, st, a);
   if (direct) return;
-  const uint64_t blocks = (uint64_t)a.n_units * a.unit_rows.d + (a.w_out ? n_rows * a.weight_blocks.d : 0);
+  const uint64_t out_rows = (uint64_t)a.n_units * a.unit_rows.d;
+  const uint64_t blocks = (a.wave_rows ? (out_rows + kWaves - 1) / kWaves : out_rows) + (a.w_out ? n_rows * a.weight_blocks.d : 0);
   if (blocks)
     hipLaunchKernelGGL((combine_kernel<DJ, F16, MT>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a);
 }
@@ -1867,6 +1899,7 @@ int ibp_kv_attention(const ibp_kv_cache* cache, const ibp_kv_table* table, uint3
   a.unit_rows = make_divisor((uint32_t)s.unit_rows);
   a.cap_tiles = s.cap_tiles;
   a.mass_in_lds = s.mass_in_lds;
+  a.wave_rows = s.n_parts <= 8ull * s.n_units;
   a.n_units = s.n_units;
   a.n_rows = (uint32_t)n_rows;
   a.n_parts = s.n_parts;
