@@ -22,9 +22,13 @@ constexpr int step_tiles(int dj, int mt) { return dj * mt <= 1 ? 4 : 2; }
 // Workgroups of the attention kernel that a compute unit holds at once: their
 // accumulators, queries and tiles on the way fill the registers.
 constexpr int workgroups_per_unit(int dj, int mt) { return dj * mt <= 4 ? 2 : 1; }
-// The most groups of 16 query rows that a unit takes.
-constexpr int most_query_tiles(int dj) { return dj <= 2 ? 4 : 2; }
+// The most groups of 16 query rows that a unit takes.  128 dims, 64 query rows, 4
+// x 8 heads x 14,000 tokens: 55 us as two units of 32, 71 us as one of 64 (both
+// launches); 64 dims: 43 and 46 us; 256 dims, 24 rows: 44 us as one unit, 56 us
+// as two of 16.
+constexpr int kQueryTiles = 2;
 constexpr int kUnit = 1024;     // bytes of a tile that one wide load of a wave takes
+constexpr float kGrowth = 8.f;
 constexpr int kMaxParts = 512;
 constexpr int kFewRows = 16;    // query rows of a unit that one thread adds up for its tile
 constexpr int kLdsMass = 4096;  // shares of tiles that a workgroup that works alone keeps in LDS
@@ -682,7 +686,7 @@ __device__ __forceinline__ uint16_t* row_of(const Strided& x, const Attention& a
 template <int DJ, int MT>
 struct State {
   f32x4 o[MT][4 * DJ];  // o[h * 4 + c][r]: dim 64 h + 16 c + 4 (lane / 16) + r of query lane % 16
-  float m[MT];          // running maximum (log2) of query lane % 16
+  float m[MT];          // about the maximum so far (log2) of query lane % 16: what its sums are scaled by
   float l[MT];          // the lane's part of the running sum
 };
 
@@ -693,8 +697,24 @@ __device__ __forceinline__ T scalar(const T* p) {
   return *(const __attribute__((address_space(4))) T*)p;
 }
 
-// The pages of a step's tiles.  Tiles that are holes or past the row's end
-// have `ok` unset and the id of a page that can be read all the same.
+// The page ids of a step's tiles; of tiles past the row's end the last one's.
+template <int ST>
+struct Ids {
+  uint32_t id[ST];
+};
+
+template <int ST>
+__device__ __forceinline__ Ids<ST> ids_of_step(const Attention& a, const Plan& p, int step) {
+  const int32_t* pages = a.rows.pages + (uint64_t)p.row * a.rows.max_pages;
+  Ids<ST> x;
+#pragma unroll
+  for (int t = 0; t < ST; ++t)
+    x.id[t] = (uint32_t)scalar(pages + (min(step * ST + t, p.tiles - 1) >> a.pool.tile_shift));
+  return x;
+}
+
+// Where a step's tiles are.  Tiles that are holes or past the row's end have `ok`
+// unset and the place of a page that can be read all the same.
 template <int ST>
 struct Where {
   uint64_t at[ST];  // byte of the tile in the pool
@@ -703,15 +723,15 @@ struct Where {
 };
 
 template <int DJ, int ST>
-__device__ __forceinline__ Where<ST> find_step(const Attention& a, const Plan& p, int step) {
-  const int32_t* pages = a.rows.pages + (uint64_t)p.row * a.rows.max_pages;
+__device__ __forceinline__ Where<ST> find_step(const Attention& a, const Plan& p, int step,
+                                               const Ids<ST>& ids) {
   Where<ST> w;
 #pragma unroll
   for (int t = 0; t < ST; ++t) {
     const int tile = step * ST + t, there = min(tile, p.tiles - 1);
-    const uint32_t id = (uint32_t)scalar(pages + (there >> a.pool.tile_shift));
-    w.ok[t] = id < a.pool.n_pages && tile < p.tiles;
-    const uint32_t page = id < a.pool.n_pages ? id : 0u;
+    const bool in = ids.id[t] < a.pool.n_pages;
+    w.ok[t] = in && tile < p.tiles;
+    const uint32_t page = in ? ids.id[t] : 0u;
     w.at[t] = (uint64_t)page * a.pool.page_bytes +
               (uint32_t)((there & ((1 << a.pool.tile_shift) - 1)) * (DJ * kUnit));
     w.ks[t] = scalar(a.pool.k_scales + page);
@@ -720,18 +740,27 @@ __device__ __forceinline__ Where<ST> find_step(const Attention& a, const Plan& p
   return w;
 }
 
+// Scalar loads return in no order, so that a wait for one is a wait for all.
+// This makes it here, for what was asked for a step ago, before more is.
+template <int ST>
+__device__ __forceinline__ void arrive(const Where<ST>& w, const Ids<ST>& ids) {
+#pragma unroll
+  for (int t = 0; t < ST; ++t) asm volatile("" ::"s"(w.ks[t]), "s"(w.vs[t]), "s"(ids.id[t]));
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // Non-temporal where a unit has all of its head's query rows, so that no other
 // workgroup of the call comes back for the tiles: 16 x 32 heads x 4096 tokens
 // take 85.6 us so (6.3 TB/s), 95.8 us with plain loads.  (By a template: of two
 // branches with one kind each the compiler makes plain loads.)
 template <int DJ, int ST, bool ONCE>
-__device__ __forceinline__ void load_tiles(const uint8_t* codes, const Where<ST>& w, int lane,
+__device__ __forceinline__ void load_tiles(const uint8_t* codes, const Where<ST>& w, int byte,
                                            u32x4 (&x)[ST][DJ]) {
 #pragma unroll
   for (int t = 0; t < ST; ++t)
 #pragma unroll
     for (int j = 0; j < DJ; ++j) {
-      const u32x4* p = (const u32x4*)(codes + w.at[t] + j * kUnit + lane * 16);
+      const u32x4* p = (const u32x4*)(codes + w.at[t] + j * kUnit + byte);
       if constexpr (ONCE)
         x[t][j] = __builtin_nontemporal_load(p);
       else
@@ -854,7 +883,9 @@ __device__ __forceinline__ void softmax(const Attention& a, const Plan& p, int s
     for (int t = 0; t < ST; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) top = fmaxf(top, s[mt][t][r]);
-    if (__ballot(top > st.m[mt])) {  // a new maximum for some query, which is rare after some steps
+    // Exponentials may grow to 2^kGrowth before the sums are brought to a new
+    // maximum: with 16 queries to a wave one of them has a new one at most steps.
+    if (__ballot(top > st.m[mt] + kGrowth)) {
       const float m = fmaxf(st.m[mt], query_max(top));
       const float keep = exp2_fast(st.m[mt] - (m == -INFINITY ? 0.f : m));
       st.m[mt] = m;
@@ -1018,22 +1049,28 @@ __global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, MT)) void attenti
   }
   float* mass_row = a.ws_mass + (uint64_t)unit * a.unit_rows.d * a.cap_tiles;
 
-  // While a step is computed the next one's tiles are on their way: its keys
-  // take the registers of this one's as soon as the scores are done, its
-  // values once they have been summed.
+  // While a step is computed the next one's tiles are on their way, and the page
+  // ids of the one after: its keys take the registers of this one's as soon as
+  // the scores are done, its values once they have been summed.  The loads are
+  // made at the last step too, of one 16 bytes by all lanes: with a branch about
+  // them the compiler's wait for the values would be one for the next keys too.
   int step = first + wave;
   if (step < last) {
     u32x4 k[ST][DJ], v[ST][DJ];
-    Where<ST> here = find_step<DJ, ST>(a, p, step);
-    load_tiles<DJ, ST, ONCE>(a.pool.k_codes, here, lane, k);
-    load_tiles<DJ, ST, ONCE>(a.pool.v_codes, here, lane, v);
+    Where<ST> here = find_step<DJ, ST>(a, p, step, ids_of_step<ST>(a, p, step));
+    Ids<ST> ids = ids_of_step<ST>(a, p, min(step + kWaves, last - 1));
+    load_tiles<DJ, ST, ONCE>(a.pool.k_codes, here, lane * 16, k);
+    load_tiles<DJ, ST, ONCE>(a.pool.v_codes, here, lane * 16, v);
     while (true) {
       const int next_step = step + kWaves;
       const bool more = next_step < last;
-      Where<ST> next = find_step<DJ, ST>(a, p, more ? next_step : step);
+      const int byte = more ? lane * 16 : 0;
+      arrive<ST>(here, ids);
+      Where<ST> next = find_step<DJ, ST>(a, p, more ? next_step : step, ids);
+      ids = ids_of_step<ST>(a, p, min(next_step + kWaves, last - 1));
       f32x4 s[MT][ST];
       scores<DJ, F16, MT, ST>(k, q, s);
-      if (more) load_tiles<DJ, ST, ONCE>(a.pool.k_codes, next, lane, k);
+      load_tiles<DJ, ST, ONCE>(a.pool.k_codes, next, byte, k);
       bool plain = (step + 1) * (kTile * ST) <= p.full;
 #pragma unroll
       for (int t = 0; t < ST; ++t) plain = plain && here.ok[t];
@@ -1047,8 +1084,8 @@ __global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, MT)) void attenti
       Probs<MT, ST> pr;
       softmax<DJ, MT, ST>(a, p, step, lane, here, s, mass_row, s_mass, st, pr);
       gather_values<DJ, MT, ST>(v, pr, st);
+      load_tiles<DJ, ST, ONCE>(a.pool.v_codes, next, byte, v);
       if (!more) break;
-      load_tiles<DJ, ST, ONCE>(a.pool.v_codes, next, lane, v);
       here = next;
       step = next_step;
     }
@@ -1702,8 +1739,7 @@ void launch_append(const Pool& pool, const Rows& rows, const Strided& k, const S
                      dim3(kThreads), 0, st, pool, rows, k, v, make_divisor(pages_per_row), tasks);
 }
 
-// How the query rows of a head are cut: at most 64 to a unit, 32 where the
-// accumulators of wide heads would not fit the registers.
+// How the query rows of a head are cut into units, and the units into parts.
 struct Shape {
   int mt;
   int32_t m_rows, m_groups, unit_rows, cap_tiles;
@@ -1730,7 +1766,7 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
   if (n_new && group > (1ull << 24) / n_new) return false;
   const uint64_t m = group * n_new;
   s->m_rows = (int32_t)m;
-  s->mt = m <= 16 ? 1 : m <= 32 ? 2 : most_query_tiles((int)head_dim / 64);
+  s->mt = m <= 16 ? 1 : kQueryTiles;
   const uint64_t per_unit = 16ull * s->mt;
   s->m_groups = (int32_t)((m + per_unit - 1) / per_unit);
   s->unit_rows = (int32_t)std::min<uint64_t>(m, per_unit);
@@ -1767,7 +1803,7 @@ void launch_attention(const Attention& a, uint64_t n_rows, hipStream_t st) {
   const bool direct = a.n_parts == a.n_units && a.m_groups.d == 1;
   if (a.n_units && a.m_groups.d == 1)
     hipLaunchKernelGGL((attention_kernel<DJ, F16, MT, true>), dim3(a.n_parts), dim3(kThreads), 0, st, a);
-  if constexpr (MT == most_query_tiles(DJ))  // only such units are one of several
+  if constexpr (MT == kQueryTiles)  // only such units are one of several
     if (a.m_groups.d > 1)
       hipLaunchKernelGGL((attention_kernel<DJ, F16, MT, false>), dim3(a.n_parts), dim3(kThreads), 0, st, a);
   if (direct) return;
@@ -1780,8 +1816,7 @@ void launch_attention(const Attention& a, uint64_t n_rows, hipStream_t st) {
 template <int DJ, bool F16>
 void launch_attention_mt(const Attention& a, int mt, uint64_t n_rows, hipStream_t st) {
   if (mt == 1) return launch_attention<DJ, F16, 1>(a, n_rows, st);
-  if (DJ > 2 || mt == 2) return launch_attention<DJ, F16, 2>(a, n_rows, st);
-  if constexpr (DJ <= 2) launch_attention<DJ, F16, 4>(a, n_rows, st);
+  launch_attention<DJ, F16, kQueryTiles>(a, n_rows, st);
 }
 
 bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
