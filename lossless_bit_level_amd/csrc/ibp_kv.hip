@@ -544,6 +544,7 @@ struct Part {
   int group;       // of the head's query rows
   int index, of;   // the unit is cut into `of` parts
   uint32_t first;  // part 0 of the unit; the next ones are m_groups apart
+  uint32_t slot;   // this part
   bool idle;
 };
 
@@ -592,17 +593,34 @@ __device__ __forceinline__ void share_out(const Attention& a, int lane, int (&le
   before = (int)wave_scan((uint32_t)mine) - mine;
 }
 
+// Workgroups go to the 8 XCDs in turn, each with an L2 of its own: the units of a
+// head that read the same tiles are 8 workgroups apart.
+constexpr uint32_t kXcds = 8;
+
 template <int ST>
 __device__ __forceinline__ Part part_of_workgroup(const Attention& a, uint32_t w, int lane) {
   Part t;
-  const uint32_t x = quotient(w, a.m_groups);
-  t.group = (int)(w - x * a.m_groups.d);
+  uint32_t x = w;
+  t.group = 0;
+  if (a.m_groups.d > 1) {
+    const uint32_t n = a.n_parts / a.m_groups.d, even = n / kXcds * kXcds;
+    if (w < even * a.m_groups.d) {
+      const uint32_t turn = w / kXcds, y = quotient(turn, a.m_groups);
+      t.group = (int)(turn - y * a.m_groups.d);
+      x = y * kXcds + w % kXcds;
+    } else {
+      const uint32_t rest = w - even * a.m_groups.d, y = quotient(rest, a.m_groups);
+      t.group = (int)(rest - y * a.m_groups.d);
+      x = even + y;
+    }
+  }
+  t.slot = x * a.m_groups.d + t.group;
   if (a.n_parts == a.n_units) {
     t.row = x;
     t.len = row_length(a.rows, x);
     t.index = 0;
     t.of = 1;
-    t.first = w;
+    t.first = t.slot;
     t.idle = false;
     return t;
   }
@@ -1114,7 +1132,7 @@ __global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, MT)) void attenti
       f[w] = exp2_fast(s_ml[w][m_local][0] - base);
       total += s_ml[w][m_local][1] * f[w];
     }
-    const uint64_t slot = (uint64_t)blockIdx.x * a.unit_rows.d + m_local;
+    const uint64_t slot = (uint64_t)part.slot * a.unit_rows.d + m_local;
     const bool here = m_local < (int)a.unit_rows.d && m < a.m_rows;
     const float share = total == 0.f ? 0.f : 1.f / total;
     const bool any = seen_by(a, p, m) > 0;
@@ -1784,7 +1802,8 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
   s->n_parts = s->n_units;
   if (units && units <= slots / 4 * 3 && n_rows <= (uint64_t)kWave * kRowsPerLane && steps > 4 * kWaves &&
       steps * units < (1ull << 31))  // the sums of share_out
-    s->n_parts = (uint32_t)std::min<uint64_t>(slots, units * ((steps + kWaves - 1) / kWaves + 1));
+    s->n_parts = (uint32_t)(std::min<uint64_t>(slots, units * ((steps + kWaves - 1) / kWaves + 1)) / s->m_groups *
+                            s->m_groups);
   const bool direct = s->n_parts == s->n_units && s->m_groups <= 1;
   const uint64_t parts = direct ? 0 : (uint64_t)s->n_parts * s->unit_rows;
   s->ml_at = parts * head_dim * 4;
