@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "ibp_kv.h"
 
@@ -1766,17 +1767,24 @@ struct Shape {
   uint64_t of_at, mass_at, ml_at, bytes;  // in the workspace; the sums come first
 };
 
-// Compute units of the current device; 256 where a HIP error is pending, which
-// is not this library's to clear, and where there is no device.
+// Compute units of the current device, read once per device; 256 where a HIP
+// error is pending, which is not this library's to clear, and where there is no
+// device.
 int compute_units() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
   int dev = 0, n = 0;
   if (hipPeekAtLastError() != hipSuccess) return 256;
-  if (hipGetDevice(&dev) != hipSuccess ||
-      hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) {
-    (void)hipGetLastError();
-    n = 0;
+  if (hipGetDevice(&dev) == hipSuccess && dev >= 0 && dev < kDevices) {
+    n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0 && hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess)
+      known[dev].store(n, std::memory_order_relaxed);
   }
-  return n > 0 ? n : 256;
+  if (n <= 0) {
+    (void)hipGetLastError();
+    n = 256;
+  }
+  return n;
 }
 
 bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint32_t head_dim,

@@ -64,14 +64,14 @@ class ibp_kv_cache(ctypes.Structure):
 
     def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
                  v_scales: torch.Tensor, page_tokens: int, head_dim: int):
+        _need(k_codes, torch.uint8, "k_codes")
+        _need(k_scales, torch.float32, "k_scales")
+        _need(v_codes, torch.uint8, "v_codes")
+        _need(v_scales, torch.float32, "v_scales")
         n = k_scales.numel()
-        for t, dtype, size, name in ((k_codes, torch.uint8, n * page_tokens * head_dim, "k_codes"),
-                                     (v_codes, torch.uint8, n * page_tokens * head_dim, "v_codes"),
-                                     (k_scales, torch.float32, n, "k_scales"),
-                                     (v_scales, torch.float32, n, "v_scales")):
-            _need(t, dtype, name)
-            if t.numel() != size:
-                raise ValueError(f"{name} must have {size} elements")
+        if not k_codes.numel() == v_codes.numel() == n * page_tokens * head_dim or v_scales.numel() != n:
+            raise ValueError(f"{n} pages of {page_tokens} x {head_dim} codes and as many scales expected, "
+                             "for keys and for values")
         super().__init__(n, page_tokens, head_dim, k_codes.data_ptr(), k_scales.data_ptr(),
                          v_codes.data_ptr(), v_scales.data_ptr())
         self.tensors = (k_codes, k_scales, v_codes, v_scales)
@@ -212,13 +212,16 @@ def ibp_kv_attention(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Te
     qt = _tensor(q, "q", q.dtype, shape)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    ot = _tensor(out, "out", q.dtype, shape)
+        ot = ibp_kv_tensor(out.data_ptr(), *out.stride()[:3])
+    else:
+        ot = _tensor(out, "out", q.dtype, shape)
     w = wo = None
     if weights is not None:
         _need(weights, torch.float32, "weights", pages.shape)
         if weights_out is None:
             weights_out = torch.empty_like(weights)
-        _need(weights_out, torch.float32, "weights_out", pages.shape)
+        else:
+            _need(weights_out, torch.float32, "weights_out", pages.shape)
         w, wo = weights.data_ptr(), weights_out.data_ptr()
     elif weights_out is not None:
         raise ValueError("weights_out without weights")
@@ -251,13 +254,16 @@ def ibp_kv_evict(pages: torch.Tensor, weights: torch.Tensor, lengths: torch.Tens
     _need(weights, torch.float32, "weights", pages.shape)
     if pages_out is None:
         pages_out = torch.empty_like(pages)
+    else:
+        _need(pages_out, torch.int32, "pages_out", pages.shape)
     if weights_out is None:
         weights_out = torch.empty_like(weights)
+    else:
+        _need(weights_out, torch.float32, "weights_out", pages.shape)
     if lengths_out is None:
         lengths_out = torch.empty_like(lengths)
-    _need(pages_out, torch.int32, "pages_out", pages.shape)
-    _need(weights_out, torch.float32, "weights_out", pages.shape)
-    _need(lengths_out, torch.int32, "lengths_out", lengths.shape)
+    else:
+        _need(lengths_out, torch.int32, "lengths_out", lengths.shape)
     _check("ibp_kv_evict",
            lib().ibp_kv_evict(table, page_tokens, keep_pages, sink_pages, recent_pages,
                               weights.data_ptr(), pages_out.data_ptr(), weights_out.data_ptr(),
