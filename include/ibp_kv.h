@@ -145,8 +145,10 @@ uint64_t ibp_kv_attention_workspace_bytes(const ibp_kv_cache *cache, const ibp_k
  *
  * A query that sees nothing (its position is negative, every page is a hole,
  * every score is minus infinity), and one past its sequence's count, gets
- * zeros.  Scores, statistics and sums are held in 32 bits.  What a query may
- * not see does not reach it, NaN included.
+ * zeros.  Scores, statistics and sums are held in 32 bits, the sums up to 2^8
+ * times their normalised value for each token of the row: values above about
+ * 2^119 / (tokens of the row) may overflow.  What a query may not see does not
+ * reach it, NaN included.
  *
  * weights, weights_out (both or neither; float, [n_seqs][kv_heads][max_pages];
  * they may be the same buffer): weights_out = weights + the w_j that the

@@ -1,5 +1,16 @@
 // libibp_kv: an 8-bit KV page cache and the attention that reads it, for AMD
 // Instinct MI355X (gfx950, CDNA4).  Formats and calls: include/ibp_kv.h.
+//
+// Times below are of one launch by kernel trace unless something else is said;
+// rates count the bytes that the operation cannot do without.  A large copy
+// reaches 6.1 TB/s on this card.
+//
+//   append     one wave per 16-token tile that gets tokens: HBM, 5.3 TB/s
+//   attention  workgroups of 4 waves over parts of a head's pages, each wave with
+//              running statistics of its own, joined in LDS and, where a head
+//              has several workgroups, by a second launch: HBM, 5.7-6.3 TB/s on
+//              long contexts; vector arithmetic and the two launches on short ones
+//   evict      one workgroup per row: vector arithmetic and the phases of a row
 #include <hip/hip_runtime.h>
 
 #include <stddef.h>
@@ -29,15 +40,17 @@ constexpr int workgroups_per_unit(int dj, int mt) { return dj * mt <= 4 ? 2 : 1;
 // as two of 16.
 constexpr int kQueryTiles = 2;
 constexpr int kUnit = 1024;     // bytes of a tile that one wide load of a wave takes
-constexpr float kGrowth = 8.f;
-constexpr int kMaxParts = 512;
-constexpr int kFewRows = 16;    // query rows of a unit that one thread adds up for its tile
+constexpr float kGrowth = 8.f;  // log2 of how far exponentials may exceed the scale of the sums
+constexpr int kMaxParts = 512;  // workgroups that the chip holds at once, at most
+// Query rows of a unit that one thread adds up for its tile.  8 rows of 131k
+// tokens: 5.5 us so, 9.9 us with the rows spread over the waves; 64 rows of 14k:
+// 18 us so, 10 us spread.
+constexpr int kFewRows = 16;
 constexpr int kLdsMass = 4096;  // shares of tiles that a workgroup that works alone keeps in LDS
 constexpr int kExpMin = -126, kExpMax = 119;  // exponents of a page's scale
 constexpr float kE4m3Max = 448.f;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -814,6 +827,8 @@ __device__ __forceinline__ float pair_sum32(float x, float y) {
 //   P^T operand of O^T = V^T P^T when the matrix instruction's index k is
 //   taken as (tile of the pair, r) within lane / 16, and the layout of a value
 //   tile gives V^T in the same order.
+//   e4m3 codes are exact in both 16-bit types; the keys' scale comes in with the
+//   scores, the values' with the weights.
 template <int DJ, bool F16, int MT, int ST>
 __device__ __forceinline__ void scores(const u32x4 (&k)[ST][DJ], const u32x4 (&q)[MT][DJ][2],
                                        f32x4 (&s)[MT][ST]) {
@@ -833,7 +848,9 @@ __device__ __forceinline__ void scores(const u32x4 (&k)[ST][DJ], const u32x4 (&q
 }
 
 // P times the page's scale goes into the second product as two 16-bit terms
-// (bf16, so that any scale fits): the products keep 16 bits of P.
+// (bf16, so that any scale fits): the products keep 16 bits of P, where one term
+// would round P to 8 and be the largest error of an fp16 output.  The second
+// product is twice as long for it, which the loads hide.
 template <int MT, int ST>
 struct Probs {
   u32x4 hi[MT][ST / 2], lo[MT][ST / 2];
@@ -975,8 +992,8 @@ __device__ __forceinline__ float log_total(float m, float l) {
 }
 
 // The shares that tile `tile` got from eight query rows of a unit (m, m + stride,
-// ...), and their sum as weights: lse is the rows' log_total (+inf for rows that see nothing, whose
-// shares are not written).
+// ...), and their sum as weights: lse is the rows' log_total (+inf for rows that
+// see nothing, whose shares are not written).
 struct Shares {
   float x[8];
 };
@@ -1011,10 +1028,19 @@ __device__ __forceinline__ void write_weight(const Attention& a, uint32_t row, i
   a.w_out[at] = a.w_in[at] + w;
 }
 
-// A workgroup takes one part of one unit; its waves take steps in turn and
-// join at the end.  With one part and one unit a row the result is written
-// here, else it is left in the workspace for the combining kernel.
-// ONCE: the unit has all query rows of its head.
+// A workgroup takes one part of one unit; its waves take steps in turn, with
+// running maximum and sum, and join at the end.  With one part and one unit a row
+// the result is written here, else it is left in the workspace for the joining
+// kernel.  ONCE: the unit has all query rows of its head.
+//
+// Everything of a step stays in the wave's registers: the tiles' layouts give the
+// operands of the matrix instructions as they are loaded, and scores become
+// weights in place.  What it reads once bounds it: 16 x 32 heads x 4096 tokens of
+// 128 dims 85.7 us, 6.3 TB/s; two contexts of 131k and 91k tokens, 8 heads, 8
+// queries each, 80.6 us, 5.7 TB/s.  Short rows pay some 6 us for finding their
+// pages, the joining and the launch (291 tokens: 7.4 us); 72 ragged rows with 25
+// queries of 64 dims, 43 MB, take 16.8 us, a third of it vector instructions of the
+// steps (250 a step), a sixth those before and after.
 template <int DJ, bool F16, int MT, bool ONCE>
 __global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, MT)) void attention_kernel(Attention a) {
   constexpr int D = 64 * DJ;
@@ -1206,7 +1232,9 @@ __device__ __forceinline__ void join_parts(const Attention& a, const Part& t, in
 
 // Joins the parts.  The first workgroups take a query row each, or one for each
 // of their waves where the units have few parts on average (264 units x 14 rows
-// in 2 parts: 11.4 us by workgroups); the others take 256 or 64 tiles of a row each and sum their weights.
+// in 2 parts: 11.4 us by workgroups, 7.5 us so); the others take 256 or 64 tiles
+// of a row each and sum their weights.  4-6 us, which is the latency of its three
+// loads that wait for each other.
 template <int DJ, bool F16, int MT>
 __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
   constexpr int D = 64 * DJ;
@@ -1398,6 +1426,10 @@ __device__ __forceinline__ Choice choice_of(const Evict& e, uint32_t row) {
 // with one count a round takes 25 rounds where this takes 2 or 3: 16,384 pages x
 // 768 rows spent 47 us on it.)  With the counts of every 64 pages in LDS each
 // page then knows its place.
+// 768 rows of 16,384 pages (153 MB for those held, 201 MB with the spare entries)
+// take 59 us: 1.5 workgroups to a place on the chip, and the loads, the choice
+// (10 us, vector instructions) and the stores of those that run together come one
+// after the other.
 template <int THREADS, int R>
 __global__ __launch_bounds__(THREADS, 8) void evict_kernel(Evict e) {
   constexpr int kW = THREADS / kWave;
@@ -1571,7 +1603,8 @@ __global__ __launch_bounds__(THREADS, 8) void evict_kernel(Evict e) {
 }
 
 // Rows of any length: the weight is found digit by digit (8 bits at a time,
-// from counts in LDS), the weights read again for each.
+// from counts in LDS), the weights read again for each (172 us for the 768 rows
+// above).
 __global__ __launch_bounds__(kThreads) void evict_long_kernel(Evict e) {
   __shared__ uint32_t s_count[256];
   __shared__ uint32_t s_pick[2];
@@ -2020,6 +2053,9 @@ int ibp_kv_evict(const ibp_kv_table* table, uint32_t page_tokens, uint64_t keep_
   e.recent = (uint32_t)std::min<uint64_t>(recent_pages, 0xFFFFFFFFull);
   const dim3 grid((uint32_t)n_rows);
   hipStream_t st = (hipStream_t)stream;
+  // The smallest that holds a row: 512 rows of 1024 pages take 8.1 us with 256
+  // threads and 10.7 with 1024, 512 rows of 4096 pages 15.0 us with 4 pages a
+  // thread and 22.4 with 16.
   if (table->max_pages <= 1024)
     hipLaunchKernelGGL((evict_kernel<256, 4>), grid, dim3(256), 0, st, e);
   else if (table->max_pages <= 4096)
