@@ -1391,10 +1391,9 @@ struct Evict {
 
 // Whole numbers above 0 in the order of the weights.
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  uint32_t b = __builtin_bit_cast(uint32_t, w);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0xFF800001u;  // NaN: one above infinity
-  if (b == 0x80000000u) b = 0u;
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  const uint32_t b = __builtin_bit_cast(uint32_t, w + 0.f);  // -0 is 0
+  const uint32_t key = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return w == w ? key : 0xFF800001u;  // NaN: one above infinity
 }
 
 // What a row's workgroup does: keep the protected pages and, of pages lo .. hi
@@ -1405,6 +1404,11 @@ struct Choice {
   uint32_t held, left, lo, hi, want;
   bool full;
 };
+
+// A buffer of `bytes` bytes at an address that is the same for the whole wave.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00027000);
+}
 
 __device__ __forceinline__ Choice choice_of(const Evict& e, uint32_t row) {
   Choice c;
@@ -1427,9 +1431,9 @@ __device__ __forceinline__ Choice choice_of(const Evict& e, uint32_t row) {
 // 768 rows spent 47 us on it.)  With the counts of every 64 pages in LDS each
 // page then knows its place.
 // 768 rows of 16,384 pages (153 MB for those held, 201 MB with the spare entries)
-// take 59 us: 1.5 workgroups to a place on the chip, and the loads, the choice
-// (10 us, vector instructions) and the stores of those that run together come one
-// after the other.
+// take 52 us: 1.5 workgroups to a place on the chip, and the loads, the choice and
+// the stores of those that run together come one after the other (a row alone
+// takes 17 us).  Without the buffers' bounds, with a branch for each page, 59 us.
 template <int THREADS, int R>
 __global__ __launch_bounds__(THREADS, 8) void evict_kernel(Evict e) {
   constexpr int kW = THREADS / kWave;
@@ -1448,30 +1452,26 @@ __global__ __launch_bounds__(THREADS, 8) void evict_kernel(Evict e) {
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const Choice c = choice_of(e, blockIdx.x);
   if (threadIdx.x == 0) e.lengths_out[blockIdx.x] = c.len - (int)((c.held - c.left) << e.page_shift);
-  const float* weights = e.weights + c.at;
-  const int32_t* pages = e.pages + c.at;
-  float* weights_out = e.weights_out + c.at;
-  int32_t* pages_out = e.pages_out + c.at;
+  // Buffers that end with the row: what lies past it is read as 0 and not
+  // written, without a branch for each.
+  const uint32_t bytes = e.max_pages * 4u;
+  const auto weights = row_buffer(e.weights + c.at, bytes), weights_out = row_buffer(e.weights_out + c.at, bytes);
+  const auto pages = row_buffer(e.pages + c.at, bytes), pages_out = row_buffer(e.pages_out + c.at, bytes);
+  const int mine = (int)threadIdx.x * 4;
   // everything is asked for at once; the ids arrive while the places are worked out
-  float w[R];
-  int32_t id[R];
+  uint32_t w[R], id[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const uint32_t p = (uint32_t)i * THREADS + threadIdx.x;
-    w[i] = p < e.max_pages ? weights[p] : 0.f;
-  }
+  for (int i = 0; i < R; ++i) w[i] = __builtin_amdgcn_raw_buffer_load_b32(weights, mine, i * THREADS * 4, 0);
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const uint32_t p = (uint32_t)i * THREADS + threadIdx.x;
-    id[i] = p < e.max_pages ? pages[p] : 0;
-  }
+  for (int i = 0; i < R; ++i) id[i] = __builtin_amdgcn_raw_buffer_load_b32(pages, mine, i * THREADS * 4, 0);
+  const uint32_t span = c.full ? c.hi - c.lo : 0u;
   uint32_t low = 0xFFFFFFFFu, high = 0;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const uint32_t p = (uint32_t)i * THREADS + threadIdx.x;
     uint32_t key = p < c.held ? kStays : 0u;
-    if (c.full && p - c.lo < c.hi - c.lo) {
-      key = weight_key(w[i]);
+    if (p - c.lo < span) {
+      key = weight_key(__builtin_bit_cast(float, w[i]));
       low = min(low, key);
       high = max(high, key);
     }
@@ -1595,10 +1595,8 @@ __global__ __launch_bounds__(THREADS, 8) void evict_kernel(Evict e) {
     }
     // past the row's pages `before` is `left`, so that they keep their places
     const uint32_t to = stays ? before : c.left + p - before;
-    if (p < e.max_pages) {
-      pages_out[to] = id[i];
-      weights_out[to] = p < c.held && !stays ? 0.f : w[i];
-    }
+    __builtin_amdgcn_raw_buffer_store_b32(id[i], pages_out, (int)to * 4, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(key != 0u && !stays ? 0u : w[i], weights_out, (int)to * 4, 0, 0);
   }
 }
 
@@ -2054,7 +2052,7 @@ int ibp_kv_evict(const ibp_kv_table* table, uint32_t page_tokens, uint64_t keep_
   const dim3 grid((uint32_t)n_rows);
   hipStream_t st = (hipStream_t)stream;
   // The smallest that holds a row: 512 rows of 1024 pages take 8.1 us with 256
-  // threads and 10.7 with 1024, 512 rows of 4096 pages 15.0 us with 4 pages a
+  // threads and 10.7 with 1024, 512 rows of 4096 pages 14.3 us with 4 pages a
   // thread and 22.4 with 16.
   if (table->max_pages <= 1024)
     hipLaunchKernelGGL((evict_kernel<256, 4>), grid, dim3(256), 0, st, e);
