@@ -9,6 +9,7 @@ use; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -115,9 +116,21 @@ def _check(fn: str, status: int):
         raise IBPKVError(fn, status)
 
 
-def _stream(stream, t: torch.Tensor) -> int:
-    """The given stream, or the current one of t's device."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else stream.cuda_stream
+def _stream(t: torch.Tensor) -> int:
+    """The current stream of t's device."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _on_stream(fn):
+    """With stream=s the call is made as if s were the current stream, so that
+    the tensors it allocates are s's too."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return call
 
 
 def _need(t: torch.Tensor, dtype: torch.dtype, name: str, shape=None):
@@ -163,22 +176,22 @@ def _counts(counts, n_seqs: int):
     return counts.data_ptr()
 
 
+@_on_stream
 def ibp_kv_append(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Tensor,
-                  k: torch.Tensor, v: torch.Tensor, counts: torch.Tensor | None = None,
-                  stream=None):
+                  k: torch.Tensor, v: torch.Tensor, counts: torch.Tensor | None = None):
     """Append the tokens of k and v ([n_seqs, n_new, kv_heads, head_dim],
     bfloat16 or float16, any strides of the leading axes) to the pages of
     their rows.  pages: int32 [n_seqs, kv_heads, max_pages]; lengths: int32
     [n_seqs, kv_heads], the new tokens counted in; counts: int32 [n_seqs], how
     many of the n_new tokens each sequence brings (default: all).
-    Asynchronous on the current stream."""
+    Asynchronous on the current stream, or on stream=."""
     dtype = _new_dtype(k, "k")
     table = _table(pages, lengths)
     shape = (table.n_seqs, k.shape[1], table.kv_heads, cache.head_dim)
     kt, vt = _tensor(k, "k", k.dtype, shape), _tensor(v, "v", k.dtype, shape)
     _check("ibp_kv_append",
            lib().ibp_kv_append(cache, table, dtype, k.shape[1], kt, vt,
-                               _counts(counts, table.n_seqs), _stream(stream, pages)))
+                               _counts(counts, table.n_seqs), _stream(pages)))
 
 
 def ibp_kv_attention_workspace_bytes(cache: ibp_kv_cache, pages: torch.Tensor,
@@ -188,12 +201,13 @@ def ibp_kv_attention_workspace_bytes(cache: ibp_kv_cache, pages: torch.Tensor,
                                                       n_new, int(with_weights)))
 
 
+@_on_stream
 def ibp_kv_attention(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Tensor,
                      q: torch.Tensor, scale: float | None = None,
                      weights: torch.Tensor | None = None,
                      weights_out: torch.Tensor | None = None,
                      counts: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                     workspace: torch.Tensor | None = None, stream=None):
+                     workspace: torch.Tensor | None = None):
     """Attention of the new tokens' queries q ([n_seqs, n_new, q_heads,
     head_dim], bfloat16 or float16) over the rows' pages, causal among the new
     tokens; scale defaults to head_dim ** -0.5.  With weights (float32
@@ -202,7 +216,7 @@ def ibp_kv_attention(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Te
     tensor.  workspace: a uint8 GPU tensor of at least
     ibp_kv_attention_workspace_bytes (default: allocated).  Returns
     (out, weights_out), the second None without weights.  Asynchronous on the
-    current stream."""
+    current stream, or on stream=."""
     dtype = _new_dtype(q, "q")
     table = _table(pages, lengths)
     n_new, q_heads = q.shape[1], q.shape[2]
@@ -237,19 +251,20 @@ def ibp_kv_attention(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Te
            L.ibp_kv_attention(cache, table, dtype, q_heads, n_new, qt, ot,
                               _counts(counts, table.n_seqs),
                               1.0 / math.sqrt(cache.head_dim) if scale is None else scale,
-                              w, wo, ws, ws_bytes, _stream(stream, q)))
+                              w, wo, ws, ws_bytes, _stream(q)))
     return out, weights_out
 
 
+@_on_stream
 def ibp_kv_evict(pages: torch.Tensor, weights: torch.Tensor, lengths: torch.Tensor,
                  page_tokens: int, keep_pages: int, sink_pages: int = 1, recent_pages: int = 1,
                  pages_out: torch.Tensor | None = None, weights_out: torch.Tensor | None = None,
-                 lengths_out: torch.Tensor | None = None, stream=None):
+                 lengths_out: torch.Tensor | None = None):
     """Cut every row to keep_pages pages: the first sink_pages, the last
     recent_pages and the heaviest between.  Returns (pages, weights, lengths)
     with the kept pages first, the evicted ones after them (weight 0) and the
     row's other entries as they were.  The outputs must not overlap the
-    inputs.  Asynchronous on the current stream."""
+    inputs.  Asynchronous on the current stream, or on stream=."""
     table = _table(pages, lengths)
     _need(weights, torch.float32, "weights", pages.shape)
     if pages_out is None:
@@ -267,5 +282,5 @@ def ibp_kv_evict(pages: torch.Tensor, weights: torch.Tensor, lengths: torch.Tens
     _check("ibp_kv_evict",
            lib().ibp_kv_evict(table, page_tokens, keep_pages, sink_pages, recent_pages,
                               weights.data_ptr(), pages_out.data_ptr(), weights_out.data_ptr(),
-                              lengths_out.data_ptr(), _stream(stream, pages)))
+                              lengths_out.data_ptr(), _stream(pages)))
     return pages_out, weights_out, lengths_out

@@ -403,6 +403,63 @@ def test_attention_strides_and_buffers(kv):
     torch.cuda.synchronize()
 
 
+def test_calls_on_a_given_stream(kv):
+    """stream=: appended, attended and evicted on a stream that waits behind
+    other work, with everything the calls allocate on it; the current stream
+    has its own memory in use meanwhile."""
+    seqs, heads, d, pt, m = 2, 2, 128, 16, 40
+    p = filled(kv, seqs, heads, m, pt, d, [500, 333], seed=3)
+    lengths = grid(seqs, heads, [501, 334])
+    k, v = values(1, (seqs, 1, heads, d), torch.bfloat16), values(2, (seqs, 1, heads, d), torch.bfloat16)
+    q = torch.randn(seqs, 1, heads * 3, d, generator=torch.Generator().manual_seed(1)).bfloat16()
+    w = np.random.default_rng(1).random((seqs, heads, m), dtype=np.float32)
+    gl, gk, gv, gq, gw = torch.from_numpy(lengths).cuda(), k.cuda(), v.cuda(), q.cuda(), torch.from_numpy(w).cuda()
+    for (codes, scales), x, place in ((p.k, k, orc.k_place), (p.v, v, orc.v_place)):
+        orc.append(codes, scales, place(pt, d), pt, p.pages, lengths, x.double().numpy())
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        busy = torch.randn(4096, 4096, device="cuda")
+        for _ in range(10):
+            busy = busy @ busy * 1e-2
+    kv.ibp_kv_append(p.cache, p.gpu_pages, gl, gk, gv, stream=s)
+    out, wo = kv.ibp_kv_attention(p.cache, p.gpu_pages, gl, gq, weights=gw, stream=s)
+    pages, weights, left = kv.ibp_kv_evict(p.gpu_pages, wo, gl, pt, keep_pages=9, recent_pages=2, stream=s)
+    for _ in range(20):  # the current stream's own allocations
+        torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda")
+    s.synchronize()
+    p.check()
+    close(out.cpu(), np_of(wo), expect(p, lengths, q, w))
+    same_eviction([np_of(pages), np_of(weights), np_of(left)],
+                  orc.evict(p.pages, np_of(wo), lengths, pt, 9, 1, 2))
+
+
+def test_pool_without_pages(kv):
+    """Every id is a hole: zeros, and the weights as they were."""
+    none = [torch.empty(0, dtype=torch.uint8, device="cuda"), torch.empty(0, device="cuda")]
+    cache = kv.ibp_kv_cache(*none, *none, 16, 64)
+    pages = torch.zeros(2, 3, 200, dtype=torch.int32, device="cuda")
+    lengths = torch.full((2, 3), 3000, dtype=torch.int32, device="cuda")
+    x = torch.ones(2, 1, 3, 64, dtype=torch.float16, device="cuda")
+    kv.ibp_kv_append(cache, pages, lengths, x, x)
+    w = torch.rand(2, 3, 200, device="cuda")
+    out, wo = kv.ibp_kv_attention(cache, pages, lengths, x.repeat(1, 1, 2, 1), weights=w)
+    assert not out.any() and torch.equal(wo, w)
+
+
+def test_attention_without_queries(kv):
+    """No new tokens: nothing to write but the weights."""
+    p = filled(kv, 1, 2, 10, 16, 64, [100], seed=1)
+    w = torch.rand(1, 2, 10, device="cuda")
+    out, wo = kv.ibp_kv_attention(p.cache, p.gpu_pages, torch.full((1, 2), 100, dtype=torch.int32, device="cuda"),
+                                  torch.zeros(1, 0, 4, 64, dtype=torch.bfloat16, device="cuda"), weights=w)
+    assert out.shape == (1, 0, 4, 64) and torch.equal(wo, w)
+    none = torch.zeros(0, 2, 10, dtype=torch.int32, device="cuda")
+    out, wo = kv.ibp_kv_attention(p.cache, none, none[..., 0].contiguous(),
+                                  torch.zeros(0, 1, 4, 64, dtype=torch.bfloat16, device="cuda"), weights=w[:0])
+    assert out.numel() == 0 and wo.numel() == 0
+
+
 def test_pages_shared_by_rows(kv):
     """A common prompt: two sequences name the same pages."""
     p = filled(kv, 2, 1, 10, 16, 64, [160, 160], seed=5)
