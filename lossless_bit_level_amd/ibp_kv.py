@@ -9,7 +9,6 @@ use; there is no fallback.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 
@@ -121,22 +120,10 @@ def _stream(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
-def _on_stream(fn):
-    """With stream=s the call is made as if s were the current stream, so that
-    the tensors it allocates are s's too."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kwargs):
-        if stream is None:
-            return fn(*args, **kwargs)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kwargs)
-    return call
-
-
 def _need(t: torch.Tensor, dtype: torch.dtype, name: str, shape=None):
     """Contiguous GPU tensors only: the kernels take their addresses as they
     are (a CPU pointer there would fault the GPU)."""
-    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+    if not t.is_cuda or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} GPU tensor")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}")
@@ -153,7 +140,7 @@ def _table(pages: torch.Tensor, lengths: torch.Tensor) -> ibp_kv_table:
 
 def _tensor(t: torch.Tensor, name: str, dtype, shape) -> ibp_kv_tensor:
     """Strides of the leading axes are free, the head axis is contiguous."""
-    if not t.is_cuda or t.dtype != dtype or t.dim() != 4 or t.shape != shape:
+    if not t.is_cuda or t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be a {dtype} GPU tensor of shape {tuple(shape)}")
     s = t.stride()
     if s[3] != 1:
@@ -176,15 +163,18 @@ def _counts(counts, n_seqs: int):
     return counts.data_ptr()
 
 
-@_on_stream
 def ibp_kv_append(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Tensor,
-                  k: torch.Tensor, v: torch.Tensor, counts: torch.Tensor | None = None):
+                  k: torch.Tensor, v: torch.Tensor, counts: torch.Tensor | None = None,
+                  stream=None):
     """Append the tokens of k and v ([n_seqs, n_new, kv_heads, head_dim],
     bfloat16 or float16, any strides of the leading axes) to the pages of
     their rows.  pages: int32 [n_seqs, kv_heads, max_pages]; lengths: int32
     [n_seqs, kv_heads], the new tokens counted in; counts: int32 [n_seqs], how
     many of the n_new tokens each sequence brings (default: all).
     Asynchronous on the current stream, or on stream=."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return ibp_kv_append(cache, pages, lengths, k, v, counts)
     dtype = _new_dtype(k, "k")
     table = _table(pages, lengths)
     shape = (table.n_seqs, k.shape[1], table.kv_heads, cache.head_dim)
@@ -201,13 +191,12 @@ def ibp_kv_attention_workspace_bytes(cache: ibp_kv_cache, pages: torch.Tensor,
                                                       n_new, int(with_weights)))
 
 
-@_on_stream
 def ibp_kv_attention(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Tensor,
                      q: torch.Tensor, scale: float | None = None,
                      weights: torch.Tensor | None = None,
                      weights_out: torch.Tensor | None = None,
                      counts: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                     workspace: torch.Tensor | None = None):
+                     workspace: torch.Tensor | None = None, stream=None):
     """Attention of the new tokens' queries q ([n_seqs, n_new, q_heads,
     head_dim], bfloat16 or float16) over the rows' pages, causal among the new
     tokens; scale defaults to head_dim ** -0.5.  With weights (float32
@@ -217,6 +206,10 @@ def ibp_kv_attention(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Te
     ibp_kv_attention_workspace_bytes (default: allocated).  Returns
     (out, weights_out), the second None without weights.  Asynchronous on the
     current stream, or on stream=."""
+    if stream is not None:  # what the call allocates is the stream's too
+        with torch.cuda.stream(stream):
+            return ibp_kv_attention(cache, pages, lengths, q, scale, weights, weights_out, counts,
+                                    out, workspace)
     dtype = _new_dtype(q, "q")
     table = _table(pages, lengths)
     n_new, q_heads = q.shape[1], q.shape[2]
@@ -255,16 +248,19 @@ def ibp_kv_attention(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Te
     return out, weights_out
 
 
-@_on_stream
 def ibp_kv_evict(pages: torch.Tensor, weights: torch.Tensor, lengths: torch.Tensor,
                  page_tokens: int, keep_pages: int, sink_pages: int = 1, recent_pages: int = 1,
                  pages_out: torch.Tensor | None = None, weights_out: torch.Tensor | None = None,
-                 lengths_out: torch.Tensor | None = None):
+                 lengths_out: torch.Tensor | None = None, stream=None):
     """Cut every row to keep_pages pages: the first sink_pages, the last
     recent_pages and the heaviest between.  Returns (pages, weights, lengths)
     with the kept pages first, the evicted ones after them (weight 0) and the
     row's other entries as they were.  The outputs must not overlap the
     inputs.  Asynchronous on the current stream, or on stream=."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return ibp_kv_evict(pages, weights, lengths, page_tokens, keep_pages, sink_pages,
+                                recent_pages, pages_out, weights_out, lengths_out)
     table = _table(pages, lengths)
     _need(weights, torch.float32, "weights", pages.shape)
     if pages_out is None:
