@@ -1,15 +1,17 @@
-"""Thin ctypes binding of libibp_kv (include/ibp_kv.h), same names as the C
-ABI: an 8-bit KV page cache, the attention that reads it, and eviction of its
-pages by accumulated attention weight.
+"""Thin binding of libibp_kv (include/ibp_kv.h), same names as the C ABI: an
+8-bit KV page cache, the attention that reads it, and eviction of its pages by
+accumulated attention weight.
 
 Argument marshalling only; every step runs in the HIP kernels of
-libibp_kv.so.  If the library has not been built this module raises on first
-use; there is no fallback.
+libibp_kv.so.  The structures and lib() are ctypes; the calls take torch
+tensors through a small extension module (csrc/ibp_kv_torch.cpp), since a
+decoding step makes many short ones: it checks the arguments, allocates
+results and calls the C ABI.  If either has not been built this module raises
+on first use; there is no fallback.
 """
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 
 import torch
@@ -21,7 +23,6 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libibp_kv.
 
 IBP_KV_BF16 = 0
 IBP_KV_FP16 = 1
-_DTYPES = {torch.bfloat16: IBP_KV_BF16, torch.float16: IBP_KV_FP16}
 
 
 class IBPKVError(RuntimeError):
@@ -64,16 +65,7 @@ class ibp_kv_cache(ctypes.Structure):
 
     def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
                  v_scales: torch.Tensor, page_tokens: int, head_dim: int):
-        _need(k_codes, torch.uint8, "k_codes")
-        _need(k_scales, torch.float32, "k_scales")
-        _need(v_codes, torch.uint8, "v_codes")
-        _need(v_scales, torch.float32, "v_scales")
-        n = k_scales.numel()
-        if not k_codes.numel() == v_codes.numel() == n * page_tokens * head_dim or v_scales.numel() != n:
-            raise ValueError(f"{n} pages of {page_tokens} x {head_dim} codes and as many scales expected, "
-                             "for keys and for values")
-        super().__init__(n, page_tokens, head_dim, k_codes.data_ptr(), k_scales.data_ptr(),
-                         v_codes.data_ptr(), v_scales.data_ptr())
+        _ext().set_cache(self, k_codes, k_scales, v_codes, v_scales, page_tokens, head_dim)
         self.tensors = (k_codes, k_scales, v_codes, v_scales)
 
 
@@ -106,6 +98,23 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_module = None
+
+
+def _ext():
+    """The extension module (built in-tree by lossless_bit_level_amd.build)."""
+    global _module
+    if _module is None:
+        lib()
+        try:
+            from . import _ibp_kv
+        except ImportError as e:
+            raise RuntimeError("_ibp_kv.so is missing or does not load: build it with "
+                               f"`python -m lossless_bit_level_amd.build` ({e})") from e
+        _module = _ibp_kv
+    return _module
+
+
 def status_string(status: int) -> str:
     return lib().ibp_kv_status_string(status).decode()
 
@@ -116,51 +125,8 @@ def _check(fn: str, status: int):
 
 
 def _stream(t: torch.Tensor) -> int:
-    """The current stream of t's device."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
-
-
-def _need(t: torch.Tensor, dtype: torch.dtype, name: str, shape=None):
-    """Contiguous GPU tensors only: the kernels take their addresses as they
-    are (a CPU pointer there would fault the GPU)."""
-    if not t.is_cuda or t.dtype is not dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} GPU tensor")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have the shape {tuple(shape)}")
-
-
-def _table(pages: torch.Tensor, lengths: torch.Tensor) -> ibp_kv_table:
-    if pages.dim() != 3:
-        raise ValueError("pages must be [n_seqs, kv_heads, max_pages]")
-    _need(pages, torch.int32, "pages")
-    _need(lengths, torch.int32, "lengths", pages.shape[:2])
-    n_seqs, heads, max_pages = pages.shape
-    return ibp_kv_table(n_seqs, heads, max_pages, pages.data_ptr(), lengths.data_ptr())
-
-
-def _tensor(t: torch.Tensor, name: str, dtype, shape) -> ibp_kv_tensor:
-    """Strides of the leading axes are free, the head axis is contiguous."""
-    if not t.is_cuda or t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name} must be a {dtype} GPU tensor of shape {tuple(shape)}")
-    s = t.stride()
-    if s[3] != 1:
-        raise ValueError(f"the last axis of {name} must be contiguous")
-    return ibp_kv_tensor(t.data_ptr(), s[0], s[1], s[2])
-
-
-def _new_dtype(t: torch.Tensor, name: str) -> int:
-    dtype = _DTYPES.get(t.dtype)
-    if dtype is None or t.dim() != 4:
-        raise ValueError(f"{name} must be a bfloat16 or float16 tensor "
-                         "[n_seqs, n_new, heads, head_dim]")
-    return dtype
-
-
-def _counts(counts, n_seqs: int):
-    if counts is None:
-        return None
-    _need(counts, torch.int32, "counts", (n_seqs,))
-    return counts.data_ptr()
+    """The current stream of t's device (a CPU tensor is refused later on)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else 0
 
 
 def ibp_kv_append(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Tensor,
@@ -175,20 +141,16 @@ def ibp_kv_append(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Tenso
     if stream is not None:
         with torch.cuda.stream(stream):
             return ibp_kv_append(cache, pages, lengths, k, v, counts)
-    dtype = _new_dtype(k, "k")
-    table = _table(pages, lengths)
-    shape = (table.n_seqs, k.shape[1], table.kv_heads, cache.head_dim)
-    kt, vt = _tensor(k, "k", k.dtype, shape), _tensor(v, "v", k.dtype, shape)
     _check("ibp_kv_append",
-           lib().ibp_kv_append(cache, table, dtype, k.shape[1], kt, vt,
-                               _counts(counts, table.n_seqs), _stream(pages)))
+           _ext().append(cache, pages, lengths, k, v, counts, _stream(pages)))
 
 
 def ibp_kv_attention_workspace_bytes(cache: ibp_kv_cache, pages: torch.Tensor,
                                      lengths: torch.Tensor, q_heads: int, n_new: int,
                                      with_weights: bool) -> int:
-    return int(lib().ibp_kv_attention_workspace_bytes(cache, _table(pages, lengths), q_heads,
-                                                      n_new, int(with_weights)))
+    table = ibp_kv_table(*pages.shape, pages.data_ptr(), lengths.data_ptr())
+    return int(lib().ibp_kv_attention_workspace_bytes(cache, table, q_heads, n_new,
+                                                      int(with_weights)))
 
 
 def ibp_kv_attention(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Tensor,
@@ -210,41 +172,9 @@ def ibp_kv_attention(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Te
         with torch.cuda.stream(stream):
             return ibp_kv_attention(cache, pages, lengths, q, scale, weights, weights_out, counts,
                                     out, workspace)
-    dtype = _new_dtype(q, "q")
-    table = _table(pages, lengths)
-    n_new, q_heads = q.shape[1], q.shape[2]
-    if table.kv_heads and (q_heads == 0 or q_heads % table.kv_heads):
-        raise ValueError("q_heads must be a multiple of kv_heads")
-    shape = (table.n_seqs, n_new, q_heads, cache.head_dim)
-    qt = _tensor(q, "q", q.dtype, shape)
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        ot = ibp_kv_tensor(out.data_ptr(), *out.stride()[:3])
-    else:
-        ot = _tensor(out, "out", q.dtype, shape)
-    w = wo = None
-    if weights is not None:
-        _need(weights, torch.float32, "weights", pages.shape)
-        if weights_out is None:
-            weights_out = torch.empty_like(weights)
-        else:
-            _need(weights_out, torch.float32, "weights_out", pages.shape)
-        w, wo = weights.data_ptr(), weights_out.data_ptr()
-    elif weights_out is not None:
-        raise ValueError("weights_out without weights")
-    L = lib()
-    if workspace is None:
-        n = L.ibp_kv_attention_workspace_bytes(cache, table, q_heads, n_new, w is not None)
-        if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    else:
-        _need(workspace, torch.uint8, "workspace")
-    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    _check("ibp_kv_attention",
-           L.ibp_kv_attention(cache, table, dtype, q_heads, n_new, qt, ot,
-                              _counts(counts, table.n_seqs),
-                              1.0 / math.sqrt(cache.head_dim) if scale is None else scale,
-                              w, wo, ws, ws_bytes, _stream(q)))
+    status, out, weights_out = _ext().attention(cache, pages, lengths, q, scale, weights,
+                                                weights_out, counts, out, workspace, _stream(q))
+    _check("ibp_kv_attention", status)
     return out, weights_out
 
 
@@ -261,22 +191,7 @@ def ibp_kv_evict(pages: torch.Tensor, weights: torch.Tensor, lengths: torch.Tens
         with torch.cuda.stream(stream):
             return ibp_kv_evict(pages, weights, lengths, page_tokens, keep_pages, sink_pages,
                                 recent_pages, pages_out, weights_out, lengths_out)
-    table = _table(pages, lengths)
-    _need(weights, torch.float32, "weights", pages.shape)
-    if pages_out is None:
-        pages_out = torch.empty_like(pages)
-    else:
-        _need(pages_out, torch.int32, "pages_out", pages.shape)
-    if weights_out is None:
-        weights_out = torch.empty_like(weights)
-    else:
-        _need(weights_out, torch.float32, "weights_out", pages.shape)
-    if lengths_out is None:
-        lengths_out = torch.empty_like(lengths)
-    else:
-        _need(lengths_out, torch.int32, "lengths_out", lengths.shape)
-    _check("ibp_kv_evict",
-           lib().ibp_kv_evict(table, page_tokens, keep_pages, sink_pages, recent_pages,
-                              weights.data_ptr(), pages_out.data_ptr(), weights_out.data_ptr(),
-                              lengths_out.data_ptr(), _stream(pages)))
-    return pages_out, weights_out, lengths_out
+    status, *out = _ext().evict(pages, weights, lengths, page_tokens, keep_pages, sink_pages,
+                                recent_pages, pages_out, weights_out, lengths_out, _stream(pages))
+    _check("ibp_kv_evict", status)
+    return tuple(out)
