@@ -1029,9 +1029,10 @@ __device__ __forceinline__ void write_weight(const Attention& a, uint32_t row, i
 }
 
 // A workgroup takes one part of one unit; its waves take steps in turn, with
-// running maximum and sum, and join at the end.  With one part and one unit a row
-// the result is written here, else it is left in the workspace for the joining
-// kernel.  ONCE: the unit has all query rows of its head.
+// running maximum and sum, and join at the end.  With one part a unit the result
+// is written here, else it is left in the workspace for the joining kernel, and so
+// is what weights need where a row has several units or parts.  ONCE: the unit has
+// all query rows of its head.
 //
 // Everything of a step stays in the wave's registers: the tiles' layouts give the
 // operands of the matrix instructions as they are loaded, and scores become
@@ -1051,7 +1052,7 @@ __global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, MT)) void attenti
   __shared__ float s_lse[MT * 16];
   __shared__ float s_mass[kLdsMass];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const bool direct = a.n_parts == a.n_units && a.m_groups.d == 1;
+  const bool whole = a.n_parts == a.n_units, alone = whole && a.m_groups.d == 1;
   const Part part = part_of_workgroup<ST>(a, blockIdx.x, lane);
   if (part.idle) return;
   const uint32_t unit = part.row * a.m_groups.d + part.group;
@@ -1062,7 +1063,7 @@ __global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, MT)) void attenti
     a.ws_of[2 * unit] = (int32_t)part.first;
     a.ws_of[2 * unit + 1] = part.of;
   }
-  if (first >= last && !direct) return;
+  if (first >= last && !whole) return;
 
   u32x4 q[MT][DJ][2];
   int seen[MT];
@@ -1164,9 +1165,9 @@ __global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, MT)) void attenti
     const float share = total == 0.f ? 0.f : 1.f / total;
     const bool any = seen_by(a, p, m) > 0;
     if (d4 == 0) {
-      if (direct)
+      if (alone)
         s_lse[m_local] = any ? log_total(top, total) : INFINITY;
-      else if (here)
+      else if (here && (!whole || a.w_out))
         a.ws_ml[slot] = f32x2{top, total};
     }
 #pragma unroll
@@ -1181,7 +1182,7 @@ __global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, MT)) void attenti
       for (int w = 0; w < kWaves; ++w) o += *(const f32x4*)&s_o[w][n][d4] * f[w];
       if (!here) continue;
       const int d = 64 * h + d4;
-      if (direct) {
+      if (whole) {
         uint16_t* dst = row_of(a.out, a, p, m) + d;
         u16x4 y;
 #pragma unroll
@@ -1197,7 +1198,7 @@ __global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, MT)) void attenti
       }
     }
   }
-  if (!direct || !a.w_out) return;
+  if (!alone || !a.w_out) return;
   __syncthreads();
   for (int base = 0; base < a.cap_tiles; base += kThreads) {  // whole waves: lanes add to each other
     const int tile = base + (int)threadIdx.x;
@@ -1245,7 +1246,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
   __shared__ __attribute__((aligned(16))) f32x4 s_sum[kGroups][kVec];
   __shared__ float s_f[kWaves][kMaxParts];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const uint32_t out_rows = a.n_units * a.unit_rows.d;
+  const uint32_t out_rows = a.n_parts == a.n_units ? 0u : a.n_units * a.unit_rows.d;
   const uint32_t out_blocks = a.wave_rows ? (out_rows + kWaves - 1) / kWaves : out_rows;
   if (blockIdx.x < out_blocks && a.wave_rows) {
     const uint32_t x = blockIdx.x * kWaves + wave, unit = quotient(x, a.unit_rows);
@@ -1843,12 +1844,12 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
       steps * units < (1ull << 31))  // the sums of share_out
     s->n_parts = (uint32_t)(std::min<uint64_t>(slots, units * ((steps + kWaves - 1) / kWaves + 1)) / s->m_groups *
                             s->m_groups);
-  const bool direct = s->n_parts == s->n_units && s->m_groups <= 1;
-  const uint64_t parts = direct ? 0 : (uint64_t)s->n_parts * s->unit_rows;
-  s->ml_at = parts * head_dim * 4;
-  s->of_at = s->ml_at + parts * 8;
+  const bool whole = s->n_parts == s->n_units, alone = whole && s->m_groups <= 1;
+  const uint64_t parts = (uint64_t)s->n_parts * s->unit_rows;
+  s->ml_at = whole ? 0 : parts * head_dim * 4;
+  s->of_at = s->ml_at + (alone || (whole && !weights) ? 0 : parts * 8);
   s->mass_at = (s->of_at + (s->n_parts != s->n_units ? units * 8 : 0) + 15) / 16 * 16;
-  s->mass_in_lds = direct && (uint64_t)s->unit_rows * s->cap_tiles <= (uint64_t)kLdsMass;
+  s->mass_in_lds = alone && (uint64_t)s->unit_rows * s->cap_tiles <= (uint64_t)kLdsMass;
   s->bytes = s->mass_at + (weights && !s->mass_in_lds ? units * s->unit_rows * s->cap_tiles * 4 : 0);
   if (units * s->unit_rows > kMaxGrid / 2 ||
       (weights && n_rows * (((uint64_t)s->cap_tiles + kWave - 1) / kWave) > kMaxGrid / 2))
@@ -1858,14 +1859,14 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
 
 template <int DJ, bool F16, int MT>
 void launch_attention(const Attention& a, uint64_t n_rows, hipStream_t st) {
-  const bool direct = a.n_parts == a.n_units && a.m_groups.d == 1;
+  const bool whole = a.n_parts == a.n_units;
   if (a.n_units && a.m_groups.d == 1)
     hipLaunchKernelGGL((attention_kernel<DJ, F16, MT, true>), dim3(a.n_parts), dim3(kThreads), 0, st, a);
   if constexpr (MT == kQueryTiles)  // only such units are one of several
     if (a.m_groups.d > 1)
       hipLaunchKernelGGL((attention_kernel<DJ, F16, MT, false>), dim3(a.n_parts), dim3(kThreads), 0, st, a);
-  if (direct) return;
-  const uint64_t out_rows = (uint64_t)a.n_units * a.unit_rows.d;
+  if (whole && (a.m_groups.d == 1 || !a.w_out)) return;
+  const uint64_t out_rows = whole ? 0 : (uint64_t)a.n_units * a.unit_rows.d;
   const uint64_t blocks = (a.wave_rows ? (out_rows + kWaves - 1) / kWaves : out_rows) + (a.w_out ? n_rows * a.weight_blocks.d : 0);
   if (blocks)
     hipLaunchKernelGGL((combine_kernel<DJ, F16, MT>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a);
