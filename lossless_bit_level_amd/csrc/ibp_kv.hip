@@ -1454,7 +1454,8 @@ __global__ __launch_bounds__(THREADS, 8) void evict_kernel(Evict e) {
   const Choice c = choice_of(e, blockIdx.x);
   if (threadIdx.x == 0) e.lengths_out[blockIdx.x] = c.len - (int)((c.held - c.left) << e.page_shift);
   // Buffers that end with the row: what lies past it is read as 0 and not
-  // written, without a branch for each.
+  // written, without a branch for each.  The whole offset is the lane's: a scalar
+  // one would take no part in the check.
   const uint32_t bytes = e.max_pages * 4u;
   const auto weights = row_buffer(e.weights + c.at, bytes), weights_out = row_buffer(e.weights_out + c.at, bytes);
   const auto pages = row_buffer(e.pages + c.at, bytes), pages_out = row_buffer(e.pages_out + c.at, bytes);
@@ -1462,9 +1463,9 @@ __global__ __launch_bounds__(THREADS, 8) void evict_kernel(Evict e) {
   // everything is asked for at once; the ids arrive while the places are worked out
   uint32_t w[R], id[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) w[i] = __builtin_amdgcn_raw_buffer_load_b32(weights, mine, i * THREADS * 4, 0);
+  for (int i = 0; i < R; ++i) w[i] = __builtin_amdgcn_raw_buffer_load_b32(weights, mine + i * THREADS * 4, 0, 0);
 #pragma unroll
-  for (int i = 0; i < R; ++i) id[i] = __builtin_amdgcn_raw_buffer_load_b32(pages, mine, i * THREADS * 4, 0);
+  for (int i = 0; i < R; ++i) id[i] = __builtin_amdgcn_raw_buffer_load_b32(pages, mine + i * THREADS * 4, 0, 0);
   const uint32_t span = c.full ? c.hi - c.lo : 0u;
   uint32_t low = 0xFFFFFFFFu, high = 0;
 #pragma unroll

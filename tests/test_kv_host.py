@@ -4,6 +4,7 @@ anything is enqueued (these calls never launch a kernel)."""
 import ctypes
 import os
 import re
+import shutil
 import subprocess
 import sys
 
@@ -122,6 +123,32 @@ def test_exports_every_declared_symbol():
     L = ctypes.CDLL(LIB)
     for n in names:
         assert hasattr(L, n), n
+
+
+@built
+def test_eviction_buffers_bound_every_access(tmp_path):
+    """The eviction reads and writes its rows through buffers that end with the
+    row.  A buffer's scalar offset takes no part in its bounds check, so that
+    every access of the built kernels has it 0."""
+    objdump = "/opt/rocm/llvm/bin/llvm-objdump"
+    if not os.path.exists(objdump):
+        pytest.skip("no llvm-objdump")
+    copy = shutil.copy(LIB, tmp_path)
+    subprocess.run([objdump, "--offloading", copy], cwd=tmp_path, check=True, capture_output=True, timeout=60)
+    image = [f for f in os.listdir(tmp_path) if f.endswith("gfx950")]
+    assert len(image) == 1
+    text = subprocess.run([objdump, "-d", "--mcpu=gfx950", image[0]], cwd=tmp_path, check=True, capture_output=True,
+                          text=True, timeout=60).stdout
+    kernels = 0
+    for kernel in re.split(r"\n(?=[0-9a-f]+ <)", text):
+        if "evict_kernel" not in kernel.split("\n", 1)[0]:
+            continue
+        kernels += 1
+        found = re.findall(r"\tbuffer_(load|store)_dword(?:x\d)? \w+(?:\[[\d:]+\])?, v\d+, s\[\d+:\d+\], (\w+) offen", kernel)
+        assert {"load", "store"} <= {what for what, _ in found}
+        assert len(found) == kernel.count("\tbuffer_") - kernel.count("\tbuffer_inv") - kernel.count("\tbuffer_wb")
+        assert {offset for _, offset in found} == {"0"}
+    assert kernels == 3
 
 
 @pytest.fixture(scope="module")
