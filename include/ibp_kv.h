@@ -59,7 +59,7 @@
  * synchronisation; a caller may capture it in a HIP graph), arguments are
  * checked on the host before anything is enqueued, statuses are those of
  * ibp.h, and a HIP error that is pending at entry is returned and left
- * pending.  Device data (ids, lengths, counts, scales) is not checked on the
+ * pending.  The buffers and the stream are the current device's.  Device data (ids, lengths, counts, scales) is not checked on the
  * host; no value of it makes a kernel read or write outside the buffers.
  * Buffers that a call writes must not overlap what it reads, except where
  * said.  Equal inputs give equal bytes.

@@ -1,7 +1,8 @@
 // The binding of libibp_kv's calls to torch tensors: checks of the arguments,
 // tensors for the results, and the call of the C ABI (include/ibp_kv.h).  Its
 // functions stand behind those of the same names in ibp_kv.py.  No step of an
-// operator is computed here.
+// operator is computed here.  A call runs on the GPU of its tensors, whichever
+// is current.
 //
 // Marshalled by ctypes a short call took the host longer than the kernel takes:
 // an append 10.0 us back to back, 5.3 us so; attention over 291 tokens 12.9 and
@@ -13,9 +14,11 @@
 
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <c10/core/DeviceGuard.h>
 
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 
 #include "ibp_kv.h"
 
@@ -42,6 +45,53 @@ bool check(const Tensor& t, ScalarType type, const char* name) {
   PyErr_Format(PyExc_ValueError, "%s must be a contiguous %s GPU tensor", name,
                type == ScalarType::Int ? "int32" : type == ScalarType::Float ? "float32" : "uint8");
   return false;
+}
+
+// The GPU of the arguments `o` that are GPU tensors, which has to be one: a
+// kernel runs on one GPU, with their addresses as they are.  What is no GPU
+// tensor is left to the checks that follow.
+struct Argument {
+  PyObject* o;
+  const char* name;
+};
+
+bool same_gpu(std::initializer_list<Argument> arguments, c10::Device* gpu) {
+  bool known = false;
+  for (const Argument& x : arguments) {
+    if (!x.o || !THPVariable_Check(x.o) || !THPVariable_Unpack(x.o).is_cuda()) continue;
+    const c10::Device d = THPVariable_Unpack(x.o).device();
+    if (known && d != *gpu) {
+      refuse("%s must be on the same GPU as the call's other tensors", x.name);
+      return false;
+    }
+    *gpu = d;
+    known = true;
+  }
+  return true;
+}
+
+// Makes a GPU current for the call.  (Most often it is: asking costs less than
+// setting it.)
+struct OnGpu {
+  explicit OnGpu(c10::Device gpu) {
+    if (c10::impl::getDeviceGuardImpl(gpu.type())->getDevice() != gpu) guard_.reset_device(gpu);
+  }
+  c10::OptionalDeviceGuard guard_;
+};
+
+// The first of the tensors that a cache holds on to, which are all on one GPU (a
+// borrowed reference, good as long as the cache); null for a structure that was
+// filled by hand.
+PyObject* tensor_of_cache(PyObject* cache) {
+  static PyObject* const name = PyUnicode_InternFromString("tensors");
+  PyObject* held = PyObject_GetAttr(cache, name);
+  if (!held) {
+    PyErr_Clear();
+    return nullptr;
+  }
+  PyObject* first = PyTuple_Check(held) && PyTuple_GET_SIZE(held) ? PyTuple_GET_ITEM(held, 0) : nullptr;
+  Py_DECREF(held);
+  return first;
 }
 
 bool check(PyObject* o, ScalarType type, const char* name) {
@@ -151,7 +201,10 @@ bool arguments(Py_ssize_t n, Py_ssize_t want) {
 PyObject* set_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   uint64_t page_tokens, head_dim;
-  if (!arguments(n, 7) || !check(a[1], ScalarType::Byte, "k_codes") ||
+  c10::Device gpu(c10::kCUDA, 0);
+  if (!arguments(n, 7) ||
+      !same_gpu({{a[1], "k_codes"}, {a[2], "k_scales"}, {a[3], "v_codes"}, {a[4], "v_scales"}}, &gpu) ||
+      !check(a[1], ScalarType::Byte, "k_codes") ||
       !check(a[2], ScalarType::Float, "k_scales") || !check(a[3], ScalarType::Byte, "v_codes") ||
       !check(a[4], ScalarType::Float, "v_scales") || !number(a[5], &page_tokens) || !number(a[6], &head_dim))
     return nullptr;
@@ -181,14 +234,18 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   uint32_t dtype;
   const int32_t* counts;
   void* stream;
-  if (!arguments(n, 7) || !check_type(a[3], "k", &dtype) || !from_structure(a[0], &cache) ||
-      !check_table(a[1], a[2], &table))
+  c10::Device gpu(c10::kCUDA, 0);
+  if (!arguments(n, 7) ||
+      !same_gpu({{tensor_of_cache(a[0]), "the cache"}, {a[1], "pages"}, {a[2], "lengths"}, {a[3], "k"}, {a[4], "v"},
+                 {a[5], "counts"}}, &gpu) ||
+      !check_type(a[3], "k", &dtype) || !from_structure(a[0], &cache) || !check_table(a[1], a[2], &table))
     return nullptr;
   const Tensor& x = THPVariable_Unpack(a[3]);
   const int64_t shape[4] = {(int64_t)table.n_seqs, x.size(1), (int64_t)table.kv_heads, cache.head_dim};
   if (!check_rows(a[3], "k", x.scalar_type(), shape, &k) || !check_rows(a[4], "v", x.scalar_type(), shape, &v) ||
       !check_counts(a[5], table.n_seqs, &counts) || !stream_of(a[6], &stream))
     return nullptr;
+  const OnGpu on(gpu);
   return PyLong_FromLong(ibp_kv_append(&cache, &table, dtype, (uint64_t)shape[1], &k, &v, counts, stream));
   END_HANDLE_TH_ERRORS
 }
@@ -203,8 +260,11 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   uint32_t dtype;
   const int32_t* counts;
   void* stream;
-  if (!arguments(n, 11) || !check_type(a[3], "q", &dtype) || !from_structure(a[0], &cache) ||
-      !check_table(a[1], a[2], &table))
+  c10::Device gpu(c10::kCUDA, 0);
+  if (!arguments(n, 11) ||
+      !same_gpu({{tensor_of_cache(a[0]), "the cache"}, {a[1], "pages"}, {a[2], "lengths"}, {a[3], "q"}, {a[5], "weights"},
+                 {a[6], "weights_out"}, {a[7], "counts"}, {a[8], "out"}, {a[9], "workspace"}}, &gpu) ||
+      !check_type(a[3], "q", &dtype) || !from_structure(a[0], &cache) || !check_table(a[1], a[2], &table))
     return nullptr;
   const Tensor& x = THPVariable_Unpack(a[3]);
   const Tensor& pages = THPVariable_Unpack(a[1]);
@@ -232,6 +292,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       (a[9] != Py_None && !check(a[9], ScalarType::Byte, "workspace")) || !stream_of(a[10], &stream))
     return nullptr;
 
+  const OnGpu on(gpu);
   const Tensor out = a[8] != Py_None ? THPVariable_Unpack(a[8]) : at::empty(shape, x.options());
   if (a[8] == Py_None) o = {out.data_ptr(), out.stride(0), out.stride(1), out.stride(2)};
   Tensor weights_out;
@@ -264,7 +325,12 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   ibp_kv_table table;
   uint64_t page_tokens, keep, sink, recent;
   void* stream;
-  if (!arguments(n, 11) || !check_table(a[0], a[2], &table)) return nullptr;
+  c10::Device gpu(c10::kCUDA, 0);
+  if (!arguments(n, 11) ||
+      !same_gpu({{a[0], "pages"}, {a[1], "weights"}, {a[2], "lengths"}, {a[7], "pages_out"}, {a[8], "weights_out"},
+                 {a[9], "lengths_out"}}, &gpu) ||
+      !check_table(a[0], a[2], &table))
+    return nullptr;
   const Tensor &pages = THPVariable_Unpack(a[0]), &lengths = THPVariable_Unpack(a[2]);
   if (!check_like(a[1], ScalarType::Float, "weights", pages) || !number(a[3], &page_tokens) || !number(a[4], &keep) ||
       !number(a[5], &sink) || !number(a[6], &recent) ||
@@ -273,6 +339,7 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
       (a[9] != Py_None && !check_like(a[9], ScalarType::Int, "lengths_out", lengths)) || !stream_of(a[10], &stream))
     return nullptr;
   const Tensor& weights = THPVariable_Unpack(a[1]);
+  const OnGpu on(gpu);
   const Tensor p = a[7] != Py_None ? THPVariable_Unpack(a[7]) : at::empty_like(pages);
   const Tensor w = a[8] != Py_None ? THPVariable_Unpack(a[8]) : at::empty_like(weights);
   const Tensor l = a[9] != Py_None ? THPVariable_Unpack(a[9]) : at::empty_like(lengths);

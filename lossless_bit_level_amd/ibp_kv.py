@@ -129,6 +129,13 @@ def _stream(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else 0
 
 
+def _on(stream, t: torch.Tensor):
+    """stream= as the current stream, for a call on t's GPU."""
+    if t.is_cuda and stream.device != t.device:
+        raise ValueError(f"stream of another GPU: {stream.device}, tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
 def ibp_kv_append(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Tensor,
                   k: torch.Tensor, v: torch.Tensor, counts: torch.Tensor | None = None,
                   stream=None):
@@ -137,9 +144,9 @@ def ibp_kv_append(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Tenso
     their rows.  pages: int32 [n_seqs, kv_heads, max_pages]; lengths: int32
     [n_seqs, kv_heads], the new tokens counted in; counts: int32 [n_seqs], how
     many of the n_new tokens each sequence brings (default: all).
-    Asynchronous on the current stream, or on stream=."""
+    Asynchronous on the current stream of the tensors' GPU, or on stream=."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, pages):
             return ibp_kv_append(cache, pages, lengths, k, v, counts)
     _check("ibp_kv_append",
            _ext().append(cache, pages, lengths, k, v, counts, _stream(pages)))
@@ -149,8 +156,9 @@ def ibp_kv_attention_workspace_bytes(cache: ibp_kv_cache, pages: torch.Tensor,
                                      lengths: torch.Tensor, q_heads: int, n_new: int,
                                      with_weights: bool) -> int:
     table = ibp_kv_table(*pages.shape, pages.data_ptr(), lengths.data_ptr())
-    return int(lib().ibp_kv_attention_workspace_bytes(cache, table, q_heads, n_new,
-                                                      int(with_weights)))
+    with torch.cuda.device_of(pages):
+        return int(lib().ibp_kv_attention_workspace_bytes(cache, table, q_heads, n_new,
+                                                          int(with_weights)))
 
 
 def ibp_kv_attention(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Tensor,
@@ -167,9 +175,9 @@ def ibp_kv_attention(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Te
     tensor.  workspace: a uint8 GPU tensor of at least
     ibp_kv_attention_workspace_bytes (default: allocated).  Returns
     (out, weights_out), the second None without weights.  Asynchronous on the
-    current stream, or on stream=."""
+    current stream of the tensors' GPU, or on stream=."""
     if stream is not None:  # what the call allocates is the stream's too
-        with torch.cuda.stream(stream):
+        with _on(stream, pages):
             return ibp_kv_attention(cache, pages, lengths, q, scale, weights, weights_out, counts,
                                     out, workspace)
     status, out, weights_out = _ext().attention(cache, pages, lengths, q, scale, weights,
@@ -186,9 +194,10 @@ def ibp_kv_evict(pages: torch.Tensor, weights: torch.Tensor, lengths: torch.Tens
     recent_pages and the heaviest between.  Returns (pages, weights, lengths)
     with the kept pages first, the evicted ones after them (weight 0) and the
     row's other entries as they were.  The outputs must not overlap the
-    inputs.  Asynchronous on the current stream, or on stream=."""
+    inputs.  Asynchronous on the current stream of the tensors' GPU, or on
+    stream=."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, pages):
             return ibp_kv_evict(pages, weights, lengths, page_tokens, keep_pages, sink_pages,
                                 recent_pages, pages_out, weights_out, lengths_out)
     status, *out = _ext().evict(pages, weights, lengths, page_tokens, keep_pages, sink_pages,

@@ -305,3 +305,50 @@ def test_missing_library_raises(tmp_path):
             "kv._LIB_PATH = '/nonexistent/libibp_kv.so'\n"
             "try:\n    kv.lib()\nexcept RuntimeError as e:\n    assert 'is missing' in str(e)\nelse:\n    raise SystemExit(1)\n")
     assert subprocess.run([sys.executable, "-c", code], cwd=ROOT, timeout=120).returncode == 0
+
+
+def test_binding_refuses_tensors_of_two_gpus(kv):
+    """The kernels run on one GPU with the addresses as they are: no tensor of
+    a call may be another GPU's, nor may the stream.  (Tensors without memory;
+    nothing is launched.)"""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    ext = kv._ext()
+
+    class Stream:
+        device = torch.device("cuda", 0)
+
+    with FakeTensorMode(allow_non_fake_inputs=True):
+        def make(i, shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=f"cuda:{i}")
+
+        def both(shape, dtype=torch.float32):
+            return make(0, shape, dtype), make(1, shape, dtype)
+        codes, scales = both((8, 2048), torch.uint8), both((8,))
+        pages, lengths = both((2, 2, 2), torch.int32), both((2, 2), torch.int32)
+        weights, counts = both((2, 2, 2)), both((2,), torch.int32)
+        x, q, workspace = both((2, 1, 2, 128), torch.float16), both((2, 1, 4, 128), torch.float16), both((64,), torch.uint8)
+
+        def each(call, args):
+            """Every tensor but the first from the other GPU, in turn."""
+            for i, a in enumerate(args):
+                if i and isinstance(a, tuple):
+                    mixed = [(b[i == j] if isinstance(b, tuple) else b) for j, b in enumerate(args)]
+                    with pytest.raises(ValueError, match="same GPU"):
+                        call(*mixed)
+        plain = cache(kv)
+        each(lambda *a: ext.set_cache(plain, *a), (codes, scales, codes, scales, 16, 128))
+        each(lambda *a: ext.append(plain, *a), (pages, lengths, x, x, counts, 0))
+        each(lambda *a: ext.attention(plain, *a), (pages, lengths, q, None, weights, weights, counts, q, workspace, 0))
+        each(ext.evict, (pages, weights, lengths, 16, 2, 1, 1, pages, weights, lengths, 0))
+        # the cache's own tensors
+        plain.tensors = (codes[1], scales[1], codes[1], scales[1])
+        with pytest.raises(ValueError, match="same GPU"):
+            ext.append(plain, pages[0], lengths[0], x[0], x[0], None, 0)
+        with pytest.raises(ValueError, match="same GPU"):
+            ext.attention(plain, pages[0], lengths[0], q[0], None, None, None, None, None, None, 0)
+        # the stream
+        for call in (lambda: kv.ibp_kv_append(plain, pages[1], lengths[1], x[1], x[1], stream=Stream),
+                     lambda: kv.ibp_kv_attention(plain, pages[1], lengths[1], q[1], stream=Stream),
+                     lambda: kv.ibp_kv_evict(pages[1], weights[1], lengths[1], 16, 2, stream=Stream)):
+            with pytest.raises(ValueError, match="stream of another GPU"):
+                call()
