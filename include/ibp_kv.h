@@ -61,6 +61,9 @@
  * ibp.h, and a HIP error that is pending at entry is returned and left
  * pending.  The buffers and the stream are the current device's.  Device data (ids, lengths, counts, scales) is not checked on the
  * host; no value of it makes a kernel read or write outside the buffers.
+ * A call whose rows need more threads than a launch has (2^32: some 2^24 rows
+ * of an eviction or of attention, 2^22 rows of 1025-16384 pages of an eviction)
+ * is an invalid argument.
  * Buffers that a call writes must not overlap what it reads, except where
  * said.  Equal inputs give equal bytes.
  */

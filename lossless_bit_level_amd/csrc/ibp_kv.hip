@@ -1710,7 +1710,8 @@ int launched() {
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
-constexpr uint64_t kMaxGrid = 0x7FFFFFFFull;
+// Workgroups of a launch, which has fewer than 2^32 threads.
+constexpr uint64_t max_grid(uint64_t threads) { return 0xFFFFFFFFull / threads; }
 
 int check_cache(const ibp_kv_cache* c) {
   if (!c) return IBP_ERR_INVALID_ARGUMENT;
@@ -1796,7 +1797,9 @@ struct Shape {
   int mt;
   int32_t m_rows, m_groups, unit_rows, cap_tiles;
   uint32_t n_units, n_parts;
-  bool mass_in_lds;
+  uint32_t weight_blocks;  // of a row, in the joining kernel
+  uint32_t join_blocks;    // workgroups of the joining kernel; 0: it is not launched
+  bool wave_rows, mass_in_lds;
   uint64_t of_at, mass_at, ml_at, bytes;  // in the workspace; the sums come first
 };
 
@@ -1831,7 +1834,7 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
   s->unit_rows = (int32_t)std::min<uint64_t>(m, per_unit);
   s->cap_tiles = (int32_t)(max_pages * page_tokens / kTile);
   const uint64_t units = n_rows * s->m_groups;
-  if (units > kMaxGrid / 64) return false;
+  if (units > max_grid(kThreads)) return false;
   s->n_units = (uint32_t)units;
   // As many parts as keep all workgroups on the chip at once: what comes after them would start over with an empty pipeline.  Rows
   // of up to four steps a wave are not worth the second launch, which costs
@@ -1852,31 +1855,33 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
   s->mass_at = (s->of_at + (s->n_parts != s->n_units ? units * 8 : 0) + 15) / 16 * 16;
   s->mass_in_lds = alone && (uint64_t)s->unit_rows * s->cap_tiles <= (uint64_t)kLdsMass;
   s->bytes = s->mass_at + (weights && !s->mass_in_lds ? units * s->unit_rows * s->cap_tiles * 4 : 0);
-  if (units * s->unit_rows > kMaxGrid / 2 ||
-      (weights && n_rows * (((uint64_t)s->cap_tiles + kWave - 1) / kWave) > kMaxGrid / 2))
-    return false;
-  return true;
+  // The joining kernel: output rows of units that were cut, weights of rows whose
+  // workgroups do not finish them.
+  const uint64_t out_rows = whole ? 0 : units * s->unit_rows;
+  const uint32_t block_tiles = s->unit_rows > kFewRows ? kWave : kThreads;
+  s->wave_rows = s->n_parts <= 8ull * s->n_units;
+  s->weight_blocks = ((uint32_t)s->cap_tiles + block_tiles - 1) / block_tiles;
+  const uint64_t join = (s->wave_rows ? (out_rows + kWaves - 1) / kWaves : out_rows) +
+                        (weights && !(whole && s->m_groups == 1) ? n_rows * s->weight_blocks : 0);
+  s->join_blocks = (uint32_t)join;
+  return join <= max_grid(kThreads);
 }
 
 template <int DJ, bool F16, int MT>
-void launch_attention(const Attention& a, uint64_t n_rows, hipStream_t st) {
-  const bool whole = a.n_parts == a.n_units;
+void launch_attention(const Attention& a, uint32_t join_blocks, hipStream_t st) {
   if (a.n_units && a.m_groups.d == 1)
     hipLaunchKernelGGL((attention_kernel<DJ, F16, MT, true>), dim3(a.n_parts), dim3(kThreads), 0, st, a);
   if constexpr (MT == kQueryTiles)  // only such units are one of several
     if (a.m_groups.d > 1)
       hipLaunchKernelGGL((attention_kernel<DJ, F16, MT, false>), dim3(a.n_parts), dim3(kThreads), 0, st, a);
-  if (whole && (a.m_groups.d == 1 || !a.w_out)) return;
-  const uint64_t out_rows = whole ? 0 : (uint64_t)a.n_units * a.unit_rows.d;
-  const uint64_t blocks = (a.wave_rows ? (out_rows + kWaves - 1) / kWaves : out_rows) + (a.w_out ? n_rows * a.weight_blocks.d : 0);
-  if (blocks)
-    hipLaunchKernelGGL((combine_kernel<DJ, F16, MT>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a);
+  if (join_blocks)
+    hipLaunchKernelGGL((combine_kernel<DJ, F16, MT>), dim3(join_blocks), dim3(kThreads), 0, st, a);
 }
 
 template <int DJ, bool F16>
-void launch_attention_mt(const Attention& a, int mt, uint64_t n_rows, hipStream_t st) {
-  if (mt == 1) return launch_attention<DJ, F16, 1>(a, n_rows, st);
-  launch_attention<DJ, F16, kQueryTiles>(a, n_rows, st);
+void launch_attention_mt(const Attention& a, const Shape& s, hipStream_t st) {
+  if (s.mt == 1) return launch_attention<DJ, F16, 1>(a, s.join_blocks, st);
+  launch_attention<DJ, F16, kQueryTiles>(a, s.join_blocks, st);
 }
 
 bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
@@ -1915,7 +1920,8 @@ int ibp_kv_append(const ibp_kv_cache* cache, const ibp_kv_table* table, uint32_t
   if (!aligned(counts, 4)) return IBP_ERR_LAYOUT;
   const uint64_t pt = cache->page_tokens;
   const uint64_t per_row = std::min<uint64_t>((n_new + pt - 2) / pt + 1, table->max_pages);
-  if (per_row > kMaxGrid / n_rows) return IBP_ERR_INVALID_ARGUMENT;
+  const uint64_t per_group = (uint64_t)kWaves * kTile / pt;
+  if (per_row > max_grid(kThreads) * per_group / n_rows) return IBP_ERR_INVALID_ARGUMENT;
   rc = pending_hip_error();
   if (rc) return rc;
   const Pool pool = make_pool(cache);
@@ -1994,22 +2000,21 @@ int ibp_kv_attention(const ibp_kv_cache* cache, const ibp_kv_table* table, uint3
   a.unit_rows = make_divisor((uint32_t)s.unit_rows);
   a.cap_tiles = s.cap_tiles;
   a.mass_in_lds = s.mass_in_lds;
-  a.wave_rows = s.n_parts <= 8ull * s.n_units;
+  a.wave_rows = s.wave_rows;
   a.n_units = s.n_units;
   a.n_rows = (uint32_t)n_rows;
   a.n_parts = s.n_parts;
-  const uint32_t block_tiles = s.unit_rows > kFewRows ? kWave : kThreads;
-  a.weight_blocks = make_divisor(((uint32_t)s.cap_tiles + block_tiles - 1) / block_tiles);
+  a.weight_blocks = make_divisor(s.weight_blocks);
   hipStream_t st = (hipStream_t)stream;
   switch (cache->head_dim / 64 * 2 + dtype) {
-    case 2: launch_attention_mt<1, false>(a, s.mt, n_rows, st); break;
-    case 3: launch_attention_mt<1, true>(a, s.mt, n_rows, st); break;
-    case 4: launch_attention_mt<2, false>(a, s.mt, n_rows, st); break;
-    case 5: launch_attention_mt<2, true>(a, s.mt, n_rows, st); break;
-    case 6: launch_attention_mt<3, false>(a, s.mt, n_rows, st); break;
-    case 7: launch_attention_mt<3, true>(a, s.mt, n_rows, st); break;
-    case 8: launch_attention_mt<4, false>(a, s.mt, n_rows, st); break;
-    default: launch_attention_mt<4, true>(a, s.mt, n_rows, st); break;
+    case 2: launch_attention_mt<1, false>(a, s, st); break;
+    case 3: launch_attention_mt<1, true>(a, s, st); break;
+    case 4: launch_attention_mt<2, false>(a, s, st); break;
+    case 5: launch_attention_mt<2, true>(a, s, st); break;
+    case 6: launch_attention_mt<3, false>(a, s, st); break;
+    case 7: launch_attention_mt<3, true>(a, s, st); break;
+    case 8: launch_attention_mt<4, false>(a, s, st); break;
+    default: launch_attention_mt<4, true>(a, s, st); break;
   }
   return launched();
 }
@@ -2035,7 +2040,8 @@ int ibp_kv_evict(const ibp_kv_table* table, uint32_t page_tokens, uint64_t keep_
     for (int j = 0; j < 3; ++j)
       if (overlap(in[i], size[i], outs[j], size[j]) || (i < j && overlap(outs[i], size[i], outs[j], size[j])))
         return IBP_ERR_INVALID_ARGUMENT;
-  if (n_rows > kMaxGrid) return IBP_ERR_INVALID_ARGUMENT;
+  const bool wide = table->max_pages > 1024 && table->max_pages <= 16384;  // 1024 threads a row
+  if (n_rows > max_grid(wide ? 1024 : kThreads)) return IBP_ERR_INVALID_ARGUMENT;
   rc = pending_hip_error();
   if (rc) return rc;
   Evict e;

@@ -352,3 +352,37 @@ def test_binding_refuses_tensors_of_two_gpus(kv):
                      lambda: kv.ibp_kv_evict(pages[1], weights[1], lengths[1], 16, 2, stream=Stream)):
             with pytest.raises(ValueError, match="stream of another GPU"):
                 call()
+
+
+def test_grids_beyond_a_launch_are_refused(kv):
+    """A launch has fewer than 2^32 threads: calls that need 2^24 workgroups of
+    256 threads, or 2^22 of 1024, are refused before anything is enqueued."""
+    L, INV = kv.lib(), kv.IBP_ERR_INVALID_ARGUMENT
+    far = [FAKE + (i << 44) for i in range(6)]
+    many = 1 << 24
+
+    def evict(n, m):
+        return L.ibp_kv_evict(table(kv, n=n, h=1, m=m, pages=far[0], lengths=far[1]), 16, 3, 1, 1, far[2], far[3], far[4], far[5], None)
+    assert evict(many, 2) == INV and evict(many, 1024) == INV
+    assert evict(many >> 2, 1025) == INV and evict(many >> 2, 4097) == INV
+    assert evict(many, 16385) == INV
+
+    def append(n, pt, new=1, m=3):
+        return L.ibp_kv_append(cache(kv, pt=pt), table(kv, n=n, h=1, m=m), 0, new, tensor(kv), tensor(kv), None, None)
+    for pt in (16, 32, 64):
+        assert append(many * (64 // pt), pt) == INV
+    assert append(1 << 12, 64, new=64 << 12, m=1 << 14) == INV
+
+    def attention(n, heads=1, new=1, m=3, weights=None):
+        return L.ibp_kv_attention(cache(kv), table(kv, n=n, h=1, m=m), 0, heads, new, tensor(kv), tensor(kv), None, 0.1,
+                                  weights, weights, FAKE, (1 << 64) - 1, None)
+
+    def workspace(n, heads=1, new=1, m=3, weights=0):
+        return L.ibp_kv_attention_workspace_bytes(cache(kv), table(kv, n=n, h=1, m=m), heads, new, weights)
+    assert attention(many) == INV
+    assert attention(many >> 8, heads=16, new=1 << 9) == INV                       # 256 units a row
+    assert attention(many >> 8, heads=16, new=4, m=1 << 14, weights=FAKE) == INV   # the joining of weights
+    assert attention(many >> 6, new=0, m=1 << 14, weights=FAKE) == INV
+    assert workspace(many >> 8, heads=16, new=4, m=1 << 14, weights=1) == 0
+    # without a joining launch these rows are no more than the others
+    assert workspace(many >> 6, m=1 << 14, weights=1) > 0
