@@ -2,7 +2,7 @@
 // tensors for the results, and the call of the C ABI (include/ibp_kv.h).  Its
 // functions stand behind those of the same names in ibp_kv.py.  No step of an
 // operator is computed here.  A call runs on the GPU of its tensors, whichever
-// is current.
+// is current; going backward through its results raises.
 //
 // Marshalled by ctypes a short call took the host longer than the kernel takes:
 // an append 10.0 us back to back, 5.3 us so; attention over 291 tokens 12.9 and
@@ -10,8 +10,11 @@
 #include <Python.h>
 
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
 #include <c10/core/DeviceGuard.h>
@@ -19,6 +22,8 @@
 #include <cmath>
 #include <cstring>
 #include <initializer_list>
+#include <memory>
+#include <vector>
 
 #include "ibp_kv.h"
 
@@ -79,19 +84,69 @@ struct OnGpu {
   c10::OptionalDeviceGuard guard_;
 };
 
-// The first of the tensors that a cache holds on to, which are all on one GPU (a
-// borrowed reference, good as long as the cache); null for a structure that was
-// filled by hand.
-PyObject* tensor_of_cache(PyObject* cache) {
+// The tensors that a cache holds on to, a tuple (a borrowed reference, good as
+// long as the cache); null for a structure that was filled by hand.
+PyObject* tensors_of_cache(PyObject* cache) {
   static PyObject* const name = PyUnicode_InternFromString("tensors");
   PyObject* held = PyObject_GetAttr(cache, name);
   if (!held) {
     PyErr_Clear();
     return nullptr;
   }
-  PyObject* first = PyTuple_Check(held) && PyTuple_GET_SIZE(held) ? PyTuple_GET_ITEM(held, 0) : nullptr;
   Py_DECREF(held);
-  return first;
+  return PyTuple_Check(held) ? held : nullptr;
+}
+
+// The first of them: they are all on one GPU.
+PyObject* tensor_of_cache(PyObject* cache) {
+  PyObject* held = tensors_of_cache(cache);
+  return held && PyTuple_GET_SIZE(held) ? PyTuple_GET_ITEM(held, 0) : nullptr;
+}
+
+// ---- autograd: no call has a gradient ----
+
+bool wants_gradient(PyObject* o) {
+  return o && THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad() && at::GradMode::is_enabled();
+}
+
+// Inputs that require a gradient give results whose backward pass raises, not
+// results that count as constants.  Results written to a given tensor cannot say
+// so; like torch's functions with out= the calls refuse them.
+class Gradients {
+ public:
+  Gradients(const char* call, std::initializer_list<PyObject*> inputs) : call_(call) {
+    for (PyObject* o : inputs)
+      if (wants_gradient(o)) wanted_.push_back(THPVariable_Unpack(o));
+  }
+
+  bool check_given(std::initializer_list<Argument> outputs) const {
+    for (const Argument& x : outputs) {
+      if (x.o == Py_None || (wanted_.empty() && !wants_gradient(x.o))) continue;
+      PyErr_Format(PyExc_ValueError, "%s: %s is given, but one of the tensors requires a gradient, which this call does not have", call_,
+                   x.name);
+      return false;
+    }
+    return true;
+  }
+
+  void mark(std::initializer_list<Tensor> outputs) const {
+    if (wanted_.empty()) return;
+    const auto raises = std::make_shared<torch::autograd::NotImplemented>(call_, torch::autograd::collect_next_edges(wanted_));
+    for (const Tensor& t : outputs)
+      if (t.defined()) torch::autograd::set_history(t, raises);
+  }
+
+ private:
+  const char* call_;
+  std::vector<Tensor> wanted_;
+};
+
+// A given tensor that a call writes has changed (tensors of inference mode keep
+// no count of that).
+void written(PyObject* o) {
+  if (!o || !THPVariable_Check(o)) return;
+  const Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 bool check(PyObject* o, ScalarType type, const char* name) {
@@ -246,6 +301,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !check_counts(a[5], table.n_seqs, &counts) || !stream_of(a[6], &stream))
     return nullptr;
   const OnGpu on(gpu);
+  if (PyObject* held = tensors_of_cache(a[0]))
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(held); ++i) written(PyTuple_GET_ITEM(held, i));
   return PyLong_FromLong(ibp_kv_append(&cache, &table, dtype, (uint64_t)shape[1], &k, &v, counts, stream));
   END_HANDLE_TH_ERRORS
 }
@@ -263,8 +320,10 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   c10::Device gpu(c10::kCUDA, 0);
   if (!arguments(n, 11) ||
       !same_gpu({{tensor_of_cache(a[0]), "the cache"}, {a[1], "pages"}, {a[2], "lengths"}, {a[3], "q"}, {a[5], "weights"},
-                 {a[6], "weights_out"}, {a[7], "counts"}, {a[8], "out"}, {a[9], "workspace"}}, &gpu) ||
-      !check_type(a[3], "q", &dtype) || !from_structure(a[0], &cache) || !check_table(a[1], a[2], &table))
+                 {a[6], "weights_out"}, {a[7], "counts"}, {a[8], "out"}, {a[9], "workspace"}}, &gpu))
+    return nullptr;
+  const Gradients gradients("ibp_kv_attention", {a[3], a[5]});
+  if (!gradients.check_given({{a[8], "out"}, {a[6], "weights_out"}}) || !check_type(a[3], "q", &dtype) || !from_structure(a[0], &cache) || !check_table(a[1], a[2], &table))
     return nullptr;
   const Tensor& x = THPVariable_Unpack(a[3]);
   const Tensor& pages = THPVariable_Unpack(a[1]);
@@ -303,11 +362,14 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   } else if (const uint64_t bytes = ibp_kv_attention_workspace_bytes(&cache, &table, (uint64_t)q_heads, (uint64_t)n_new, weighted)) {
     workspace = at::empty({(int64_t)bytes}, x.options().dtype(at::kByte));
   }
+  written(a[8]);
+  written(a[6]);
   const int status = ibp_kv_attention(
       &cache, &table, dtype, (uint64_t)q_heads, (uint64_t)n_new, &q, &o, counts, scale,
       weighted ? (const float*)THPVariable_Unpack(a[5]).data_ptr() : nullptr,
       weighted ? (float*)weights_out.data_ptr() : nullptr, workspace.defined() ? workspace.data_ptr() : nullptr,
       workspace.defined() ? (uint64_t)workspace.numel() : 0, stream);
+  gradients.mark({out, weights_out});
   PyObject* w = Py_None;
   Py_INCREF(w);
   if (weighted) {
@@ -328,9 +390,10 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   c10::Device gpu(c10::kCUDA, 0);
   if (!arguments(n, 11) ||
       !same_gpu({{a[0], "pages"}, {a[1], "weights"}, {a[2], "lengths"}, {a[7], "pages_out"}, {a[8], "weights_out"},
-                 {a[9], "lengths_out"}}, &gpu) ||
-      !check_table(a[0], a[2], &table))
+                 {a[9], "lengths_out"}}, &gpu))
     return nullptr;
+  const Gradients gradients("ibp_kv_evict", {a[1]});
+  if (!gradients.check_given({{a[8], "weights_out"}}) || !check_table(a[0], a[2], &table)) return nullptr;
   const Tensor &pages = THPVariable_Unpack(a[0]), &lengths = THPVariable_Unpack(a[2]);
   if (!check_like(a[1], ScalarType::Float, "weights", pages) || !number(a[3], &page_tokens) || !number(a[4], &keep) ||
       !number(a[5], &sink) || !number(a[6], &recent) ||
@@ -343,9 +406,11 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor p = a[7] != Py_None ? THPVariable_Unpack(a[7]) : at::empty_like(pages);
   const Tensor w = a[8] != Py_None ? THPVariable_Unpack(a[8]) : at::empty_like(weights);
   const Tensor l = a[9] != Py_None ? THPVariable_Unpack(a[9]) : at::empty_like(lengths);
+  for (int i = 7; i < 10; ++i) written(a[i]);
   const int status = ibp_kv_evict(&table, (uint32_t)std::min<uint64_t>(page_tokens, 0xFFFFFFFFull), keep, sink, recent,
                                   (const float*)weights.data_ptr(), (int32_t*)p.data_ptr(), (float*)w.data_ptr(),
                                   (int32_t*)l.data_ptr(), stream);
+  gradients.mark({w});
   return Py_BuildValue("(iNNN)", status, THPVariable_Wrap(p), THPVariable_Wrap(w), THPVariable_Wrap(l));
   END_HANDLE_TH_ERRORS
 }

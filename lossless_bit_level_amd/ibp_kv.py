@@ -8,6 +8,10 @@ tensors through a small extension module (csrc/ibp_kv_torch.cpp), since a
 decoding step makes many short ones: it checks the arguments, allocates
 results and calls the C ABI.  If either has not been built this module raises
 on first use; there is no fallback.
+
+No call has a gradient.  Codes and scales carry none; going backward through a
+result of inputs that require one raises, and a given output with such inputs
+is refused.
 """
 from __future__ import annotations
 

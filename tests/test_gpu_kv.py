@@ -632,3 +632,78 @@ def test_example_runs_them_together(kv):
     # weights of pages that are not held are 0
     held = -(-lengths.long() // 16)
     assert not weights[torch.arange(weights.shape[2], device="cuda") >= held[..., None]].any()
+
+
+# ------------------------------------------------------------- autograd ----
+
+
+def test_going_backward_through_a_result_raises(kv):
+    """No call has a gradient: a result of inputs that require one says so when
+    it is asked for, instead of counting as a constant."""
+    p = filled(kv, 1, 2, 10, 16, 64, [100], seed=1)
+    lengths = torch.full((1, 2), 100, dtype=torch.int32, device="cuda")
+    q = torch.randn(1, 1, 4, 64, device="cuda").bfloat16().requires_grad_()
+    w = torch.rand(1, 2, 10, device="cuda")
+    plain, plain_w = kv.ibp_kv_attention(p.cache, p.gpu_pages, lengths, q.detach(), weights=w)
+    assert not plain.requires_grad and not plain_w.requires_grad
+    out, wo = kv.ibp_kv_attention(p.cache, p.gpu_pages, lengths, q * 1, weights=w)
+    assert torch.equal(out.detach(), plain) and torch.equal(wo.detach(), plain_w)
+    for x in (out, wo):
+        with pytest.raises(RuntimeError, match="ibp_kv_attention is not implemented"):
+            x.float().sum().backward()
+    assert q.grad is None
+    with torch.no_grad():
+        out, wo = kv.ibp_kv_attention(p.cache, p.gpu_pages, lengths, q, weights=w, weights_out=w.clone())
+    assert not out.requires_grad and torch.equal(out, plain) and torch.equal(wo, plain_w)
+    pages, left, _ = kv.ibp_kv_evict(p.gpu_pages, w.clone().requires_grad_(), lengths, 16, 3)
+    assert not pages.requires_grad
+    with pytest.raises(RuntimeError, match="ibp_kv_evict is not implemented"):
+        left.sum().backward()
+    # codes are whole numbers: they have no gradient, as torch's own casts to such
+    k = torch.randn(1, 1, 2, 64, device="cuda").bfloat16().requires_grad_()
+    kv.ibp_kv_append(p.cache, p.gpu_pages, lengths, k, k)
+    assert not any(t.requires_grad for t in p.t)
+
+
+def test_given_outputs_without_a_gradient(kv):
+    """As torch's functions with out=."""
+    p = filled(kv, 1, 2, 10, 16, 64, [100], seed=1)
+    lengths = torch.full((1, 2), 100, dtype=torch.int32, device="cuda")
+    q, w = torch.randn(1, 1, 4, 64, device="cuda").bfloat16(), torch.rand(1, 2, 10, device="cuda")
+    for bad in (dict(q=q.clone().requires_grad_(), out=q.clone()), dict(q=q, out=q.clone().requires_grad_()),
+                dict(q=q, weights=w.clone().requires_grad_(), weights_out=w.clone()),
+                dict(q=q.clone().requires_grad_(), weights=w, weights_out=w)):
+        with pytest.raises(ValueError, match="requires a gradient"):
+            kv.ibp_kv_attention(p.cache, p.gpu_pages, lengths, bad.pop("q"), **bad)
+    with pytest.raises(ValueError, match="requires a gradient"):
+        kv.ibp_kv_evict(p.gpu_pages, w.clone().requires_grad_(), lengths, 16, 3, weights_out=w.clone())
+
+
+def test_written_tensors_have_a_new_version(kv):
+    """What a call writes in place counts as changed, so that autograd notices
+    where it had been saved."""
+    p = filled(kv, 1, 2, 10, 16, 64, [100], seed=1)
+    lengths = torch.full((1, 2), 100, dtype=torch.int32, device="cuda")
+    q, w = torch.randn(1, 1, 4, 64, device="cuda").bfloat16(), torch.rand(1, 2, 10, device="cuda")
+    k = torch.randn(1, 1, 2, 64, device="cuda").bfloat16()
+    out, wo = torch.empty_like(q), w.clone()
+    given = [torch.empty_like(x) for x in (p.gpu_pages, w, lengths)]
+
+    def versions(*tensors):
+        return [t._version for t in tensors]
+    before = versions(*p.t, out, wo, *given)
+    kv.ibp_kv_append(p.cache, p.gpu_pages, lengths, k, k)
+    kv.ibp_kv_attention(p.cache, p.gpu_pages, lengths, q, weights=w, weights_out=wo, out=out)
+    kv.ibp_kv_evict(p.gpu_pages, w, lengths, 16, 3, pages_out=given[0], weights_out=given[1], lengths_out=given[2])
+    assert all(x > y for x, y in zip(versions(*p.t, out, wo, *given), before))
+    only_read = (p.gpu_pages, lengths, q, w, k)
+    assert versions(*only_read) == [0] * len(only_read)
+    x = torch.rand(1, 2, 10, device="cuda", requires_grad=True)
+    y = (x * wo).sum()                        # wo saved for the backward pass
+    kv.ibp_kv_attention(p.cache, p.gpu_pages, lengths, q, weights=w, weights_out=wo)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():              # tensors that have no version
+        a, b = kv.ibp_kv_attention(p.cache, p.gpu_pages, lengths, q, weights=w)
+        kv.ibp_kv_attention(p.cache, p.gpu_pages, lengths, q, weights=b, weights_out=b, out=a)
+    kv.ibp_kv_attention(p.cache, p.gpu_pages, lengths, q, weights=b, weights_out=b, out=a)

@@ -386,3 +386,20 @@ def test_grids_beyond_a_launch_are_refused(kv):
     assert workspace(many >> 8, heads=16, new=4, m=1 << 14, weights=1) == 0
     # without a joining launch these rows are no more than the others
     assert workspace(many >> 6, m=1 << 14, weights=1) > 0
+
+
+def test_binding_refuses_given_outputs_of_a_gradient(kv):
+    """(Tensors without memory; nothing is launched.)"""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    ext, plain = kv._ext(), cache(kv)
+    with FakeTensorMode():
+        def make(*shape, dtype=torch.float32):
+            return torch.empty(shape, dtype=dtype, device="cuda:0")
+        pages, lengths, w = make(2, 2, 2, dtype=torch.int32), make(2, 2, dtype=torch.int32), make(2, 2, 2)
+        q, grown = make(2, 1, 4, 128, dtype=torch.float16), make(2, 1, 4, 128, dtype=torch.float16).requires_grad_()
+        for args in ((grown, None, None, None, None, q), (q, None, None, None, None, grown), (grown, None, w, w, None, None),
+                     (q, None, w, make(2, 2, 2).requires_grad_(), None, None)):
+            with pytest.raises(ValueError, match="requires a gradient"):
+                ext.attention(plain, pages, lengths, *args, None, 0)
+        with pytest.raises(ValueError, match="requires a gradient"):
+            ext.evict(pages, make(2, 2, 2).requires_grad_(), lengths, 16, 2, 1, 1, None, w, None, 0)
