@@ -151,7 +151,7 @@ uint64_t ibp_kv_attention_workspace_bytes(const ibp_kv_cache *cache, const ibp_k
  * zeros.  Scores, statistics and sums are held in 32 bits, the sums up to 2^8
  * times their normalised value for each token of the row: values above about
  * 2^119 / (tokens of the row) may overflow.  What a query may not see does not
- * reach it, NaN included.
+ * reach it, NaN included.  Values whose scale is not finite are NaN.
  *
  * weights, weights_out (both or neither; float, [n_seqs][kv_heads][max_pages];
  * they may be the same buffer): weights_out = weights + the w_j that the

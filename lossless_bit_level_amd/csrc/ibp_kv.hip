@@ -859,7 +859,8 @@ struct Probs {
 // Takes out of a step what its queries may not see: scores become minus
 // infinity, value bytes that no query sees (they may hold anything) 0.  A NaN
 // value that only some of the queries see is 0 to the products, and those that
-// see it get NaN here.
+// see it get NaN here; so do values of a scale that is not finite, which would
+// make a NaN of an unseen token's weight of 0.
 template <int DJ, int MT, int ST>
 __device__ __forceinline__ void mask_step(const Plan& p, int step, int lane, const int (&seen)[MT],
                                           Where<ST>& w, f32x4 (&s)[MT][ST], u32x4 (&v)[ST][DJ],
@@ -872,14 +873,15 @@ __device__ __forceinline__ void mask_step(const Plan& p, int step, int lane, con
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (!w.ok[t] || at + 16 * t + r >= seen[mt]) s[mt][t][r] = -INFINITY;
-    if (!w.ok[t]) w.vs[t] = 0.f;
+    const uint32_t odd = finite(w.vs[t]) ? 0u : 0x7F7F7F7Fu;  // NaN's code
+    if (!w.ok[t] || odd) w.vs[t] = 0.f;
     const uint32_t inside = w.ok[t] ? byte_mask(p.end - (at + 16 * t)) : 0u;
     uint32_t any = 0;
 #pragma unroll
     for (int h = 0; h < DJ; ++h)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        v[t][h][c] &= inside;
+        v[t][h][c] = (v[t][h][c] | odd) & inside;
         any |= nan_codes(v[t][h][c]);
       }
     if (__ballot(any != 0)) {

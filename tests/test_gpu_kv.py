@@ -707,3 +707,28 @@ def test_written_tensors_have_a_new_version(kv):
         a, b = kv.ibp_kv_attention(p.cache, p.gpu_pages, lengths, q, weights=w)
         kv.ibp_kv_attention(p.cache, p.gpu_pages, lengths, q, weights=b, weights_out=b, out=a)
     kv.ibp_kv_attention(p.cache, p.gpu_pages, lengths, q, weights=b, weights_out=b, out=a)
+
+
+# --------------------------------------------------------- scales that are not finite ----
+
+
+@pytest.mark.parametrize("d,group", [(64, 2), (128, 4), (256, 5)])
+@pytest.mark.parametrize("scale", [float("nan"), float("inf")])
+def test_attention_scale_not_finite_stays_with_those_who_see_it(kv, d, group, scale):
+    """A page whose scale is not finite (no append writes one) reaches the
+    queries that see a token of it and no earlier one; a page that no query
+    sees reaches none."""
+    pt, n, new = 16, 101, 7                       # the page from 96 on: seen by the last five
+    p = filled(kv, 1, 1, 9, pt, d, [n], seed=6)
+    for pool in (p.k, p.v):
+        pool[1][p.pages[0, 0, 7:]] = scale        # past the row's end
+    p.v[1][p.pages[0, 0, 6]] = scale
+    p.upload()
+    q = torch.randn(1, new, group, d, generator=torch.Generator().manual_seed(1)).bfloat16()
+    w = np.zeros((1, 1, 9), np.float32)
+    out, wo = run_attention(kv, p, [[n]], q, w)
+    assert out[:, 2:].isnan().all()
+    p.v[1][p.pages[0, 0, 6]] = 1.0
+    want = expect(p, [[n]], q, w)
+    close(out[:, :2], None, (want[0][:, :2], None, want[2][:, :2], None))
+    close(out[:, :0], wo, (want[0][:, :0], want[1], want[2][:, :0], want[3]))
