@@ -68,10 +68,17 @@ def main(seqs=4, heads=8, group=4, d=128, prompt=2048, steps=64, keep=96, seed=0
     weights = torch.zeros(seqs, heads, m, device=dev)
     lengths = torch.full((seqs, heads), prompt, dtype=torch.int32, device=dev)
 
-    # which archive row a pool page was filled from, -1 for tokens of the answer
+    # which archive row a pool page holds, -1 for tokens of the answer, and which
+    # rows have been given up (the last entry is no row's)
     rows = torch.arange(seqs * heads * per_head, device=dev).reshape(seqs, heads, per_head)
     source = torch.full((n_pages,), -1, dtype=torch.int64, device=dev)
     source[pages[..., :per_head].long()] = rows
+    given_up = torch.zeros(rows.numel() + 1, dtype=torch.bool, device=dev)
+    place = torch.arange(m, device=dev)
+
+    def held(lengths):
+        """Places of the table that hold tokens, [seqs, heads, m]."""
+        return place < -(-lengths // PAGE)[..., None]
 
     # the prompt: archive -> 16-bit pages -> 8-bit pages
     shape = (seqs, heads, prompt, d)
@@ -82,6 +89,8 @@ def main(seqs=4, heads=8, group=4, d=128, prompt=2048, steps=64, keep=96, seed=0
     for _ in range(steps):
         q = torch.randn(seqs, 1, heads * group, d, generator=gen, device=dev).to(torch.bfloat16)
         lengths += 1
+        begun = pages.gather(2, ((lengths - 1) // PAGE)[..., None].long())[..., 0].long()
+        source[begun] = torch.where((lengths - 1) % PAGE == 0, -1, source[begun])  # a page filled anew
         ibp_kv.ibp_kv_append(cache, pages, lengths, random_kv(gen, seqs, 1, heads, d),
                              random_kv(gen, seqs, 1, heads, d))
         out, weights = ibp_kv.ibp_kv_attention(cache, pages, lengths, q, weights=weights,
@@ -90,19 +99,21 @@ def main(seqs=4, heads=8, group=4, d=128, prompt=2048, steps=64, keep=96, seed=0
         pages, weights, lengths = ibp_kv.ibp_kv_evict(pages, weights, lengths, PAGE, keep_pages=keep,
                                                       sink_pages=1, recent_pages=4)
         evicted += (before - lengths).sum() // PAGE
+        given_up[torch.where(held(before) & ~held(lengths), source[pages.long()], -1)] = True
 
-    # what the first head gave up, from the archive: the original bits
-    held = -(-int(lengths[0, 0]) // PAGE)
-    gone = source[pages[0, 0, held:].long()]
-    gone = gone[(gone >= 0) & (gone < per_head)]
+    # what the heads gave up, from the archive: the original bits.  With what they
+    # still hold these are the prompt's pages, each once.
+    gone = given_up[:-1].nonzero()[:, 0]
+    kept = source[pages.long()][held(lengths)]
+    assert torch.equal(torch.cat([gone, kept[kept >= 0]]).sort()[0], rows.reshape(-1))
     for x, a in ((k, k_arch), (v, v_arch)):
-        want = x[0, :, 0].reshape(per_head, PAGE, d)[gone]
+        want = x.transpose(1, 2).reshape(-1, PAGE, d)[gone]
         assert torch.equal(restore(a, gone, d).view(torch.int16), want.view(torch.int16))
     if not quiet:
         print(f"archive: {k_ratio:.3f} (keys) and {v_ratio:.3f} (values) of the 16-bit pages, in host memory")
         print(f"{steps} steps of {seqs} sequences: {int(evicted)} pages given up, "
               f"{int(lengths.sum())} tokens held in {seqs * heads} heads, "
-              f"{len(gone)} pages of the first head fetched back bit for bit")
+              f"{len(gone)} pages of the prompt fetched back bit for bit")
     return out, lengths, weights
 
 

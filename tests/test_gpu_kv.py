@@ -732,3 +732,52 @@ def test_attention_scale_not_finite_stays_with_those_who_see_it(kv, d, group, sc
     want = expect(p, [[n]], q, w)
     close(out[:, :2], None, (want[0][:, :2], None, want[2][:, :2], None))
     close(out[:, :0], wo, (want[0][:, :0], want[1], want[2][:, :0], want[3]))
+
+
+# ------------------------------------------------------------- the example ----
+
+
+def test_example_fetches_back_every_page_given_up(kv, monkeypatch):
+    """What the example asks of its archive at the end, against a record of its
+    calls: every page of the prompt that some head gave up, though the places of
+    such pages were filled again, and given up again, meanwhile."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "kv_decode.py")
+    spec = importlib.util.spec_from_file_location("kv_decode", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    seqs, heads, prompt, pt = 2, 3, 320, example.PAGE
+    asked, filled_from, gone, again = [], {}, set(), 0
+    append, evict, restore = kv.ibp_kv_append, kv.ibp_kv_evict, example.restore
+
+    def recorded_append(cache, pages, lengths, k, v, **more):
+        ids, ends = np_of(pages), np_of(lengths)
+        for s, h in np.ndindex(ends.shape):
+            first = int(ends[s, h]) - k.shape[1]
+            for at in range(-(-first // pt), -(-int(ends[s, h]) // pt)):   # pages that these tokens begin
+                row = (s * heads + h) * (prompt // pt) + at if k.shape[1] == prompt else None
+                filled_from[int(ids[s, h, at])] = row
+        return append(cache, pages, lengths, k, v, **more)
+
+    def recorded_evict(pages, weights, lengths, *args, **more):
+        nonlocal again
+        out = evict(pages, weights, lengths, *args, **more)
+        ids, was, now = np_of(out[0]), np_of(lengths), np_of(out[2])
+        for s, h in np.ndindex(was.shape):
+            for page in ids[s, h, -(-int(now[s, h]) // pt):-(-int(was[s, h]) // pt)]:
+                row = filled_from.pop(int(page))
+                again += row is None
+                gone.update([] if row is None else [row])
+        return out
+
+    def recorded_restore(arch, ids, d):
+        asked.append(ids.tolist())
+        return restore(arch, ids, d)
+    monkeypatch.setattr(example.ibp_kv, "ibp_kv_append", recorded_append)
+    monkeypatch.setattr(example.ibp_kv, "ibp_kv_evict", recorded_evict)
+    monkeypatch.setattr(example, "restore", recorded_restore)
+    example.main(seqs=seqs, heads=heads, group=2, prompt=prompt, steps=150, keep=7, quiet=True)
+    assert again and len(gone) > seqs * heads * (prompt // pt - 7)
+    assert len(asked) == 4 and asked[2] == asked[3]
+    assert sorted(asked[2]) == sorted(gone)
