@@ -106,7 +106,8 @@ typedef struct ibp_kv_table {
 
 /* A 16-bit tensor [n_seqs][n_new][heads][head_dim]: element (s, i, h, d) is
  * at data + s * seq_stride + i * token_stride + h * head_stride + d, strides
- * in elements, any sign, 0 for a broadcast input.  Rows whose address and
+ * in elements, any sign, 0 for a broadcast input; rows of an output must not lie
+ * on each other.  Rows whose address and
  * strides are multiples of 16 bytes are moved 16 bytes at a time, others
  * element by element. */
 typedef struct ibp_kv_tensor {

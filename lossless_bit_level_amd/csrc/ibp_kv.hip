@@ -1744,6 +1744,12 @@ int check_tensor(const ibp_kv_tensor* x) {
   return aligned(x->data, 2) ? IBP_OK : IBP_ERR_LAYOUT;
 }
 
+// Whether rows of `d` elements lie on each other along one axis, as those of a
+// broadcast tensor do.
+bool rows_overlap(uint64_t size, int64_t stride, uint32_t d) {
+  return size > 1 && stride < (int64_t)d && stride > -(int64_t)d;
+}
+
 Pool make_pool(const ibp_kv_cache* c) {
   Pool p;
   p.k_codes = c->k_codes;
@@ -1972,6 +1978,10 @@ int ibp_kv_attention(const ibp_kv_cache* cache, const ibp_kv_table* table, uint3
   if (q_heads == 0 || q_heads % table->kv_heads || !weights != !weights_out || !(scale - scale == 0.f))
     return IBP_ERR_INVALID_ARGUMENT;
   if (n_new && ((rc = check_tensor(q)) || (rc = check_tensor(out)))) return rc;
+  if (n_new && (rows_overlap(table->n_seqs, out->seq_stride, cache->head_dim) ||
+                rows_overlap(n_new, out->token_stride, cache->head_dim) ||
+                rows_overlap(q_heads, out->head_stride, cache->head_dim)))
+    return IBP_ERR_INVALID_ARGUMENT;
   if (!aligned(counts, 4) || !aligned(weights, 4) || !aligned(weights_out, 4)) return IBP_ERR_LAYOUT;
   if (!aligned(workspace, 16)) return IBP_ERR_LAYOUT;
   Shape s;

@@ -403,3 +403,20 @@ def test_binding_refuses_given_outputs_of_a_gradient(kv):
                 ext.attention(plain, pages, lengths, *args, None, 0)
         with pytest.raises(ValueError, match="requires a gradient"):
             ext.evict(pages, make(2, 2, 2).requires_grad_(), lengths, 16, 2, 1, 1, None, w, None, 0)
+
+
+def test_attention_refuses_rows_on_each_other(kv):
+    """An output whose rows share memory, a broadcast one among them, would hold
+    whichever workgroup came last."""
+    f, INV = kv.lib().ibp_kv_attention, kv.IBP_ERR_INVALID_ARGUMENT
+
+    def call(out, q=None, new=2, ws=None):
+        """With too little workspace at the end, so that nothing is launched."""
+        return f(cache(kv), table(kv, m=4096), 0, 4, new, tensor(kv) if q is None else q, kv.ibp_kv_tensor(FAKE, *out), None, 0.1,
+                 None, None, FAKE + 4 if ws is None else ws, 0, None)
+    for out in ((0, 512, 128), (1024, 0, 128), (1024, 512, 0), (1024, 512, 127), (1024, -127, 128), (64, 512, 128)):
+        assert call(out) == INV
+    LAY = kv.IBP_ERR_LAYOUT     # the workspace's, which is looked at next
+    assert call((1024, 512, 128)) == LAY and call((-1024, 512, -128)) == LAY
+    assert call((1024, 0, 128), new=1) == LAY
+    assert call((1024, 512, 128), q=kv.ibp_kv_tensor(FAKE, 0, 0, 0)) == LAY    # inputs may be broadcast
