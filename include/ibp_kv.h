@@ -107,9 +107,8 @@ typedef struct ibp_kv_table {
 /* A 16-bit tensor [n_seqs][n_new][heads][head_dim]: element (s, i, h, d) is
  * at data + s * seq_stride + i * token_stride + h * head_stride + d, strides
  * in elements, any sign, 0 for a broadcast input; rows of an output must not lie
- * on each other.  Rows whose address and
- * strides are multiples of 16 bytes are moved 16 bytes at a time, others
- * element by element. */
+ * on each other.  Rows whose address and strides are multiples of 16 bytes are
+ * moved 16 bytes at a time, others element by element. */
 typedef struct ibp_kv_tensor {
   void *data;
   int64_t seq_stride;
@@ -151,8 +150,11 @@ uint64_t ibp_kv_attention_workspace_bytes(const ibp_kv_cache *cache, const ibp_k
  * every score is minus infinity), and one past its sequence's count, gets
  * zeros.  Scores, statistics and sums are held in 32 bits, the sums up to 2^8
  * times their normalised value for each token of the row: values above about
- * 2^119 / (tokens of the row) may overflow.  What a query may not see does not
- * reach it, NaN included.  Values whose scale is not finite are NaN.
+ * 2^119 / (tokens of the row) may overflow.  The w_j enter the second product
+ * with 16 bits, and a page's share of them is the exponential of a difference of
+ * 32-bit logarithms (a relative error of about 2^-23 times the largest score).
+ * What a query may not see does not reach it, NaN included.  Values whose scale
+ * is not finite are NaN.
  *
  * weights, weights_out (both or neither; float, [n_seqs][kv_heads][max_pages];
  * they may be the same buffer): weights_out = weights + the w_j that the

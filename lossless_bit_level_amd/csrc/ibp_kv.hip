@@ -35,16 +35,16 @@ constexpr int step_tiles(int dj, int mt) { return dj * mt <= 1 ? 4 : 2; }
 // accumulators, queries and tiles on the way fill the registers.
 constexpr int workgroups_per_unit(int dj, int mt) { return dj * mt <= 4 ? 2 : 1; }
 // The most groups of 16 query rows that a unit takes.  128 dims, 64 query rows, 4
-// x 8 heads x 14,000 tokens: 55 us as two units of 32, 71 us as one of 64 (both
-// launches); 64 dims: 43 and 46 us; 256 dims, 24 rows: 44 us as one unit, 56 us
+// x 8 heads x 14,000 tokens: 51 us as two units of 32, 59 us as one of 64 (both
+// launches); 64 dims: 40 and 43 us; 256 dims, 24 rows: 39 us as one unit, 48 us
 // as two of 16.
 constexpr int kQueryTiles = 2;
 constexpr int kUnit = 1024;     // bytes of a tile that one wide load of a wave takes
 constexpr float kGrowth = 8.f;  // log2 of how far exponentials may exceed the scale of the sums
 constexpr int kMaxParts = 512;  // workgroups that the chip holds at once, at most
 // Query rows of a unit that one thread adds up for its tile.  8 rows of 131k
-// tokens: 5.5 us so, 9.9 us with the rows spread over the waves; 64 rows of 14k:
-// 18 us so, 10 us spread.
+// tokens: 5.6 us so, 9.4 us with the rows spread over the waves; 64 rows of 14k:
+// 13.2 us so, 8.9 us spread.
 constexpr int kFewRows = 16;
 constexpr int kLdsMass = 4096;  // shares of tiles that a workgroup that works alone keeps in LDS
 constexpr int kExpMin = -126, kExpMax = 119;  // exponents of a page's scale
@@ -1039,11 +1039,12 @@ __device__ __forceinline__ void write_weight(const Attention& a, uint32_t row, i
 // Everything of a step stays in the wave's registers: the tiles' layouts give the
 // operands of the matrix instructions as they are loaded, and scores become
 // weights in place.  What it reads once bounds it: 16 x 32 heads x 4096 tokens of
-// 128 dims 85.7 us, 6.3 TB/s; two contexts of 131k and 91k tokens, 8 heads, 8
-// queries each, 80.6 us, 5.7 TB/s.  Short rows pay some 6 us for finding their
-// pages, the joining and the launch (291 tokens: 7.4 us); 72 ragged rows with 25
-// queries of 64 dims, 43 MB, take 16.8 us, a third of it vector instructions of the
-// steps (250 a step), a sixth those before and after.
+// 128 dims 85.4 us, 6.3 TB/s; two contexts of 131k and 91k tokens, 8 heads, 8
+// queries each, 80.7 us, 5.7 TB/s.  Short rows pay some 6 us for finding their
+// pages, the joining and the launch (291 tokens: 7.2 us); 72 ragged rows with 25
+// queries of 64 dims, 43 MB, take 16.4 us: vector instructions for half of the
+// cycles, a third in the steps (250 a step), a sixth before and after; matrix
+// instructions for 13%.
 template <int DJ, bool F16, int MT, bool ONCE>
 __global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, MT)) void attention_kernel(Attention a) {
   constexpr int D = 64 * DJ;
@@ -1235,9 +1236,9 @@ __device__ __forceinline__ void join_parts(const Attention& a, const Part& t, in
 
 // Joins the parts.  The first workgroups take a query row each, or one for each
 // of their waves where the units have few parts on average (264 units x 14 rows
-// in 2 parts: 11.4 us by workgroups, 7.5 us so); the others take 256 or 64 tiles
-// of a row each and sum their weights.  4-6 us, which is the latency of its three
-// loads that wait for each other.
+// in 2 parts, with weights: 11.9 us by workgroups, 7.6 us so); the others take 256 or 64 tiles
+// of a row each and sum their weights.  4-6 us with one unit to a head, which is the
+// latency of its three loads that wait for each other.
 template <int DJ, bool F16, int MT>
 __global__ __launch_bounds__(kThreads) void combine_kernel(Attention a) {
   constexpr int D = 64 * DJ;
@@ -1434,7 +1435,7 @@ __device__ __forceinline__ Choice choice_of(const Evict& e, uint32_t row) {
 // 768 rows spent 47 us on it.)  With the counts of every 64 pages in LDS each
 // page then knows its place.
 // 768 rows of 16,384 pages (153 MB for those held, 201 MB with the spare entries)
-// take 52 us: 1.5 workgroups to a place on the chip, and the loads, the choice and
+// take 51 us: 1.5 workgroups to a place on the chip, and the loads, the choice and
 // the stores of those that run together come one after the other (a row alone
 // takes 17 us).  Without the buffers' bounds, with a branch for each page, 59 us.
 template <int THREADS, int R>
@@ -1844,10 +1845,15 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
   const uint64_t units = n_rows * s->m_groups;
   if (units > max_grid(kThreads)) return false;
   s->n_units = (uint32_t)units;
-  // As many parts as keep all workgroups on the chip at once: what comes after them would start over with an empty pipeline.  Rows
-  // of up to four steps a wave are not worth the second launch, which costs
-  // about as much as those.  Units that nearly fill the chip are not cut either:
-  // 264 ragged rows of up to 4538 tokens took 48.8 us whole.
+  // As many parts as keep all workgroups on the chip at once: what comes after them
+  // would start over with an empty pipeline.  Rows of up to four steps a wave are
+  // not worth the second launch, which costs about as much as those.  Units that
+  // fill three quarters of the chip are cut for the sake of rows much longer than
+  // the others: of 264 rows of 128 dims and 14 query rows, one with 4538 tokens
+  // and the rest with 454, 17.1 us cut and 30.9 whole (384 rows: 22.1 and 31.7);
+  // rows of 454 to 4538 tokens pay the second launch for it, 42.4 us cut and 39.7
+  // whole (384 rows: 64.8 and 58.4).  Past that, and past the rows whose lengths
+  // share_out holds, every unit is a workgroup, whatever its row's length.
   const int st = step_tiles((int)head_dim / 64, s->mt);
   const uint64_t steps = (uint64_t)(s->cap_tiles + st - 1) / st;
   const uint64_t slots = std::min<uint64_t>((uint64_t)workgroups_per_unit((int)head_dim / 64, s->mt) * cus, kMaxParts);
@@ -2071,9 +2077,9 @@ int ibp_kv_evict(const ibp_kv_table* table, uint32_t page_tokens, uint64_t keep_
   e.recent = (uint32_t)std::min<uint64_t>(recent_pages, 0xFFFFFFFFull);
   const dim3 grid((uint32_t)n_rows);
   hipStream_t st = (hipStream_t)stream;
-  // The smallest that holds a row: 512 rows of 1024 pages take 8.1 us with 256
-  // threads and 10.7 with 1024, 512 rows of 4096 pages 14.3 us with 4 pages a
-  // thread and 22.4 with 16.
+  // The smallest that holds a row: 512 rows of 1024 pages take 7.7 us with 256
+  // threads and 10.8 with 1024, 512 rows of 4096 pages 14.2 us with 4 pages a
+  // thread and 21.6 with 16.  Past 16384 pages the keys no longer fit LDS.
   if (table->max_pages <= 1024)
     hipLaunchKernelGGL((evict_kernel<256, 4>), grid, dim3(256), 0, st, e);
   else if (table->max_pages <= 4096)
