@@ -1,7 +1,8 @@
-"""Build libibp.so (the IBP library), libibp_kv.so (the 8-bit KV page cache)
-and libibp_ceiling.so (the gather-copy floor the benchmark measures the IBP
-library against) in-tree with hipcc for gfx950, and _ibp_kv.so (libibp_kv's
-binding to torch tensors, host code only) with the host compiler.
+"""Build libibp.so (the IBP library), libibp_kv.so (the 8-bit KV page cache),
+libibp_kv_long.so (long and shared contexts over its pages) and
+libibp_ceiling.so (the gather-copy floor the benchmark measures the IBP
+library against) in-tree with hipcc for gfx950, and _ibp_kv.so (the binding of
+the two KV libraries to torch tensors, host code only) with the host compiler.
 
 Usage: python -m lossless_bit_level_amd.build
 """
@@ -19,6 +20,8 @@ SRC = os.path.join(PKG, "csrc", "ibp.hip")
 LIB = os.path.join(PKG, "libibp.so")
 KV_SRC = os.path.join(PKG, "csrc", "ibp_kv.hip")
 KV_LIB = os.path.join(PKG, "libibp_kv.so")
+KV_LONG_SRC = os.path.join(PKG, "csrc", "ibp_kv_long.hip")
+KV_LONG_LIB = os.path.join(PKG, "libibp_kv_long.so")
 KV_EXT_SRC = os.path.join(PKG, "csrc", "ibp_kv_torch.cpp")
 KV_EXT = os.path.join(PKG, "_ibp_kv.so")
 CEILING_SRC = os.path.join(PKG, "csrc", "ceiling.hip")
@@ -42,7 +45,7 @@ def command(out: str = LIB, extra=(), src: str = SRC) -> list[str]:
 
 
 def extension_command(out: str = KV_EXT, src: str = KV_EXT_SRC) -> list[str]:
-    """libibp_kv.so has to be built first: the module links to it."""
+    """The KV libraries have to be built first: the module links to them."""
     import torch
     torch_dir = os.path.dirname(torch.__file__)
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
@@ -51,6 +54,7 @@ def extension_command(out: str = KV_EXT, src: str = KV_EXT_SRC) -> list[str]:
             "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
             "-isystem", sysconfig.get_paths()["include"], src, "-o", out,
             "-L", os.path.join(torch_dir, "lib"), "-L", PKG, f"-l:{os.path.basename(KV_LIB)}",
+            f"-l:{os.path.basename(KV_LONG_LIB)}",
             "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
 
 
@@ -58,7 +62,7 @@ def build(verbose: bool = False) -> str:
     """Compile the libraries, side by side (always recompiles; the IBP
     library takes about a minute)."""
     jobs = []
-    for src, lib in ((SRC, LIB), (KV_SRC, KV_LIB), (CEILING_SRC, CEILING_LIB)):
+    for src, lib in ((SRC, LIB), (KV_SRC, KV_LIB), (KV_LONG_SRC, KV_LONG_LIB), (CEILING_SRC, CEILING_LIB)):
         cmd = command(lib + ".tmp", src=src)
         if verbose:
             print(" ".join(cmd), flush=True)

@@ -1,0 +1,1119 @@
+// libibp_kv_long: appends with rotated positions, outlines and selection of
+// pages, and attention over a shared prefix, on the 8-bit KV pages of libibp_kv,
+// for AMD Instinct MI355X (gfx950, CDNA4).  Calls: include/ibp_kv_long.h.
+#include "ibp_kv_core.h"
+
+#include "ibp_kv_long.h"
+
+namespace {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
+// ------------------------------------------------------------- rotation ----
+
+struct Angles {
+  const float* cos;
+  const float* sin;
+  const int32_t* positions;
+  uint32_t n_positions;
+  int32_t half;  // pairs
+};
+
+// Where the other number of a pair is: half a rotation away, which with all dims
+// of an even number of 64s rotated is in the same lane's registers, or next to it.
+enum class Pairs { kFar, kLane, kNeighbour };
+
+struct Floats8 {
+  float x[8];
+};
+
+template <bool F16>
+__device__ __forceinline__ Floats8 floats_of(u32x4 h) {
+  Floats8 r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r.x[i] = to_float<F16>((uint16_t)(h[i / 2] >> (i % 2 * 16)));
+  return r;
+}
+
+// Each product and each sum rounded: plain 32-bit arithmetic gives the same.
+__device__ __forceinline__ float turned_first(float x, float y, float c, float s) {
+#pragma clang fp contract(off)
+  const float a = x * c, b = y * s;
+  return a - b;
+}
+__device__ __forceinline__ float turned_second(float x, float y, float c, float s) {
+#pragma clang fp contract(off)
+  const float a = y * c, b = x * s;
+  return a + b;
+}
+
+template <Pairs PAIRS>
+struct Turn {
+  static constexpr bool kTurns = true;
+  Angles t;
+
+  __device__ __forceinline__ int position(const Rows& rows, uint32_t seq, int token, int place) const {
+    return t.positions ? t.positions[(uint64_t)seq * (uint32_t)rows.n_new + (uint32_t)token] : place;
+  }
+
+  // cos and sin of N pairs from pair `i` on (a multiple of 4); NaN outside the tables.
+  template <int N>
+  __device__ __forceinline__ void angles(int pos, int i, float (&c)[N], float (&s)[N]) const {
+    const bool in = (uint32_t)pos < t.n_positions;
+    const uint64_t at = (uint64_t)(in ? (uint32_t)pos : 0u) * (uint32_t)t.half + (uint32_t)i;
+#pragma unroll
+    for (int n = 0; n < N; n += 4) {
+      f32x4 a = {NAN, NAN, NAN, NAN}, b = a;
+      if (in) {
+        a = *(const f32x4*)(t.cos + at + n);
+        b = *(const f32x4*)(t.sin + at + n);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        c[n + r] = a[r];
+        s[n + r] = b[r];
+      }
+    }
+  }
+
+  // Eight numbers, whole pairs of neighbours, in place.
+  __device__ __forceinline__ void neighbours(int pos, int d, Floats8& f) const {
+    float c[4], s[4];
+    angles(pos, d / 2, c, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = f.x[2 * i], y = f.x[2 * i + 1];
+      f.x[2 * i] = turned_first(x, y, c[i], s[i]);
+      f.x[2 * i + 1] = turned_second(x, y, c[i], s[i]);
+    }
+  }
+
+  // Eight pairs from pair `i` on, in place.
+  __device__ __forceinline__ void pairs(int pos, int i, Floats8& a, Floats8& b) const {
+    float c[8], s[8];
+    angles(pos, i, c, s);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const float x = a.x[n], y = b.x[n];
+      a.x[n] = turned_first(x, y, c[n], s[n]);
+      b.x[n] = turned_second(x, y, c[n], s[n]);
+    }
+  }
+
+  // The lane's numbers of a key, dims 64 j + 16 g + 0..15, turned.  `key`: its dim
+  // 0; kx: what the lane has of it.
+  template <int DJ, bool F16>
+  __device__ __forceinline__ void keys(const uint16_t* key, bool wide, int g, int pos, const u32x4 (&kx)[DJ][2],
+                                       float (&ky)[DJ][16]) const {
+    if constexpr (PAIRS == Pairs::kLane) {
+#pragma unroll
+      for (int j = 0; j < DJ / 2; ++j)
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          Floats8 a = floats_of<F16>(kx[j][o]), b = floats_of<F16>(kx[j + DJ / 2][o]);
+          pairs(pos, 64 * j + 16 * g + 8 * o, a, b);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            ky[j][8 * o + i] = a.x[i];
+            ky[j + DJ / 2][8 * o + i] = b.x[i];
+          }
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < DJ; ++j)
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          const int d = 64 * j + 16 * g + 8 * o;
+          Floats8 a = floats_of<F16>(kx[j][o]);
+          if (d < 2 * t.half) {
+            if constexpr (PAIRS == Pairs::kNeighbour) {
+              neighbours(pos, d, a);
+            } else {
+              const bool first = d < t.half;
+              const int other = first ? d + t.half : d - t.half;
+              Floats8 b = floats_of<F16>(load8(key + other, wide));
+              float c[8], s[8];
+              angles(pos, first ? d : other, c, s);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                a.x[i] = first ? turned_first(a.x[i], b.x[i], c[i], s[i]) : turned_second(b.x[i], a.x[i], c[i], s[i]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ky[j][8 * o + i] = a.x[i];
+        }
+    }
+  }
+};
+
+struct Queries {
+  Strided q, out;
+  Divisor q_heads, group, n_new;
+  uint32_t n_items;  // 16 numbers of a query each
+};
+
+template <bool F16>
+__device__ __forceinline__ void store8(uint16_t* p, bool wide, const Floats8& f, bool there) {
+  u16x8 h;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = there ? to_half<F16>(f.x[i]) : (uint16_t)0;
+  if (wide) {
+    *(u16x8*)p = h;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = h[i];
+  }
+}
+
+// 16 numbers of a query: eight pairs, or what is not rotated.
+template <int DJ, bool F16, Pairs PAIRS>
+__device__ __forceinline__ void turn_query(const Queries& a, const Rows& rows, const Turn<PAIRS>& turn, uint32_t x) {
+  constexpr uint32_t kItems = 4 * DJ;
+  if (x >= a.n_items) return;
+  const uint32_t y = x / kItems;
+  const int item = (int)(x - y * kItems), half = turn.t.half;
+  const uint32_t t = quotient(y, a.q_heads), head = y - t * a.q_heads.d;
+  const uint32_t seq = quotient(t, a.n_new), i = t - seq * a.n_new.d;
+  const uint32_t row = seq * rows.heads.d + quotient(head, a.group);
+  const int count = new_count(rows, seq), place = row_length(rows, row) - count + (int)i;
+  const bool there = (int)i < count && place >= 0;
+  const bool rotated = PAIRS == Pairs::kNeighbour ? 16 * item < 2 * half : 8 * item < half;
+  int d0 = 16 * item, d1 = d0 + 8;
+  if (PAIRS != Pairs::kNeighbour) {
+    d0 = rotated ? 8 * item : 2 * half + 16 * (item - half / 8);
+    d1 = rotated ? d0 + half : d0 + 8;
+  }
+  const uint16_t* p = a.q.data + (int64_t)seq * a.q.seq + (int64_t)i * a.q.token + (int64_t)head * a.q.head;
+  uint16_t* to = a.out.data + (int64_t)seq * a.out.seq + (int64_t)i * a.out.token + (int64_t)head * a.out.head;
+  Floats8 f, g;
+  if (there) {
+    f = floats_of<F16>(load8(p + d0, a.q.wide));
+    g = floats_of<F16>(load8(p + d1, a.q.wide));
+    if (rotated) {
+      const int pos = turn.position(rows, seq, (int)i, place);
+      if constexpr (PAIRS == Pairs::kNeighbour) {
+        turn.neighbours(pos, d0, f);
+        turn.neighbours(pos, d1, g);
+      } else {
+        turn.pairs(pos, d0, f, g);
+      }
+    }
+  }
+  store8<F16>(to + d0, a.out.wide, f, there);
+  store8<F16>(to + d1, a.out.wide, g, there);
+}
+
+// The first workgroups append, the others rotate the queries.
+template <int DJ, bool F16, Pairs PAIRS>
+__global__ __launch_bounds__(kThreads) void append_rotated_kernel(Pool pool, Rows rows, Strided k, Strided v,
+                                                                  Divisor pages_per_row, uint32_t n_tasks,
+                                                                  Turn<PAIRS> turn, Queries queries,
+                                                                  uint32_t append_blocks) {
+  if (blockIdx.x < append_blocks)
+    append_tile<DJ, F16>(pool, rows, k, v, pages_per_row, n_tasks, turn);
+  else
+    turn_query<DJ, F16, PAIRS>(queries, rows, turn, (blockIdx.x - append_blocks) * kThreads + threadIdx.x);
+}
+
+// -------------------------------------------------------------- outline ----
+
+__device__ __forceinline__ f16x2 pair_max(f16x2 a, f16x2 b) { return __builtin_elementwise_max(a, b); }
+__device__ __forceinline__ f16x2 pair_min(f16x2 a, f16x2 b) { return __builtin_elementwise_min(a, b); }
+
+template <int CTRL>
+__device__ __forceinline__ f16x2 swapped(f16x2 x) {
+  return __builtin_bit_cast(f16x2, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
+}
+
+// Smallest e with a <= 127 * 2^e (127 = 1.984375 * 2^6), for a > 0.
+__device__ __forceinline__ int whole_exponent(float a) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, a);
+  return (int)(b >> 23) - 127 - 6 + ((b & 0x7FFFFFu) > 0x7E0000u ? 1 : 0);
+}
+
+// 16 dims of a page's keys to four lanes, which have a quarter of its tokens each:
+// neighbouring lanes read 64 bytes of neighbouring tokens.  e4m3 codes are exact in
+// 16 bits, two to an instruction.  What a page has no token for is read as its last
+// token, which changes neither the largest nor the smallest.
+template <int DJ>
+__global__ __launch_bounds__(kThreads) void outline_kernel(Pool pool, Rows rows, ibp_kv_outlines o,
+                                                           Divisor pages_per_row, uint32_t n_tasks) {
+  constexpr int D = 64 * DJ;
+  constexpr int kLanes = 16 * DJ, kPages = kWave / kLanes;  // of a wave
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const int sub = lane / kLanes, r = lane % kLanes, tq = r % 4;
+  const uint32_t task = (blockIdx.x * kWaves + wave) * kPages + sub;
+  const uint32_t line = quotient(min(task, n_tasks - 1), rows.heads);
+  const uint32_t head = min(task, n_tasks - 1) - line * rows.heads.d;
+  const uint32_t seq = quotient(line, pages_per_row), row = seq * rows.heads.d + head;
+  const int end = row_length(rows, row), count = new_count(rows, seq);
+  const int page_shift = 4 + (int)pool.tile_shift;
+  const int page = (max(end - count, 0) >> page_shift) + (int)(line - seq * pages_per_row.d);
+  const int n = min(end - (page << page_shift), 16 << pool.tile_shift);  // tokens
+  const bool reached = sub < kPages && task < n_tasks && count > 0 && page < (int)rows.max_pages && n > 0;
+  uint32_t id = ~0u;
+  if (reached) id = (uint32_t)rows.pages[(uint64_t)row * rows.max_pages + page];
+  const bool live = id < pool.n_pages;
+  f16x2 hi[8], lo[8];
+  uint32_t odd = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) hi[i] = lo[i] = f16x2{0, 0};
+  float scale = 0.f;
+  if (live) {
+    scale = pool.k_scales[id];
+    const uint8_t* p = pool.k_codes + (uint64_t)id * pool.page_bytes + (r / 4) * 256;
+    for (int tile = 0; tile * kTile < n; ++tile) {
+      u32x4 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = __builtin_nontemporal_load((const u32x4*)(p + tile * (kTile * D) + 16 * min(4 * i + tq, n - 1 - tile * kTile)));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          odd |= (w[i][x] & 0x7F7F7F7Fu) + 0x01010101u;
+          const f16x2 a = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i][x], 1.f, false));
+          const f16x2 b = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i][x], 1.f, true));
+          const bool first = i == 0 && tile == 0;
+          hi[2 * x] = first ? a : pair_max(hi[2 * x], a);
+          hi[2 * x + 1] = first ? b : pair_max(hi[2 * x + 1], b);
+          lo[2 * x] = first ? a : pair_min(lo[2 * x], a);
+          lo[2 * x + 1] = first ? b : pair_min(lo[2 * x + 1], b);
+        }
+    }
+  }
+  f16x2 top = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    hi[i] = pair_max(hi[i], swapped<0xB1>(hi[i]));
+    lo[i] = pair_min(lo[i], swapped<0xB1>(lo[i]));
+    hi[i] = pair_max(hi[i], swapped<0x4E>(hi[i]));
+    lo[i] = pair_min(lo[i], swapped<0x4E>(lo[i]));
+    top = pair_max(top, pair_max(hi[i], -lo[i]));  // of a magnitude: hi >= lo
+  }
+  float amax = fmaxf((float)top[0], (float)top[1]);
+  amax = fmaxf(amax, row_rotate<0x124>(amax));
+  amax = fmaxf(amax, row_rotate<0x128>(amax));
+  if constexpr (DJ > 1) {
+    const f32x2 y = both16(amax);
+    amax = fmaxf(y[0], y[1]);
+  }
+  if constexpr (DJ > 2) {
+    const f32x2 y = both32(amax);
+    amax = fmaxf(y[0], y[1]);
+  }
+  const uint64_t odds = __ballot((odd & 0x80808080u) != 0 || !finite(scale));
+  if (!live) return;
+  const uint64_t mine = kLanes == 64 ? ~0ull : ((1ull << kLanes) - 1ull) << (sub * kLanes);
+  const bool bad = (odds & mine) != 0;
+  const int e = max(whole_exponent(amax), -15);
+  const float per = bad ? 0.f : power2(-e);
+  if (r == 0) o.scales[id] = bad ? NAN : scale * power2(e);
+  if (tq > 1) return;
+  // lanes 0 of four write the largest, rounded up, which is the negative rounded down of
+  // the negative, lanes 1 the smallest
+  u32x4 c;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    uint32_t word = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const f16x2 h = tq ? lo[2 * x + b / 2] : -hi[2 * x + b / 2];
+      const int whole = (int)__builtin_floorf((float)h[b % 2] * per);
+      word |= (uint32_t)((tq ? whole : -whole) & 255) << (8 * b);
+    }
+    c[x] = bad ? 0u : word;
+  }
+  *(u32x4*)(o.codes + (uint64_t)id * (2 * D) + tq * D + (r / 4) * 16) = c;
+}
+
+// ------------------------------------------------------------ selection ----
+
+struct Select {
+  Rows rows;
+  uint32_t n_pages;
+  const int8_t* codes;
+  const float* outline_scales;
+  Strided q;
+  Divisor group;
+  int32_t m_rows;  // query rows of a key/value head
+  float* scores;   // [row][max_pages]
+  Divisor chunks;  // of a row, in the scoring kernel
+  uint32_t page_shift;
+  uint32_t keep, sink, recent;
+  int32_t* pages_out;
+  int32_t* lengths_out;
+  int32_t* places_out;
+};
+
+// What a row's workgroup does: keep the protected pages and, of pages lo .. hi
+// - 1, the `want` with the largest scores.
+struct Selection {
+  int len;
+  uint32_t held, left, lo, hi, want;
+  bool full;
+};
+
+__device__ __forceinline__ Selection selection_of(const Select& s, uint32_t row) {
+  Selection c;
+  c.len = row_length(s.rows, row);
+  c.held = ((uint32_t)c.len + (1u << s.page_shift) - 1u) >> s.page_shift;
+  c.full = c.held > s.keep;
+  c.left = c.full ? s.keep : c.held;
+  c.lo = s.sink;
+  c.hi = c.full ? c.held - s.recent : c.held;
+  c.want = c.full ? s.keep - s.sink - s.recent : 0;
+  return c;
+}
+
+// Groups of 16 pages that a wave has in registers.
+constexpr int score_groups(int dj) { return dj <= 2 ? 4 : 2; }
+constexpr int score_pages(int dj) { return 16 * score_groups(dj) * kWaves; }  // of a workgroup
+
+// Scores of a run of a row's pages.  S of 16 queries and 16 pages is a product of
+// 8-bit matrices: a query's whole numbers in two limbs of at most 127, those of
+// positive numbers against the largest and those of negative ones against the
+// smallest of each dim.  With the sums of the upper limbs shifted by 7 the lower
+// ones add on top; all is exact in 32 bits (16256 * 127 * 256 < 2^30).
+template <int DJ, bool F16>
+__global__ __launch_bounds__(kThreads) void score_kernel(Select s) {
+  constexpr int D = 64 * DJ;
+  constexpr int P = score_groups(DJ);
+  __shared__ __attribute__((aligned(16))) uint32_t s_limbs[DJ][2][2][kWave][4];
+  __shared__ float s_unit[16];  // 0: no query
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const uint32_t row = quotient(blockIdx.x, s.chunks);
+  const Selection c = selection_of(s, row);
+  const uint32_t from = (blockIdx.x - row * s.chunks.d) * score_pages(DJ);
+  if (!c.full || !c.want || from >= c.hi || from + score_pages(DJ) <= c.lo) return;
+  const uint32_t seq = quotient(row, s.rows.heads), head = row - seq * s.rows.heads.d;
+  const int count = new_count(s.rows, seq), origin = c.len - count;
+
+  // the wave's outlines are on their way while the queries are read
+  const int32_t* pages = s.rows.pages + (uint64_t)row * s.rows.max_pages;
+  const uint32_t first = from + wave * (16 * P);
+  u32x4 b[P][DJ][2];
+  float scale[P];
+  bool live[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const uint32_t page = first + 16 * p + lane % 16;
+    const uint32_t id = page < c.hi ? (uint32_t)pages[page] : ~0u;
+    live[p] = id < s.n_pages;
+    const uint32_t at = live[p] ? id : 0u;
+    scale[p] = 0.f;
+    if (s.n_pages == 0) continue;
+    scale[p] = s.outline_scales[at];
+    const int8_t* codes = s.codes + (uint64_t)at * (2 * D) + (lane / 16) * 16;
+#pragma unroll
+    for (int j = 0; j < DJ; ++j)
+#pragma unroll
+      for (int end = 0; end < 2; ++end) b[p][j][end] = *(const u32x4*)(codes + end * D + 64 * j);
+  }
+  float best[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) best[p] = -INFINITY;
+
+  for (int m0 = 0; m0 < s.m_rows; m0 += 16) {
+    // wave w: queries 4 w .. 4 w + 3, 16 lanes each; lane x: dims 64 j + 4 x + 0..3
+    const int n = wave * 4 + lane / 16, x = lane % 16, m = m0 + n;
+    const int t = (int)quotient((uint32_t)m, s.group);
+    const bool there = m < s.m_rows && t < count && origin + t >= 0;
+    uint16_t q[DJ][4];
+    uint32_t top = 0;
+    if (m0) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < DJ; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[j][i] = 0;
+      if (there) {
+        const uint16_t* src = s.q.data + (int64_t)seq * s.q.seq + (int64_t)t * s.q.token +
+                              ((int64_t)head * s.group.d + (m - t * (int)s.group.d)) * s.q.head + 64 * j + 4 * x;
+        if (s.q.wide) {
+          const u16x4 h = *(const u16x4*)src;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q[j][i] = h[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q[j][i] = src[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max(top, q[j][i] & 0x7FFFu);
+    }
+    float amax = to_float<F16>((uint16_t)top);
+    const bool plain = !not_finite<F16>(top);
+    amax = plain ? amax : INFINITY;
+    amax = fmaxf(amax, row_rotate<0x121>(amax));
+    amax = fmaxf(amax, row_rotate<0x122>(amax));
+    amax = fmaxf(amax, row_rotate<0x124>(amax));
+    amax = fmaxf(amax, row_rotate<0x128>(amax));
+    // 127 * 128 * 2^e is 127 * 2^(e + 7)
+    const bool counts = there && finite(amax);
+    const int e = counts ? max(whole_exponent(amax) - 7, -126) : 0;
+    const float per = power2(-e);
+    if (x == 0) s_unit[n] = counts ? power2(e) : 0.f;
+#pragma unroll
+    for (int j = 0; j < DJ; ++j) {
+      uint32_t words[2][2] = {{0, 0}, {0, 0}};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int whole = counts ? (int)__builtin_rintf(to_float<F16>(q[j][i]) * per) : 0;
+        const int upper = (whole + 64) >> 7, lower = whole - 128 * upper;
+        const int side = whole < 0 ? 1 : 0;
+        const uint32_t u = (uint32_t)(upper & 255) << (8 * i), l = (uint32_t)(lower & 255) << (8 * i);
+        words[0][0] |= side ? 0u : u;
+        words[0][1] |= side ? 0u : l;
+        words[1][0] |= side ? u : 0u;
+        words[1][1] |= side ? l : 0u;
+      }
+#pragma unroll
+      for (int end = 0; end < 2; ++end)
+#pragma unroll
+        for (int limb = 0; limb < 2; ++limb) s_limbs[j][end][limb][x / 4 * 16 + n][x % 4] = words[end][limb];
+    }
+    __syncthreads();
+    float unit[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) unit[r] = s_unit[4 * (lane / 16) + r];
+    i32x4 sum[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) sum[p] = i32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int limb = 0; limb < 2; ++limb) {
+#pragma unroll
+      for (int j = 0; j < DJ; ++j)
+#pragma unroll
+        for (int end = 0; end < 2; ++end) {
+          const i32x4 a = *(const i32x4*)s_limbs[j][end][limb][lane];
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+            sum[p] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, __builtin_bit_cast(i32x4, b[p][j][end]), sum[p], 0, 0, 0);
+        }
+      if (limb == 0) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) sum[p] <<= 7;
+      }
+    }
+    // the lane has queries 4 (lane / 16) + r of page lane % 16
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) best[p] = unit[r] > 0.f ? fmaxf(best[p], (float)sum[p][r] * unit[r]) : best[p];
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    f32x2 y = both16(best[p]);
+    y = both32(fmaxf(y[0], y[1]));
+    best[p] = live[p] ? fmaxf(y[0], y[1]) * scale[p] : -INFINITY;
+  }
+  // lanes 16 p .. 16 p + 15 write group p
+  float mine = best[0];
+#pragma unroll
+  for (int p = 1; p < P; ++p)
+    if (lane / 16 == p) mine = best[p];
+  const uint32_t page = first + lane;
+  if (lane < 16 * P && page < c.hi) s.scores[(uint64_t)row * s.rows.max_pages + page] = mine;
+}
+
+// Writes what stays, in order, and -1 past it.
+__device__ __forceinline__ void fill_rest(const Select& s, uint32_t row, uint32_t left, uint32_t threads) {
+  for (uint32_t i = left + threadIdx.x; i < s.keep; i += threads) {
+    s.pages_out[(uint64_t)row * s.keep + i] = -1;
+    s.places_out[(uint64_t)row * s.keep + i] = -1;
+  }
+}
+
+// One workgroup per row of up to THREADS * R pages.
+template <int THREADS, int R>
+__global__ __launch_bounds__(THREADS) void select_kernel(Select s) {
+  __shared__ ChoiceLds<THREADS, R> lds;
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const uint32_t row = blockIdx.x;
+  const Selection c = selection_of(s, row);
+  if (threadIdx.x == 0) s.lengths_out[row] = c.len - (int)((c.held - c.left) << s.page_shift);
+  const uint64_t at = (uint64_t)row * s.rows.max_pages;
+  const uint32_t span = c.want ? c.hi - c.lo : 0u;
+  uint32_t low = 0xFFFFFFFFu, high = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const uint32_t p = (uint32_t)i * THREADS + threadIdx.x;
+    uint32_t key = p < c.held && (!c.full || p < c.lo || p >= c.hi) ? kStays : 0u;
+    if (p - c.lo < span) {
+      key = weight_key(s.scores[at + p]);
+      low = min(low, key);
+      high = max(high, key);
+    }
+    lds.key[i][threadIdx.x] = key;
+  }
+  const Cut cut = cut_of<THREADS, R>(lds, low, high, c.want, wave, lane);
+  count_chunks<THREADS, R>(lds, cut, wave, lane);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const uint32_t p = (uint32_t)i * THREADS + threadIdx.x;
+    const Stay x = stay_of<THREADS, R>(lds, cut, i, lds.key[i][threadIdx.x], wave);
+    if (x.stays) {
+      s.pages_out[(uint64_t)row * s.keep + x.before] = s.rows.pages[at + p];
+      s.places_out[(uint64_t)row * s.keep + x.before] = (int32_t)p;
+    }
+  }
+  fill_rest(s, row, c.left, THREADS);
+}
+
+// Rows of any length: the score is found digit by digit (8 bits at a time, from
+// counts in LDS), the scores read again for each.
+__global__ __launch_bounds__(kThreads) void select_long_kernel(Select s) {
+  __shared__ uint32_t s_count[256];
+  __shared__ uint32_t s_pick[2];
+  __shared__ uint32_t s_sum[2][kWaves];
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const uint32_t row = blockIdx.x;
+  const Selection c = selection_of(s, row);
+  if (threadIdx.x == 0) s.lengths_out[row] = c.len - (int)((c.held - c.left) << s.page_shift);
+  const uint64_t at = (uint64_t)row * s.rows.max_pages;
+  uint32_t key = 0, want = c.want;
+  if (want) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      s_count[threadIdx.x] = 0;
+      __syncthreads();
+      for (uint32_t i = c.lo + threadIdx.x; i < c.hi; i += kThreads) {
+        const uint32_t k = weight_key(s.scores[at + i]);
+        if (shift == 24 || (k ^ key) >> (shift + 8) == 0) atomicAdd(&s_count[(k >> shift) & 255u], 1u);
+      }
+      __syncthreads();
+      if (wave == 0) {  // lane l: digits 255 - 4 l down to 252 - 4 l
+        uint32_t n[4], mine = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mine += n[i] = s_count[255 - 4 * lane - i];
+        uint32_t before = wave_scan(mine) - mine;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (before < want && before + n[i] >= want) {
+            s_pick[0] = 255u - 4u * lane - i;
+            s_pick[1] = want - before;
+          }
+          before += n[i];
+        }
+      }
+      __syncthreads();
+      key |= s_pick[0] << shift;
+      want = s_pick[1];
+    }
+  }
+  uint32_t above_before = 0, equal_before = 0;
+  for (uint32_t base = 0; base < c.held; base += kThreads) {
+    const uint32_t i = base + threadIdx.x;
+    const bool middle = c.full && i >= c.lo && i < c.hi;
+    const uint32_t k = middle && want ? weight_key(s.scores[at + i]) : 0u;
+    const bool above = i < c.held && (!middle || (want && k > key));
+    const bool equal = middle && want && k == key;
+    const uint64_t ba = __ballot(above), be = __ballot(equal);
+    if (lane == 0) {
+      s_sum[0][wave] = (uint32_t)__popcll(ba);
+      s_sum[1][wave] = (uint32_t)__popcll(be);
+    }
+    __syncthreads();
+    uint32_t a = above_before, q = equal_before;
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) {
+      if (x < wave) {
+        a += s_sum[0][x];
+        q += s_sum[1][x];
+      }
+      above_before += s_sum[0][x];
+      equal_before += s_sum[1][x];
+    }
+    __syncthreads();
+    a += lanes_below(ba, 0);
+    q += lanes_below(be, 0);
+    if (above || (equal && q < want)) {
+      const uint32_t to = a + min(q, want);
+      s.pages_out[(uint64_t)row * s.keep + to] = s.rows.pages[at + i];
+      s.places_out[(uint64_t)row * s.keep + to] = (int32_t)i;
+    }
+  }
+  fill_rest(s, row, c.left, kThreads);
+}
+
+// ---------------------------------------------------- a shared prefix ----
+
+template <int DJ, bool F16, int MT, bool ONCE>
+__global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, MT)) void prefix_kernel(Attention a) {
+  attend_part<DJ, F16, MT, ONCE, Sums::kShared>(a, blockIdx.x);
+}
+
+template <int DJ, bool F16, int MT, bool ONCE>
+__global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, MT)) void own_kernel(Attention a) {
+  attend_part<DJ, F16, MT, ONCE, Sums::kLeft>(a, blockIdx.x);
+}
+
+// Joins the sums over the prefix (a) with those over a row's own tokens (b), a
+// query row to each wave.
+template <int DJ, bool F16, int MT>
+__global__ __launch_bounds__(kThreads) void join_shared_kernel(Attention a, Attention b, Divisor rows_of_head,
+                                                               uint32_t n_rows, int shared_step_tiles) {
+  constexpr int D = 64 * DJ;
+  constexpr int ST = step_tiles(DJ, MT);
+  __shared__ float s_f[kWaves][2 * kMaxParts];
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const uint32_t x = blockIdx.x * kWaves + wave;
+  if (x >= n_rows) return;
+  const uint32_t row = quotient(x, rows_of_head);
+  const int m = (int)(x - row * rows_of_head.d);
+  const uint32_t group = quotient((uint32_t)m, b.unit_rows);
+  const int own_local = m - (int)(group * b.unit_rows.d);
+  const Part t = parts_of_unit(b, row, (int)group);
+  const Plan p = plan_unit<MT, ST>(b, t);
+  const bool any = seen_by(b, p, m) > 0;
+  // the prefix's units are of the query rows of all sequences
+  const uint32_t all = p.seq * rows_of_head.d + (uint32_t)m;
+  const uint32_t unit = quotient(all, a.unit_rows);
+  const int local = (int)(all - unit * a.unit_rows.d);
+  const uint32_t first = (p.head * a.m_groups.d + unit) * a.shared_parts;
+  const int tiles = (row_length(a.rows, p.head) + kTile - 1) / kTile;
+  const int steps = (tiles + shared_step_tiles - 1) / shared_step_tiles;
+  const int part_steps = max((steps + (int)a.shared_parts - 1) / (int)a.shared_parts, 1);
+  const int shared = any ? (steps + part_steps - 1) / part_steps : 0, parts = any ? shared + p.parts : 0;
+  auto slot = [&](int n) {
+    return n < shared ? (uint64_t)(first + n) * a.unit_rows.d + local
+                      : ((uint64_t)t.first + (uint64_t)(n - shared) * b.m_groups.d) * b.unit_rows.d + own_local;
+  };
+  auto part = [&](int n) { return n < shared ? a.ws_ml[slot(n)] : b.ws_ml[slot(n)]; };
+  float top = -INFINITY, total = 0.f;
+  for (int n = lane; n < parts; n += kWave) top = fmaxf(top, part(n)[0]);
+  top = wave_max(top);
+  const float base = top == -INFINITY ? 0.f : top;
+  for (int n = lane; n < parts; n += kWave) {
+    const f32x2 ml = part(n);
+    const float f = exp2_fast(ml[0] - base);
+    s_f[wave][n] = f;
+    total += f * ml[1];
+  }
+  total = wave_sum(total);
+  const float share = total == 0.f ? 0.f : 1.f / total;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  float o[DJ];  // dims 64 j + lane
+#pragma unroll
+  for (int j = 0; j < DJ; ++j) o[j] = 0.f;
+#pragma unroll 4
+  for (int n = 0; n < parts; ++n) {
+    const float* sums = (n < shared ? a.ws_o : b.ws_o) + slot(n) * D;
+    const float f = s_f[wave][n];
+#pragma unroll
+    for (int j = 0; j < DJ; ++j) o[j] += sums[64 * j + lane] * f;
+  }
+  uint16_t* dst = row_of(b.out, b, p, m);
+#pragma unroll
+  for (int j = 0; j < DJ; ++j) dst[64 * j + lane] = to_half<F16>(o[j] * share);
+}
+
+// ------------------------------------------------------------------ host ----
+
+int check_outlines(const ibp_kv_outlines* o, const ibp_kv_cache* c) {
+  if (!o) return IBP_ERR_INVALID_ARGUMENT;
+  if (c->n_pages == 0) return IBP_OK;
+  if (!o->codes || !o->scales) return IBP_ERR_INVALID_ARGUMENT;
+  return aligned(o->codes, 16) && aligned(o->scales, 4) ? IBP_OK : IBP_ERR_LAYOUT;
+}
+
+// Pages of a row that n_new tokens may be in.
+uint64_t touched_pages(uint64_t n_new, uint64_t page_tokens, uint64_t max_pages) {
+  return std::min<uint64_t>((n_new + page_tokens - 2) / page_tokens + 1, max_pages);
+}
+
+template <int DJ, bool F16, Pairs PAIRS>
+void launch_append_rotated(const Pool& pool, const Rows& rows, const Strided& k, const Strided& v, uint32_t per_row,
+                           uint32_t tasks, const Angles& t, const Queries& q, hipStream_t st) {
+  const uint32_t per_group = kWaves >> pool.tile_shift;
+  const uint32_t append = (tasks + per_group - 1) / per_group;
+  const uint32_t turn = (q.n_items + kThreads - 1) / kThreads;
+  hipLaunchKernelGGL((append_rotated_kernel<DJ, F16, PAIRS>), dim3(append + turn), dim3(kThreads), 0, st, pool, rows, k, v,
+                     make_divisor(per_row), tasks, Turn<PAIRS>{t}, q, append);
+}
+
+template <int DJ, bool F16>
+void launch_append_pairs(const Pool& pool, const Rows& rows, const Strided& k, const Strided& v, uint32_t per_row,
+                         uint32_t tasks, const Angles& t, bool interleaved, const Queries& q, hipStream_t st) {
+  if (interleaved) return launch_append_rotated<DJ, F16, Pairs::kNeighbour>(pool, rows, k, v, per_row, tasks, t, q, st);
+  if constexpr (DJ % 2 == 0)
+    if (t.half == 32 * DJ) return launch_append_rotated<DJ, F16, Pairs::kLane>(pool, rows, k, v, per_row, tasks, t, q, st);
+  launch_append_rotated<DJ, F16, Pairs::kFar>(pool, rows, k, v, per_row, tasks, t, q, st);
+}
+
+int launch_outline(const ibp_kv_cache* cache, const ibp_kv_outlines* o, const Rows& rows, uint64_t n_rows,
+                   uint64_t n_new, hipStream_t st) {
+  const Pool pool = make_pool(cache);
+  const int dj = (int)cache->head_dim / 64;
+  const uint64_t per_row = touched_pages(n_new, cache->page_tokens, rows.max_pages);
+  const uint64_t tasks = n_rows * per_row, per_group = (uint64_t)kWaves * (kWave / (16 * dj));
+  const dim3 grid((uint32_t)((tasks + per_group - 1) / per_group));
+  const Divisor d = make_divisor((uint32_t)per_row);
+  switch (dj) {
+    case 1: hipLaunchKernelGGL(outline_kernel<1>, grid, dim3(kThreads), 0, st, pool, rows, *o, d, (uint32_t)tasks); break;
+    case 2: hipLaunchKernelGGL(outline_kernel<2>, grid, dim3(kThreads), 0, st, pool, rows, *o, d, (uint32_t)tasks); break;
+    case 3: hipLaunchKernelGGL(outline_kernel<3>, grid, dim3(kThreads), 0, st, pool, rows, *o, d, (uint32_t)tasks); break;
+    default: hipLaunchKernelGGL(outline_kernel<4>, grid, dim3(kThreads), 0, st, pool, rows, *o, d, (uint32_t)tasks); break;
+  }
+  return launched();
+}
+
+// Whether the tasks of a wave for each touched page, or of a workgroup of `per_group`,
+// are more than a launch (and a Divisor's numbers) can have.
+bool too_many(uint64_t n_rows, uint64_t per_row, uint64_t per_group) {
+  return per_row && (per_row > 0x7FFFFFFFull / n_rows || n_rows * per_row / per_group >= max_grid(kThreads));
+}
+
+template <int DJ>
+void launch_score(const Select& s, uint64_t n_rows, uint32_t dtype, hipStream_t st) {
+  const dim3 grid((uint32_t)n_rows * s.chunks.d);
+  if (dtype == IBP_KV_FP16)
+    hipLaunchKernelGGL((score_kernel<DJ, true>), grid, dim3(kThreads), 0, st, s);
+  else
+    hipLaunchKernelGGL((score_kernel<DJ, false>), grid, dim3(kThreads), 0, st, s);
+}
+
+// The prefix of a call, as units of the query rows of all sequences, each cut into
+// `parts`; and where the sums are in the workspace.
+struct SharedShape {
+  Shape own;
+  int mt, step;
+  int32_t m_rows, m_groups, unit_rows;
+  uint32_t n_units, parts, n_rows, join_blocks;
+  uint64_t own_o, ml, own_ml, own_of, bytes;
+};
+
+bool make_shared_shape(uint64_t n_seqs, uint64_t heads, uint64_t prefix_pages, uint64_t own_pages, uint32_t page_tokens,
+                       uint32_t head_dim, uint64_t group, uint64_t n_new, int cus, SharedShape* s) {
+  if (!make_shape(n_seqs * heads, own_pages, page_tokens, head_dim, group, n_new, false, cus, &s->own)) return false;
+  const uint64_t own_rows = group * n_new;
+  if (n_seqs && own_rows > 0x7FFFFFFFull / n_seqs) return false;
+  const uint64_t m = own_rows * n_seqs;
+  if (m && heads > 0x7FFFFFFFull / m) return false;
+  const int dj = (int)head_dim / 64;
+  s->m_rows = (int32_t)m;
+  s->mt = m <= 16 ? 1 : m <= 32 || dj > 2 ? 2 : 4;
+  s->step = step_tiles(dj, s->mt);
+  const uint64_t per_unit = 16ull * s->mt;
+  s->m_groups = (int32_t)((m + per_unit - 1) / per_unit);
+  s->unit_rows = (int32_t)std::min<uint64_t>(m, per_unit);
+  const uint64_t units = heads * s->m_groups;
+  s->n_units = (uint32_t)units;
+  const uint64_t steps = (prefix_pages * page_tokens / kTile + s->step - 1) / s->step;
+  const uint64_t slots = (uint64_t)workgroups_per_unit(dj, s->mt) * cus;
+  s->parts = 1;
+  if (units)
+    s->parts = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>({slots / units, (steps + kWaves - 1) / kWaves, (uint64_t)kMaxParts}));
+  if (units * s->parts > max_grid(kThreads)) return false;
+  const uint64_t shared_slots = units * s->parts * s->unit_rows, own_slots = (uint64_t)s->own.n_parts * s->own.unit_rows;
+  s->own_o = shared_slots * head_dim * 4;
+  s->ml = s->own_o + own_slots * head_dim * 4;
+  s->own_ml = s->ml + shared_slots * 8;
+  s->own_of = s->own_ml + own_slots * 8;
+  s->bytes = s->own_of + (s->own.n_parts != s->own.n_units ? (uint64_t)s->own.n_units * 8 : 0);
+  s->n_rows = (uint32_t)(heads * m);
+  s->join_blocks = (s->n_rows + kWaves - 1) / kWaves;
+  return s->join_blocks <= max_grid(kThreads);
+}
+
+template <int DJ, bool F16, int MT>
+void launch_prefix(const Attention& a, uint32_t blocks, hipStream_t st) {
+  if (a.m_groups.d == 1)
+    hipLaunchKernelGGL((prefix_kernel<DJ, F16, MT, true>), dim3(blocks), dim3(kThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL((prefix_kernel<DJ, F16, MT, false>), dim3(blocks), dim3(kThreads), 0, st, a);
+}
+
+template <int DJ, bool F16>
+void launch_shared(const Attention& a, const Attention& b, const SharedShape& s, const Divisor& rows_of_head,
+                   hipStream_t st) {
+  const uint32_t blocks = s.n_units * s.parts;
+  if (s.mt == 1) launch_prefix<DJ, F16, 1>(a, blocks, st);
+  if (s.mt == 2) launch_prefix<DJ, F16, 2>(a, blocks, st);
+  if constexpr (DJ <= 2)
+    if (s.mt == 4) launch_prefix<DJ, F16, 4>(a, blocks, st);
+  const dim3 own(s.own.n_parts), join(s.join_blocks);
+  if (s.own.mt == 1) {
+    hipLaunchKernelGGL((own_kernel<DJ, F16, 1, true>), own, dim3(kThreads), 0, st, b);
+    hipLaunchKernelGGL((join_shared_kernel<DJ, F16, 1>), join, dim3(kThreads), 0, st, a, b, rows_of_head, s.n_rows, s.step);
+  } else {
+    if (b.m_groups.d == 1)
+      hipLaunchKernelGGL((own_kernel<DJ, F16, kQueryTiles, true>), own, dim3(kThreads), 0, st, b);
+    else
+      hipLaunchKernelGGL((own_kernel<DJ, F16, kQueryTiles, false>), own, dim3(kThreads), 0, st, b);
+    hipLaunchKernelGGL((join_shared_kernel<DJ, F16, kQueryTiles>), join, dim3(kThreads), 0, st, a, b, rows_of_head, s.n_rows, s.step);
+  }
+}
+
+// The prefix's table, of one sequence and as many heads.
+int check_prefix(const ibp_kv_table* prefix, const ibp_kv_table* table, uint64_t page_tokens) {
+  uint64_t heads = 0;
+  if (!prefix || prefix->n_seqs != 1 || prefix->kv_heads != table->kv_heads) return IBP_ERR_INVALID_ARGUMENT;
+  return check_table(prefix, page_tokens, &heads);
+}
+
+}  // namespace
+
+extern "C" {
+
+int ibp_kv_long_last_hip_error(void) { return g_last_hip; }
+
+int ibp_kv_append_rotated(const ibp_kv_cache* cache, const ibp_kv_table* table, uint32_t dtype, uint64_t n_new,
+                          const ibp_kv_tensor* k, const ibp_kv_tensor* v, const int32_t* counts,
+                          const ibp_kv_rotation* rotation, uint64_t q_heads, const ibp_kv_tensor* q,
+                          const ibp_kv_tensor* q_out, const ibp_kv_outlines* outlines, void* stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (dtype > IBP_KV_FP16) return IBP_ERR_UNSUPPORTED;
+  uint64_t n_rows = 0;
+  rc = check_table(table, cache->page_tokens, &n_rows);
+  if (rc) return rc;
+  if (!rotation || !q != !q_out) return IBP_ERR_INVALID_ARGUMENT;
+  if (rotation->rotary_dim == 0 || rotation->rotary_dim % 16 || rotation->rotary_dim > cache->head_dim || rotation->interleaved > 1)
+    return IBP_ERR_UNSUPPORTED;
+  if (rotation->n_positions && (!rotation->cos || !rotation->sin)) return IBP_ERR_INVALID_ARGUMENT;
+  if (!aligned(rotation->cos, 16) || !aligned(rotation->sin, 16) || !aligned(rotation->positions, 4)) return IBP_ERR_LAYOUT;
+  if (outlines && (rc = check_outlines(outlines, cache))) return rc;
+  if (n_rows == 0 || n_new == 0) return IBP_OK;
+  if (n_new > 0x7FFFFFFFull) return IBP_ERR_INVALID_ARGUMENT;
+  if ((rc = check_tensor(k)) || (rc = check_tensor(v))) return rc;
+  if (!aligned(counts, 4)) return IBP_ERR_LAYOUT;
+  const bool pages = table->max_pages != 0 && cache->n_pages != 0;
+  const uint64_t per_row = pages ? touched_pages(n_new, cache->page_tokens, table->max_pages) : 0;
+  if (too_many(n_rows, per_row, (uint64_t)kWaves * kTile / cache->page_tokens)) return IBP_ERR_INVALID_ARGUMENT;
+  Queries queries{};
+  if (q) {
+    if (q_heads == 0 || q_heads % table->kv_heads) return IBP_ERR_INVALID_ARGUMENT;
+    if ((rc = check_tensor(q)) || (rc = check_tensor(q_out))) return rc;
+    if (rows_overlap(table->n_seqs, q_out->seq_stride, cache->head_dim) ||
+        rows_overlap(n_new, q_out->token_stride, cache->head_dim) ||
+        rows_overlap(q_heads, q_out->head_stride, cache->head_dim))
+      return IBP_ERR_INVALID_ARGUMENT;
+    // items, and with the pages' workgroups the grid
+    const uint64_t most = 0x7FFFFFFFull / (cache->head_dim / 16) / table->n_seqs;
+    if (n_new > most || q_heads > most / n_new) return IBP_ERR_INVALID_ARGUMENT;
+    queries.n_items = (uint32_t)(table->n_seqs * n_new * q_heads * (cache->head_dim / 16));
+    queries.q = make_strided(q);
+    queries.out = make_strided(q_out);
+    queries.q_heads = make_divisor((uint32_t)q_heads);
+    queries.group = make_divisor((uint32_t)(q_heads / table->kv_heads));
+    queries.n_new = make_divisor((uint32_t)n_new);
+  }
+  const uint64_t tasks = n_rows * per_row;
+  if (tasks / (kWaves * kTile / cache->page_tokens) + queries.n_items / kThreads + 2 > max_grid(kThreads))
+    return IBP_ERR_INVALID_ARGUMENT;
+  if (tasks == 0 && queries.n_items == 0) return IBP_OK;
+  rc = pending_hip_error();
+  if (rc) return rc;
+  const Pool pool = make_pool(cache);
+  const Rows rows = make_rows(table, cache->page_tokens, n_new, counts);
+  const Strided ks = make_strided(k), vs = make_strided(v);
+  Angles t;
+  t.cos = rotation->cos;
+  t.sin = rotation->sin;
+  t.positions = rotation->positions;
+  t.n_positions = (uint32_t)std::min<uint64_t>(rotation->n_positions, 1ull << 31);
+  t.half = (int32_t)rotation->rotary_dim / 2;
+  hipStream_t st = (hipStream_t)stream;
+  const uint32_t pr = (uint32_t)std::max<uint64_t>(per_row, 1), n = (uint32_t)tasks;
+  const bool il = rotation->interleaved != 0;
+  switch (cache->head_dim / 64 * 2 + dtype) {
+    case 2: launch_append_pairs<1, false>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
+    case 3: launch_append_pairs<1, true>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
+    case 4: launch_append_pairs<2, false>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
+    case 5: launch_append_pairs<2, true>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
+    case 6: launch_append_pairs<3, false>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
+    case 7: launch_append_pairs<3, true>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
+    case 8: launch_append_pairs<4, false>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
+    default: launch_append_pairs<4, true>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
+  }
+  rc = launched();
+  if (rc || !outlines || !tasks) return rc;
+  return launch_outline(cache, outlines, rows, n_rows, n_new, st);
+}
+
+int ibp_kv_outline(const ibp_kv_cache* cache, const ibp_kv_outlines* outlines, const ibp_kv_table* table,
+                   uint64_t n_new, const int32_t* counts, void* stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  uint64_t n_rows = 0;
+  rc = check_table(table, cache->page_tokens, &n_rows);
+  if (rc || (rc = check_outlines(outlines, cache))) return rc;
+  if (n_rows == 0 || n_new == 0 || table->max_pages == 0 || cache->n_pages == 0) return IBP_OK;
+  if (n_new > 0x7FFFFFFFull) return IBP_ERR_INVALID_ARGUMENT;
+  if (!aligned(counts, 4)) return IBP_ERR_LAYOUT;
+  if (too_many(n_rows, touched_pages(n_new, cache->page_tokens, table->max_pages), kWaves)) return IBP_ERR_INVALID_ARGUMENT;
+  rc = pending_hip_error();
+  if (rc) return rc;
+  return launch_outline(cache, outlines, make_rows(table, cache->page_tokens, n_new, counts), n_rows, n_new, (hipStream_t)stream);
+}
+
+uint64_t ibp_kv_select_workspace_bytes(const ibp_kv_cache* cache, const ibp_kv_table* table) {
+  uint64_t n_rows = 0;
+  if (check_cache(cache) || !table || check_table(table, cache->page_tokens, &n_rows)) return 0;
+  return n_rows * table->max_pages * 4;
+}
+
+int ibp_kv_select(const ibp_kv_cache* cache, const ibp_kv_outlines* outlines, const ibp_kv_table* table,
+                  uint32_t dtype, uint64_t q_heads, uint64_t n_new, const ibp_kv_tensor* q, const int32_t* counts,
+                  uint64_t keep_pages, uint64_t sink_pages, uint64_t recent_pages, int32_t* pages_out,
+                  int32_t* lengths_out, int32_t* places_out, void* workspace, uint64_t workspace_bytes, void* stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (dtype > IBP_KV_FP16) return IBP_ERR_UNSUPPORTED;
+  const uint64_t pt = cache->page_tokens;
+  uint64_t n_rows = 0;
+  rc = check_table(table, pt, &n_rows);
+  if (rc || (rc = check_outlines(outlines, cache))) return rc;
+  if (recent_pages == 0 || sink_pages > keep_pages || recent_pages > keep_pages - sink_pages || keep_pages > 0x7FFFFFFFull / pt)
+    return IBP_ERR_INVALID_ARGUMENT;
+  if (n_new > 0x7FFFFFFFull || recent_pages < (n_new ? (n_new + pt - 2) / pt + 1 : 1)) return IBP_ERR_INVALID_ARGUMENT;
+  if (n_rows == 0) return IBP_OK;
+  if (q_heads == 0 || q_heads % table->kv_heads) return IBP_ERR_INVALID_ARGUMENT;
+  if (n_new && (rc = check_tensor(q))) return rc;
+  if (!pages_out || !lengths_out || !places_out) return IBP_ERR_INVALID_ARGUMENT;
+  if (!aligned(counts, 4) || !aligned(pages_out, 4) || !aligned(lengths_out, 4) || !aligned(places_out, 4) || !aligned(workspace, 16))
+    return IBP_ERR_LAYOUT;
+  const uint64_t group = q_heads / table->kv_heads;
+  if (n_new && group > (1ull << 24) / n_new) return IBP_ERR_INVALID_ARGUMENT;
+  const uint64_t bytes = n_rows * table->max_pages * 4;
+  if (bytes && (!workspace || workspace_bytes < bytes)) return IBP_ERR_INVALID_ARGUMENT;
+  if (keep_pages > (1ull << 60) / n_rows) return IBP_ERR_INVALID_ARGUMENT;
+  const uint64_t kept = n_rows * keep_pages * 4;
+  const void* in[3] = {table->pages, table->lengths, workspace};
+  void* outs[3] = {pages_out, places_out, lengths_out};
+  const uint64_t in_size[3] = {bytes, n_rows * 4, bytes}, out_size[3] = {kept, kept, n_rows * 4};
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < 3; ++j)
+      if (overlap(in[i], in_size[i], outs[j], out_size[j]) || (i < j && overlap(outs[i], out_size[i], outs[j], out_size[j])))
+        return IBP_ERR_INVALID_ARGUMENT;
+  const int dj = (int)cache->head_dim / 64;
+  const uint64_t chunks = (table->max_pages + score_pages(dj) - 1) / score_pages(dj);
+  if (n_rows > max_grid(1024) || chunks > max_grid(kThreads) / n_rows) return IBP_ERR_INVALID_ARGUMENT;
+  rc = pending_hip_error();
+  if (rc) return rc;
+  Select s{};
+  s.rows = make_rows(table, (uint32_t)pt, n_new, counts);
+  s.n_pages = (uint32_t)std::min<uint64_t>(cache->n_pages, 1ull << 31);
+  s.codes = outlines->codes;
+  s.outline_scales = outlines->scales;
+  if (n_new) s.q = make_strided(q);
+  s.group = make_divisor((uint32_t)group);
+  s.m_rows = (int32_t)(group * n_new);
+  s.scores = (float*)workspace;
+  s.chunks = make_divisor((uint32_t)std::max<uint64_t>(chunks, 1));
+  s.page_shift = pt == 16 ? 4 : pt == 32 ? 5 : 6;
+  s.keep = (uint32_t)keep_pages;
+  s.sink = (uint32_t)sink_pages;
+  s.recent = (uint32_t)recent_pages;
+  s.pages_out = pages_out;
+  s.lengths_out = lengths_out;
+  s.places_out = places_out;
+  hipStream_t st = (hipStream_t)stream;
+  // rows with room for no more than keep_pages keep what they have
+  if (table->max_pages > keep_pages && keep_pages > sink_pages + recent_pages) {
+    switch (dj) {
+      case 1: launch_score<1>(s, n_rows, dtype, st); break;
+      case 2: launch_score<2>(s, n_rows, dtype, st); break;
+      case 3: launch_score<3>(s, n_rows, dtype, st); break;
+      default: launch_score<4>(s, n_rows, dtype, st); break;
+    }
+    if ((rc = launched())) return rc;
+  }
+  const dim3 grid((uint32_t)n_rows);
+  if (table->max_pages <= 1024)
+    hipLaunchKernelGGL((select_kernel<256, 4>), grid, dim3(256), 0, st, s);
+  else if (table->max_pages <= 4096)
+    hipLaunchKernelGGL((select_kernel<1024, 4>), grid, dim3(1024), 0, st, s);
+  else if (table->max_pages <= 16384)
+    hipLaunchKernelGGL((select_kernel<1024, 16>), grid, dim3(1024), 0, st, s);
+  else
+    hipLaunchKernelGGL(select_long_kernel, grid, dim3(kThreads), 0, st, s);
+  return launched();
+}
+
+uint64_t ibp_kv_attention_shared_workspace_bytes(const ibp_kv_cache* cache, const ibp_kv_table* prefix,
+                                                 const ibp_kv_table* table, uint64_t q_heads, uint64_t n_new) {
+  if (check_cache(cache) || !prefix || !table || table->kv_heads == 0 || q_heads % table->kv_heads) return 0;
+  if (table->n_seqs && table->kv_heads > (1ull << 30) / table->n_seqs) return 0;
+  if (table->max_pages > 0x7FFFFFFFull / cache->page_tokens || prefix->max_pages > 0x7FFFFFFFull / cache->page_tokens) return 0;
+  SharedShape s;
+  if (!make_shared_shape(table->n_seqs, table->kv_heads, prefix->max_pages, table->max_pages, cache->page_tokens,
+                         cache->head_dim, q_heads / table->kv_heads, n_new, compute_units(), &s))
+    return 0;
+  return s.bytes;
+}
+
+int ibp_kv_attention_shared(const ibp_kv_cache* cache, const ibp_kv_table* prefix, const ibp_kv_table* table,
+                            uint32_t dtype, uint64_t q_heads, uint64_t n_new, const ibp_kv_tensor* q,
+                            const ibp_kv_tensor* out, const int32_t* counts, float scale, void* workspace,
+                            uint64_t workspace_bytes, void* stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (dtype > IBP_KV_FP16) return IBP_ERR_UNSUPPORTED;
+  uint64_t n_rows = 0;
+  rc = check_table(table, cache->page_tokens, &n_rows);
+  if (rc || (rc = check_prefix(prefix, table, cache->page_tokens))) return rc;
+  if (n_rows == 0) return IBP_OK;
+  if (q_heads == 0 || q_heads % table->kv_heads || !(scale - scale == 0.f)) return IBP_ERR_INVALID_ARGUMENT;
+  if (n_new == 0) return IBP_OK;
+  if ((rc = check_tensor(q)) || (rc = check_tensor(out))) return rc;
+  if (rows_overlap(table->n_seqs, out->seq_stride, cache->head_dim) ||
+      rows_overlap(n_new, out->token_stride, cache->head_dim) ||
+      rows_overlap(q_heads, out->head_stride, cache->head_dim))
+    return IBP_ERR_INVALID_ARGUMENT;
+  if (!aligned(counts, 4) || !aligned(workspace, 16)) return IBP_ERR_LAYOUT;
+  const uint64_t group = q_heads / table->kv_heads;
+  SharedShape s;
+  if (!make_shared_shape(table->n_seqs, table->kv_heads, prefix->max_pages, table->max_pages, cache->page_tokens,
+                         cache->head_dim, group, n_new, compute_units(), &s))
+    return IBP_ERR_INVALID_ARGUMENT;
+  if (s.bytes && (!workspace || workspace_bytes < s.bytes)) return IBP_ERR_INVALID_ARGUMENT;
+  rc = pending_hip_error();
+  if (rc) return rc;
+  Attention a{}, b{};
+  a.pool = b.pool = make_pool(cache);
+  a.rows = make_rows(prefix, cache->page_tokens, n_new, nullptr);
+  b.rows = make_rows(table, cache->page_tokens, n_new, counts);
+  if (cache->n_pages == 0) a.rows.capacity = b.rows.capacity = 0;  // holes only: nothing to see, and no page to read
+  a.q = b.q = make_strided(q);
+  a.out = b.out = make_strided(out);
+  a.scale = b.scale = scale * 1.44269504088896340736f;
+  a.group = b.group = make_divisor((uint32_t)group);
+  a.n_new = b.n_new = make_divisor((uint32_t)n_new);
+  char* ws = (char*)workspace;
+  a.ws_o = (float*)ws;
+  b.ws_o = (float*)(ws + s.own_o);
+  a.ws_ml = (f32x2*)(ws + s.ml);
+  b.ws_ml = (f32x2*)(ws + s.own_ml);
+  b.ws_of = (int32_t*)(ws + s.own_of);
+  a.m_rows = s.m_rows;
+  a.m_groups = make_divisor((uint32_t)s.m_groups);
+  a.unit_rows = make_divisor((uint32_t)s.unit_rows);
+  a.n_units = s.n_units;
+  a.n_rows = (uint32_t)table->kv_heads;
+  a.n_parts = s.n_units * s.parts;
+  a.shared_parts = s.parts;
+  b.m_rows = s.own.m_rows;
+  b.m_groups = make_divisor((uint32_t)s.own.m_groups);
+  b.unit_rows = make_divisor((uint32_t)s.own.unit_rows);
+  b.cap_tiles = s.own.cap_tiles;
+  b.n_units = s.own.n_units;
+  b.n_rows = (uint32_t)n_rows;
+  b.n_parts = s.own.n_parts;
+  const Divisor rows_of_head = make_divisor((uint32_t)(group * n_new));
+  hipStream_t st = (hipStream_t)stream;
+  switch (cache->head_dim / 64 * 2 + dtype) {
+    case 2: launch_shared<1, false>(a, b, s, rows_of_head, st); break;
+    case 3: launch_shared<1, true>(a, b, s, rows_of_head, st); break;
+    case 4: launch_shared<2, false>(a, b, s, rows_of_head, st); break;
+    case 5: launch_shared<2, true>(a, b, s, rows_of_head, st); break;
+    case 6: launch_shared<3, false>(a, b, s, rows_of_head, st); break;
+    case 7: launch_shared<3, true>(a, b, s, rows_of_head, st); break;
+    case 8: launch_shared<4, false>(a, b, s, rows_of_head, st); break;
+    default: launch_shared<4, true>(a, b, s, rows_of_head, st); break;
+  }
+  return launched();
+}
+
+}  // extern "C"

@@ -1,5 +1,6 @@
-// The binding of libibp_kv's calls to torch tensors: checks of the arguments,
-// tensors for the results, and the call of the C ABI (include/ibp_kv.h).  Its
+// The binding of the calls of libibp_kv and libibp_kv_long to torch tensors: checks
+// of the arguments, tensors for the results, and the call of the C ABI
+// (include/ibp_kv.h, include/ibp_kv_long.h).  Its
 // functions stand behind those of the same names in ibp_kv.py.  No step of an
 // operator is computed here.  A call runs on the GPU of its tensors, whichever
 // is current; going backward through its results raises.
@@ -27,6 +28,7 @@
 #include <vector>
 
 #include "ibp_kv.h"
+#include "ibp_kv_long.h"
 
 namespace {
 
@@ -49,7 +51,7 @@ bool is_tensor(PyObject* o, const char* name) {
 bool check(const Tensor& t, ScalarType type, const char* name) {
   if (t.is_cuda() && t.scalar_type() == type && t.is_contiguous()) return true;
   PyErr_Format(PyExc_ValueError, "%s must be a contiguous %s GPU tensor", name,
-               type == ScalarType::Int ? "int32" : type == ScalarType::Float ? "float32" : "uint8");
+               type == ScalarType::Int ? "int32" : type == ScalarType::Float ? "float32" : type == ScalarType::Char ? "int8" : "uint8");
   return false;
 }
 
@@ -416,11 +418,268 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ---- libibp_kv_long ----
+
+// The outlines of a cache's pages.
+bool check_outlines(PyObject* codes, PyObject* scales, const ibp_kv_cache& cache, ibp_kv_outlines* out) {
+  if (!check(codes, ScalarType::Char, "outline codes") || !check(scales, ScalarType::Float, "outline scales")) return false;
+  const Tensor &c = THPVariable_Unpack(codes), &s = THPVariable_Unpack(scales);
+  if (c.dim() != 3 || (uint64_t)c.size(0) != cache.n_pages || c.size(1) != 2 || (uint64_t)c.size(2) != cache.head_dim ||
+      (uint64_t)s.numel() != cache.n_pages) {
+    PyErr_Format(PyExc_ValueError, "outlines must be codes [%llu, 2, %u] and as many scales", (unsigned long long)cache.n_pages,
+                 cache.head_dim);
+    return false;
+  }
+  *out = {(int8_t*)c.data_ptr(), (float*)s.data_ptr()};
+  return true;
+}
+
+// Queries [n_seqs, n_new, q_heads, head_dim] of the type of `like` (null: of their own).
+bool check_queries(PyObject* o, const ibp_kv_cache& cache, const ibp_kv_table& table, const Tensor* like, int64_t* n_new,
+                   int64_t* q_heads, uint32_t* dtype, ibp_kv_tensor* q) {
+  if (!check_type(o, "q", dtype)) return false;
+  const Tensor& x = THPVariable_Unpack(o);
+  *q_heads = x.size(2);
+  if (table.kv_heads && (*q_heads == 0 || *q_heads % (int64_t)table.kv_heads)) {
+    PyErr_SetString(PyExc_ValueError, "q_heads must be a multiple of kv_heads");
+    return false;
+  }
+  if (!like) *n_new = x.size(1);
+  const int64_t shape[4] = {(int64_t)table.n_seqs, *n_new, *q_heads, cache.head_dim};
+  return check_rows(o, "q", like ? like->scalar_type() : x.scalar_type(), shape, q);
+}
+
+void written_all(PyObject* tuple) {
+  if (tuple)
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(tuple); ++i) written(PyTuple_GET_ITEM(tuple, i));
+}
+
+// append_rotated(cache, pages, lengths, k, v, cos, sin, positions, q, q_out, counts,
+//                interleaved, outline_codes, outline_scales, stream) -> (status, q_out)
+PyObject* append_rotated(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  ibp_kv_cache cache;
+  ibp_kv_table table;
+  ibp_kv_tensor k, v, q, q_out;
+  ibp_kv_outlines outlines;
+  ibp_kv_rotation rotation;
+  uint32_t dtype;
+  const int32_t* counts;
+  void* stream;
+  c10::Device gpu(c10::kCUDA, 0);
+  if (!arguments(n, 15) ||
+      !same_gpu({{tensor_of_cache(a[0]), "the cache"}, {a[1], "pages"}, {a[2], "lengths"}, {a[3], "k"}, {a[4], "v"}, {a[5], "cos"},
+                 {a[6], "sin"}, {a[7], "positions"}, {a[8], "q"}, {a[9], "q_out"}, {a[10], "counts"}, {a[12], "outline codes"},
+                 {a[13], "outline scales"}}, &gpu))
+    return nullptr;
+  const Gradients gradients("ibp_kv_append_rotated", {a[8], a[5], a[6]});
+  const bool queries = a[8] != Py_None, outlined = a[12] != Py_None;
+  if ((queries && !gradients.check_given({{a[9], "q_out"}})) || !check_type(a[3], "k", &dtype) || !from_structure(a[0], &cache) ||
+      !check_table(a[1], a[2], &table))
+    return nullptr;
+  const Tensor& x = THPVariable_Unpack(a[3]);
+  int64_t n_new = x.size(1), q_heads = 0;
+  const int64_t shape[4] = {(int64_t)table.n_seqs, n_new, (int64_t)table.kv_heads, cache.head_dim};
+  if (!check_rows(a[3], "k", x.scalar_type(), shape, &k) || !check_rows(a[4], "v", x.scalar_type(), shape, &v) ||
+      !check(a[5], ScalarType::Float, "cos") || !check(a[6], ScalarType::Float, "sin"))
+    return nullptr;
+  const Tensor &cos = THPVariable_Unpack(a[5]), &sin = THPVariable_Unpack(a[6]);
+  if (cos.dim() != 2 || cos.sizes() != sin.sizes()) {
+    PyErr_SetString(PyExc_ValueError, "cos and sin must be [n_positions, rotary_dim / 2]");
+    return nullptr;
+  }
+  rotation.n_positions = (uint64_t)cos.size(0);
+  rotation.rotary_dim = (uint32_t)std::min<int64_t>(2 * cos.size(1), 0x7FFFFFF0);
+  const int interleaved = PyObject_IsTrue(a[11]);
+  if (interleaved < 0) return nullptr;
+  rotation.interleaved = (uint32_t)interleaved;
+  rotation.cos = (const float*)cos.data_ptr();
+  rotation.sin = (const float*)sin.data_ptr();
+  rotation.positions = nullptr;
+  if (a[7] != Py_None) {
+    if (!check(a[7], ScalarType::Int, "positions")) return nullptr;
+    const Tensor& p = THPVariable_Unpack(a[7]);
+    if (p.dim() != 2 || (uint64_t)p.size(0) != table.n_seqs || p.size(1) != n_new) {
+      refuse("%s must be [n_seqs, n_new]", "positions");
+      return nullptr;
+    }
+    rotation.positions = (const int32_t*)p.data_ptr();
+  }
+  uint32_t q_type;
+  if ((queries && !check_queries(a[8], cache, table, &x, &n_new, &q_heads, &q_type, &q)) || !check_counts(a[10], table.n_seqs, &counts) ||
+      (outlined && !check_outlines(a[12], a[13], cache, &outlines)) || !stream_of(a[14], &stream))
+    return nullptr;
+  const int64_t q_shape[4] = {(int64_t)table.n_seqs, n_new, q_heads, cache.head_dim};
+  if (!queries && a[9] != Py_None) {
+    PyErr_SetString(PyExc_ValueError, "q_out without q");
+    return nullptr;
+  }
+  if (a[9] != Py_None && !check_rows(a[9], "q_out", x.scalar_type(), q_shape, &q_out)) return nullptr;
+  const OnGpu on(gpu);
+  Tensor turned;
+  if (queries) {
+    turned = a[9] != Py_None ? THPVariable_Unpack(a[9]) : at::empty(q_shape, x.options());
+    q_out = {turned.data_ptr(), turned.stride(0), turned.stride(1), turned.stride(2)};
+  }
+  written_all(tensors_of_cache(a[0]));
+  written(a[9]);
+  written(a[12]);
+  written(a[13]);
+  const int status = ibp_kv_append_rotated(&cache, &table, dtype, (uint64_t)n_new, &k, &v, counts, &rotation, (uint64_t)q_heads,
+                                           queries ? &q : nullptr, queries ? &q_out : nullptr, outlined ? &outlines : nullptr, stream);
+  gradients.mark({turned});
+  PyObject* result = Py_None;
+  if (queries)
+    result = THPVariable_Wrap(turned);
+  else
+    Py_INCREF(result);
+  return Py_BuildValue("(iN)", status, result);
+  END_HANDLE_TH_ERRORS
+}
+
+// outline(cache, outline_codes, outline_scales, pages, lengths, n_new, counts, stream) -> status
+PyObject* outline(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  ibp_kv_cache cache;
+  ibp_kv_table table;
+  ibp_kv_outlines outlines;
+  uint64_t n_new = 0x7FFFFFFF;  // every page that holds tokens
+  const int32_t* counts;
+  void* stream;
+  c10::Device gpu(c10::kCUDA, 0);
+  if (!arguments(n, 8) ||
+      !same_gpu({{tensor_of_cache(a[0]), "the cache"}, {a[1], "outline codes"}, {a[2], "outline scales"}, {a[3], "pages"},
+                 {a[4], "lengths"}, {a[6], "counts"}}, &gpu) ||
+      !from_structure(a[0], &cache) || !check_outlines(a[1], a[2], cache, &outlines) || !check_table(a[3], a[4], &table) ||
+      (a[5] != Py_None && !number(a[5], &n_new)) || !check_counts(a[6], table.n_seqs, &counts) || !stream_of(a[7], &stream))
+    return nullptr;
+  const OnGpu on(gpu);
+  written(a[1]);
+  written(a[2]);
+  return PyLong_FromLong(ibp_kv_outline(&cache, &outlines, &table, n_new, counts, stream));
+  END_HANDLE_TH_ERRORS
+}
+
+bool check_shape(PyObject* o, ScalarType type, const char* name, at::IntArrayRef shape) {
+  if (!check(o, type, name)) return false;
+  if (THPVariable_Unpack(o).sizes() == shape) return true;
+  refuse("%s has the wrong shape", name);
+  return false;
+}
+
+// select(cache, outline_codes, outline_scales, pages, lengths, q, keep, sink, recent, counts,
+//        pages_out, lengths_out, places_out, workspace, stream) -> (status, pages, lengths, places)
+PyObject* select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  ibp_kv_cache cache;
+  ibp_kv_table table;
+  ibp_kv_tensor q;
+  ibp_kv_outlines outlines;
+  uint32_t dtype;
+  uint64_t keep, sink, recent;
+  int64_t n_new, q_heads;
+  const int32_t* counts;
+  void* stream;
+  c10::Device gpu(c10::kCUDA, 0);
+  if (!arguments(n, 15) ||
+      !same_gpu({{tensor_of_cache(a[0]), "the cache"}, {a[1], "outline codes"}, {a[2], "outline scales"}, {a[3], "pages"},
+                 {a[4], "lengths"}, {a[5], "q"}, {a[9], "counts"}, {a[10], "pages_out"}, {a[11], "lengths_out"}, {a[12], "places_out"},
+                 {a[13], "workspace"}}, &gpu) ||
+      !from_structure(a[0], &cache) || !check_outlines(a[1], a[2], cache, &outlines) || !check_table(a[3], a[4], &table) ||
+      !check_queries(a[5], cache, table, nullptr, &n_new, &q_heads, &dtype, &q) || !number(a[6], &keep) || !number(a[7], &sink) ||
+      !number(a[8], &recent) || !check_counts(a[9], table.n_seqs, &counts))
+    return nullptr;
+  if (keep > 0x7FFFFFFF) {
+    PyErr_SetString(PyExc_ValueError, "keep_pages is past 2^31");
+    return nullptr;
+  }
+  const int64_t shape[3] = {(int64_t)table.n_seqs, (int64_t)table.kv_heads, (int64_t)keep};
+  if ((a[10] != Py_None && !check_shape(a[10], ScalarType::Int, "pages_out", shape)) ||
+      (a[11] != Py_None && !check_shape(a[11], ScalarType::Int, "lengths_out", at::IntArrayRef(shape, 2))) ||
+      (a[12] != Py_None && !check_shape(a[12], ScalarType::Int, "places_out", shape)) ||
+      (a[13] != Py_None && !check(a[13], ScalarType::Byte, "workspace")) || !stream_of(a[14], &stream))
+    return nullptr;
+  const OnGpu on(gpu);
+  const auto options = THPVariable_Unpack(a[3]).options();
+  const Tensor p = a[10] != Py_None ? THPVariable_Unpack(a[10]) : at::empty(shape, options);
+  const Tensor l = a[11] != Py_None ? THPVariable_Unpack(a[11]) : at::empty(at::IntArrayRef(shape, 2), options);
+  const Tensor w = a[12] != Py_None ? THPVariable_Unpack(a[12]) : at::empty(shape, options);
+  Tensor workspace;
+  if (a[13] != Py_None)
+    workspace = THPVariable_Unpack(a[13]);
+  else if (const uint64_t bytes = ibp_kv_select_workspace_bytes(&cache, &table))
+    workspace = at::empty({(int64_t)bytes}, options.dtype(at::kByte));
+  for (int i = 10; i < 13; ++i) written(a[i]);
+  const int status = ibp_kv_select(&cache, &outlines, &table, dtype, (uint64_t)q_heads, (uint64_t)n_new, &q, counts, keep, sink, recent,
+                                   (int32_t*)p.data_ptr(), (int32_t*)l.data_ptr(), (int32_t*)w.data_ptr(),
+                                   workspace.defined() ? workspace.data_ptr() : nullptr,
+                                   workspace.defined() ? (uint64_t)workspace.numel() : 0, stream);
+  return Py_BuildValue("(iNNN)", status, THPVariable_Wrap(p), THPVariable_Wrap(l), THPVariable_Wrap(w));
+  END_HANDLE_TH_ERRORS
+}
+
+// attention_shared(cache, prefix_pages, prefix_lengths, pages, lengths, q, scale, counts, out,
+//                  workspace, stream) -> (status, out)
+PyObject* attention_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  ibp_kv_cache cache;
+  ibp_kv_table table;
+  ibp_kv_tensor q, o;
+  uint32_t dtype;
+  int64_t n_new, q_heads;
+  const int32_t* counts;
+  void* stream;
+  c10::Device gpu(c10::kCUDA, 0);
+  if (!arguments(n, 11) ||
+      !same_gpu({{tensor_of_cache(a[0]), "the cache"}, {a[1], "prefix_pages"}, {a[2], "prefix_lengths"}, {a[3], "pages"},
+                 {a[4], "lengths"}, {a[5], "q"}, {a[7], "counts"}, {a[8], "out"}, {a[9], "workspace"}}, &gpu))
+    return nullptr;
+  const Gradients gradients("ibp_kv_attention_shared", {a[5]});
+  if (!gradients.check_given({{a[8], "out"}}) || !from_structure(a[0], &cache) || !check_table(a[3], a[4], &table) ||
+      !check(a[1], ScalarType::Int, "prefix_pages") || !check(a[2], ScalarType::Int, "prefix_lengths"))
+    return nullptr;
+  const Tensor &pp = THPVariable_Unpack(a[1]), &pl = THPVariable_Unpack(a[2]);
+  if (pp.dim() != 2 || pl.dim() != 1 || (uint64_t)pp.size(0) != table.kv_heads || (uint64_t)pl.size(0) != table.kv_heads) {
+    PyErr_SetString(PyExc_ValueError, "prefix_pages must be [kv_heads, max_pages] and prefix_lengths [kv_heads]");
+    return nullptr;
+  }
+  const ibp_kv_table prefix = {1, table.kv_heads, (uint64_t)pp.size(1), (const int32_t*)pp.data_ptr(), (const int32_t*)pl.data_ptr()};
+  if (!check_queries(a[5], cache, table, nullptr, &n_new, &q_heads, &dtype, &q)) return nullptr;
+  const Tensor& x = THPVariable_Unpack(a[5]);
+  float scale = 1.f / std::sqrt((float)cache.head_dim);
+  if (a[6] != Py_None) {
+    scale = (float)PyFloat_AsDouble(a[6]);
+    if (PyErr_Occurred()) return nullptr;
+  }
+  if (!check_counts(a[7], table.n_seqs, &counts) || (a[8] != Py_None && !check_rows(a[8], "out", x.scalar_type(), x.sizes(), &o)) ||
+      (a[9] != Py_None && !check(a[9], ScalarType::Byte, "workspace")) || !stream_of(a[10], &stream))
+    return nullptr;
+  const OnGpu on(gpu);
+  const Tensor out = a[8] != Py_None ? THPVariable_Unpack(a[8]) : at::empty(x.sizes(), x.options());
+  if (a[8] == Py_None) o = {out.data_ptr(), out.stride(0), out.stride(1), out.stride(2)};
+  Tensor workspace;
+  if (a[9] != Py_None)
+    workspace = THPVariable_Unpack(a[9]);
+  else if (const uint64_t bytes = ibp_kv_attention_shared_workspace_bytes(&cache, &prefix, &table, (uint64_t)q_heads, (uint64_t)n_new))
+    workspace = at::empty({(int64_t)bytes}, x.options().dtype(at::kByte));
+  written(a[8]);
+  const int status = ibp_kv_attention_shared(&cache, &prefix, &table, dtype, (uint64_t)q_heads, (uint64_t)n_new, &q, &o, counts, scale,
+                                             workspace.defined() ? workspace.data_ptr() : nullptr,
+                                             workspace.defined() ? (uint64_t)workspace.numel() : 0, stream);
+  gradients.mark({out});
+  return Py_BuildValue("(iN)", status, THPVariable_Wrap(out));
+  END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"set_cache", (PyCFunction)(void (*)(void))set_cache, METH_FASTCALL, nullptr},
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, nullptr},
     {"attention", (PyCFunction)(void (*)(void))attention, METH_FASTCALL, nullptr},
     {"evict", (PyCFunction)(void (*)(void))evict, METH_FASTCALL, nullptr},
+    {"append_rotated", (PyCFunction)(void (*)(void))append_rotated, METH_FASTCALL, nullptr},
+    {"outline", (PyCFunction)(void (*)(void))outline, METH_FASTCALL, nullptr},
+    {"select", (PyCFunction)(void (*)(void))select, METH_FASTCALL, nullptr},
+    {"attention_shared", (PyCFunction)(void (*)(void))attention_shared, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

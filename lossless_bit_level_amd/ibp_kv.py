@@ -1,13 +1,15 @@
-"""Thin binding of libibp_kv (include/ibp_kv.h), same names as the C ABI: an
-8-bit KV page cache, the attention that reads it, and eviction of its pages by
-accumulated attention weight.
+"""Thin binding of libibp_kv and libibp_kv_long (include/ibp_kv.h,
+include/ibp_kv_long.h), same names as the C ABI: an 8-bit KV page cache, the
+attention that reads it, and eviction of its pages by accumulated attention
+weight; for long and shared contexts appends with rotated positions, outlines
+and selection of pages, and attention over a shared prefix.
 
 Argument marshalling only; every step runs in the HIP kernels of
-libibp_kv.so.  The structures and lib() are ctypes; the calls take torch
-tensors through a small extension module (csrc/ibp_kv_torch.cpp), since a
-decoding step makes many short ones: it checks the arguments, allocates
-results and calls the C ABI.  If either has not been built this module raises
-on first use; there is no fallback.
+libibp_kv.so and libibp_kv_long.so.  The structures, lib() and long_lib() are
+ctypes; the calls take torch tensors through a small extension module
+(csrc/ibp_kv_torch.cpp), since a decoding step makes many short ones: it checks
+the arguments, allocates results and calls the C ABI.  If one of them has not
+been built this module raises on first use; there is no fallback.
 
 No call has a gradient.  Codes and scales carry none; going backward through a
 result of inputs that require one raises, and a given output with such inputs
@@ -24,6 +26,7 @@ from .ibp import (IBP_ERR_HIP, IBP_ERR_INVALID_ARGUMENT, IBP_ERR_LAYOUT,  # noqa
                   IBP_ERR_UNSUPPORTED, IBP_OK)
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libibp_kv.so")
+_LONG_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libibp_kv_long.so")
 
 IBP_KV_BF16 = 0
 IBP_KV_FP16 = 1
@@ -33,7 +36,8 @@ class IBPKVError(RuntimeError):
     def __init__(self, fn: str, status: int):
         msg = f"{fn}: {status_string(status)} ({status})"
         if status == IBP_ERR_HIP:
-            msg += f", hipError {lib().ibp_kv_last_hip_error()}"
+            last = long_lib().ibp_kv_long_last_hip_error if fn in _LONG else lib().ibp_kv_last_hip_error
+            msg += f", hipError {last()}"
         super().__init__(msg)
         self.status = status
 
@@ -53,6 +57,22 @@ class ibp_kv_tensor(ctypes.Structure):
                 ("seq_stride", ctypes.c_int64),
                 ("token_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64)]
+
+
+class ibp_kv_rotation(ctypes.Structure):
+    """Tables of a rotation (see include/ibp_kv_long.h)."""
+    _fields_ = [("n_positions", ctypes.c_uint64),
+                ("rotary_dim", ctypes.c_uint32),
+                ("interleaved", ctypes.c_uint32),
+                ("cos", ctypes.c_void_p),
+                ("sin", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p)]
+
+
+class ibp_kv_outlines(ctypes.Structure):
+    """What bounds the keys of each page (see include/ibp_kv_long.h)."""
+    _fields_ = [("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
 
 
 class ibp_kv_cache(ctypes.Structure):
@@ -102,6 +122,40 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_long_lib = None
+_LONG = ("ibp_kv_append_rotated", "ibp_kv_outline", "ibp_kv_select", "ibp_kv_attention_shared")
+
+
+def long_lib() -> ctypes.CDLL:
+    """Load libibp_kv_long.so (built in-tree by lossless_bit_level_amd.build)."""
+    global _long_lib
+    if _long_lib is None:
+        if not os.path.exists(_LONG_LIB_PATH):
+            raise RuntimeError(f"{_LONG_LIB_PATH} is missing: build it with "
+                               "`python -m lossless_bit_level_amd.build`")
+        L = ctypes.CDLL(_LONG_LIB_PATH)
+        vp, u64, u32, i32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int
+        cache, table = ctypes.POINTER(ibp_kv_cache), ctypes.POINTER(ibp_kv_table)
+        tensor, outlines = ctypes.POINTER(ibp_kv_tensor), ctypes.POINTER(ibp_kv_outlines)
+        L.ibp_kv_append_rotated.argtypes = [cache, table, u32, u64, tensor, tensor, vp,
+                                            ctypes.POINTER(ibp_kv_rotation), u64, tensor, tensor,
+                                            outlines, vp]
+        L.ibp_kv_outline.argtypes = [cache, outlines, table, u64, vp, vp]
+        L.ibp_kv_select_workspace_bytes.argtypes = [cache, table]
+        L.ibp_kv_select.argtypes = [cache, outlines, table, u32, u64, u64, tensor, vp, u64, u64, u64,
+                                    vp, vp, vp, vp, u64, vp]
+        L.ibp_kv_attention_shared_workspace_bytes.argtypes = [cache, table, table, u64, u64]
+        L.ibp_kv_attention_shared.argtypes = [cache, table, table, u32, u64, u64, tensor, tensor, vp,
+                                              ctypes.c_float, vp, u64, vp]
+        L.ibp_kv_long_last_hip_error.argtypes = []
+        for f in (*_LONG, "ibp_kv_long_last_hip_error"):
+            getattr(L, f).restype = i32
+        for f in ("ibp_kv_select_workspace_bytes", "ibp_kv_attention_shared_workspace_bytes"):
+            getattr(L, f).restype = u64
+        _long_lib = L
+    return _long_lib
+
+
 _module = None
 
 
@@ -110,6 +164,7 @@ def _ext():
     global _module
     if _module is None:
         lib()
+        long_lib()
         try:
             from . import _ibp_kv
         except ImportError as e:
@@ -208,3 +263,107 @@ def ibp_kv_evict(pages: torch.Tensor, weights: torch.Tensor, lengths: torch.Tens
                                 recent_pages, pages_out, weights_out, lengths_out, _stream(pages))
     _check("ibp_kv_evict", status)
     return tuple(out)
+
+
+def ibp_kv_append_rotated(cache: ibp_kv_cache, pages: torch.Tensor, lengths: torch.Tensor,
+                          k: torch.Tensor, v: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor,
+                          positions: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                          q_out: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                          interleaved: bool = False,
+                          outlines: tuple[torch.Tensor, torch.Tensor] | None = None, stream=None):
+    """ibp_kv_append of keys whose positions are rotated on the way.  cos, sin:
+    float32 [n_positions, rotary_dim / 2]; pairs are dims i and i +
+    rotary_dim / 2 or, interleaved, 2 i and 2 i + 1.  positions: int32
+    [n_seqs, n_new] (default: the tokens' places in their rows).  With q
+    ([n_seqs, n_new, q_heads, head_dim], the type of k) the queries are rotated
+    too, into q_out (default: a new tensor; q itself is allowed), which is
+    returned.  outlines: (int8 [n_pages, 2, head_dim], float32 [n_pages]),
+    brought up to date for the pages that receive tokens.  Asynchronous on the
+    current stream of the tensors' GPU, or on stream=."""
+    if stream is not None:
+        with _on(stream, pages):
+            return ibp_kv_append_rotated(cache, pages, lengths, k, v, cos, sin, positions, q, q_out,
+                                         counts, interleaved, outlines)
+    codes, scales = outlines if outlines is not None else (None, None)
+    status, out = _ext().append_rotated(cache, pages, lengths, k, v, cos, sin, positions, q, q_out,
+                                        counts, interleaved, codes, scales, _stream(pages))
+    _check("ibp_kv_append_rotated", status)
+    return out
+
+
+def ibp_kv_outline(cache: ibp_kv_cache, outlines: tuple[torch.Tensor, torch.Tensor],
+                   pages: torch.Tensor, lengths: torch.Tensor, n_new: int | None = None,
+                   counts: torch.Tensor | None = None, stream=None):
+    """Outlines (int8 [n_pages, 2, head_dim], float32 [n_pages]) of the pages
+    that hold the rows' last tokens: n_new of them or, with counts (int32
+    [n_seqs]), each sequence's own number up to n_new; by default of all pages
+    that hold tokens.  Asynchronous on the current stream of the tensors' GPU,
+    or on stream=."""
+    if stream is not None:
+        with _on(stream, pages):
+            return ibp_kv_outline(cache, outlines, pages, lengths, n_new, counts)
+    _check("ibp_kv_outline",
+           _ext().outline(cache, *outlines, pages, lengths, n_new, counts, _stream(pages)))
+
+
+def ibp_kv_select_workspace_bytes(cache: ibp_kv_cache, pages: torch.Tensor,
+                                  lengths: torch.Tensor) -> int:
+    table = ibp_kv_table(*pages.shape, pages.data_ptr(), lengths.data_ptr())
+    return int(long_lib().ibp_kv_select_workspace_bytes(cache, table))
+
+
+def ibp_kv_select(cache: ibp_kv_cache, outlines: tuple[torch.Tensor, torch.Tensor],
+                  pages: torch.Tensor, lengths: torch.Tensor, q: torch.Tensor, keep_pages: int,
+                  sink_pages: int = 1, recent_pages: int = 1, counts: torch.Tensor | None = None,
+                  pages_out: torch.Tensor | None = None, lengths_out: torch.Tensor | None = None,
+                  places_out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                  stream=None):
+    """For each row the pages that its new tokens' queries q ([n_seqs, n_new,
+    q_heads, head_dim]) are to attend over: the first sink_pages, the last
+    recent_pages (which must cover the new tokens) and, of those between, the
+    ones whose outlines promise the largest scores, keep_pages at most.  Returns
+    (pages, lengths, places): int32 [n_seqs, kv_heads, keep_pages] ids in table
+    order, -1 past the kept ones; the tokens of the kept pages; and the pages'
+    places in the row's table.  The first two are a table for
+    ibp_kv_attention.  workspace: a uint8 GPU tensor of at least
+    ibp_kv_select_workspace_bytes (default: allocated).  Asynchronous on the
+    current stream of the tensors' GPU, or on stream=."""
+    if stream is not None:
+        with _on(stream, pages):
+            return ibp_kv_select(cache, outlines, pages, lengths, q, keep_pages, sink_pages,
+                                 recent_pages, counts, pages_out, lengths_out, places_out, workspace)
+    status, *out = _ext().select(cache, *outlines, pages, lengths, q, keep_pages, sink_pages,
+                                 recent_pages, counts, pages_out, lengths_out, places_out, workspace,
+                                 _stream(pages))
+    _check("ibp_kv_select", status)
+    return tuple(out)
+
+
+def ibp_kv_attention_shared_workspace_bytes(cache: ibp_kv_cache, prefix_pages: torch.Tensor,
+                                            prefix_lengths: torch.Tensor, pages: torch.Tensor,
+                                            lengths: torch.Tensor, q_heads: int, n_new: int) -> int:
+    prefix = ibp_kv_table(1, *prefix_pages.shape, prefix_pages.data_ptr(), prefix_lengths.data_ptr())
+    table = ibp_kv_table(*pages.shape, pages.data_ptr(), lengths.data_ptr())
+    with torch.cuda.device_of(pages):
+        return int(long_lib().ibp_kv_attention_shared_workspace_bytes(cache, prefix, table, q_heads, n_new))
+
+
+def ibp_kv_attention_shared(cache: ibp_kv_cache, prefix_pages: torch.Tensor,
+                            prefix_lengths: torch.Tensor, pages: torch.Tensor,
+                            lengths: torch.Tensor, q: torch.Tensor, scale: float | None = None,
+                            counts: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                            workspace: torch.Tensor | None = None, stream=None):
+    """ibp_kv_attention of sequences that begin with the same tokens, those of
+    prefix_pages (int32 [kv_heads, max_prefix_pages]) and prefix_lengths (int32
+    [kv_heads]), which are read once for all of them; pages and lengths are the
+    sequences' own.  workspace: a uint8 GPU tensor of at least
+    ibp_kv_attention_shared_workspace_bytes (default: allocated).  Returns out.
+    Asynchronous on the current stream of the tensors' GPU, or on stream=."""
+    if stream is not None:  # what the call allocates is the stream's too
+        with _on(stream, pages):
+            return ibp_kv_attention_shared(cache, prefix_pages, prefix_lengths, pages, lengths, q,
+                                           scale, counts, out, workspace)
+    status, out = _ext().attention_shared(cache, prefix_pages, prefix_lengths, pages, lengths, q,
+                                          scale, counts, out, workspace, _stream(q))
+    _check("ibp_kv_attention_shared", status)
+    return out
