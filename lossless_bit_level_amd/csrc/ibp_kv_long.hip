@@ -637,14 +637,285 @@ __global__ __launch_bounds__(kThreads) void select_long_kernel(Select s) {
 
 // ---------------------------------------------------- a shared prefix ----
 
-template <int DJ, bool F16, int MT, bool ONCE>
-__global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, MT)) void prefix_kernel(Attention a) {
-  attend_part<DJ, F16, MT, ONCE, Sums::kShared>(a, blockIdx.x);
+// A prefix under many query rows, where the arithmetic counts.  As attend_part, a
+// workgroup takes one part of one unit and its waves take steps of 32 tokens in
+// turn; but a unit is four groups of 16 query rows (two of wide heads), whose
+// queries are in LDS, where all waves read them, and two waves share a SIMD, so
+// that one's matrix instructions run beside the other's exponentials.
+//
+// An exponential is taken once, of the score plus the logarithm of the values'
+// scale,
+//     z_j = exp2(s_j + log2(vs_j) - M),
+// so that the second product takes z as it is, with the codes; its largest is what
+// M follows.  The softmax's sum needs exp2(s_j) alone: with L the logarithm of the
+// part's largest scale, rounded up, a tile's sum of z times 2^L / vs is that in
+// units of 2^(M - L).  (Pages whose scale is below 2^(L - 64) count as zeros, and
+// their weight counts.)  z is held between 2^-24 and 2^kTop, M a step of 2^kStart
+// below the largest so far: in fp16 that is 11 bits of each weight of at least
+// 2^-21 of the largest.  Outputs of bf16 have 8; for those of fp16 what the
+// rounding cuts off goes through the product as well.
+constexpr float kTop = 15.f, kStart = 7.f;
+constexpr int many_tiles(int dj) { return dj <= 2 ? 4 : 2; }  // groups of 16 query rows
+
+__device__ __forceinline__ float maximum(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+template <int DJ, int MT>
+struct ManyLds {
+  union {
+    u32x4 q[MT][DJ][2][kWave];  // as the lanes of the matrix instructions take them
+    float o[kWaves][16][64 + 4];
+  };
+  f32x2 ml[kWaves][MT * 16];
+  float top[kWaves];
+};
+
+// Logarithm of a scale above 0; exact for powers of two.
+__device__ __forceinline__ float log2_scale(float x) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, x);
+  if ((b & 0x7FFFFFu) == 0 && b >= 0x00800000u) return (float)((int)(b >> 23) - 127);
+  return log2_fast(x * 0x1p64f) - 64.f;
 }
 
-template <int DJ, bool F16, int MT, bool ONCE>
-__global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, MT)) void own_kernel(Attention a) {
-  attend_part<DJ, F16, MT, ONCE, Sums::kLeft>(a, blockIdx.x);
+template <int DJ, bool F16>
+__device__ __forceinline__ void attend_many(const Attention& a, uint32_t block) {
+  constexpr int D = 64 * DJ, MT = many_tiles(DJ), ST = 2;
+  __shared__ __attribute__((aligned(16))) ManyLds<DJ, MT> lds;
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const Part part = part_of_shared(a, block);
+  const Plan p = plan_shared<MT, ST>(a, part);
+  const int first = part.index * p.part_steps, last = min(first + p.part_steps, p.steps);
+  if (first >= last) return;
+
+  // the queries, negated where the scale is below 0, so that the largest product gives
+  // the largest score
+  const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
+  for (int i = wave; i < MT * DJ; i += kWaves) {
+    const int mt = i / DJ, j = i % DJ, m = p.m0 + mt * 16 + lane % 16;
+    u32x4 x[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    if (m < a.m_rows) {
+      const uint16_t* src = row_of_all(a.q, a, p, m) + 64 * j + 16 * (lane / 16);
+      x[0] = load8(src, a.q.wide);
+      x[1] = load8(src + 8, a.q.wide);
+    }
+    lds.q[mt][j][0][lane] = x[0] ^ sign;
+    lds.q[mt][j][1][lane] = x[1] ^ sign;
+  }
+  // the largest scale
+  const int tiles_of_page = 1 << a.pool.tile_shift;
+  float top_scale = 0.f;
+  {
+    const int from = first * ST / tiles_of_page, to = (min(last * ST, p.tiles) + tiles_of_page - 1) / tiles_of_page;
+    const int32_t* pages = a.rows.pages + (uint64_t)p.row * a.rows.max_pages;
+    for (int i = from + (int)threadIdx.x; i < to; i += kThreads) {
+      const uint32_t id = (uint32_t)pages[i];
+      const float x = id < a.pool.n_pages ? fabsf(a.pool.v_scales[id]) : 0.f;
+      top_scale = fmaxf(top_scale, finite(x) ? x : 0.f);
+    }
+  }
+  top_scale = wave_max(top_scale);
+  if (lane == 0) lds.top[wave] = top_scale;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) top_scale = fmaxf(top_scale, lds.top[w]);
+  const int scale_log = uniform(held_exponent(fmaxf(top_scale, 0x1p-126f)));  // L
+  const float c_scale = fabsf(a.scale);
+
+  State<DJ, MT> st;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    st.m[mt] = -INFINITY;
+    st.l[mt] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4 * DJ; ++i) st.o[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  int step = first + wave;
+  if (step < last) {
+    u32x4 k[ST][DJ], v[ST][DJ];
+    Where<ST> here = find_step<DJ, ST>(a, p, step, ids_of_step<ST>(a, p, step));
+    Ids<ST> ids = ids_of_step<ST>(a, p, min(step + kWaves, last - 1));
+    load_tiles<DJ, ST, false>(a.pool.k_codes, here, lane * 16, k);
+    load_tiles<DJ, ST, false>(a.pool.v_codes, here, lane * 16, v);
+    while (true) {
+      const int next_step = step + kWaves;
+      const bool more = next_step < last;
+      const int byte = more ? lane * 16 : 0;
+      arrive<ST>(here, ids);
+      Where<ST> next = find_step<DJ, ST>(a, p, more ? next_step : step, ids);
+      ids = ids_of_step<ST>(a, p, min(next_step + kWaves, last - 1));
+      f32x4 s[MT][ST];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int t = 0; t < ST; ++t) s[mt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < DJ; ++j)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          u32x4 kk[ST];
+#pragma unroll
+          for (int t = 0; t < ST; ++t) kk[t] = widen8<F16>(k[t][j][2 * half], k[t][j][2 * half + 1]);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const u32x4 q = lds.q[mt][j][half][lane];
+#pragma unroll
+            for (int t = 0; t < ST; ++t) s[mt][t] = mfma<F16>(kk[t], q, s[mt][t]);
+          }
+        }
+      load_tiles<DJ, ST, false>(a.pool.k_codes, next, byte, k);
+      float c[ST], lv[ST], back[ST];
+      bool plain = (step + 1) * (kTile * ST) <= p.full;
+#pragma unroll
+      for (int t = 0; t < ST; ++t) {
+        const uint32_t bits = __builtin_bit_cast(uint32_t, here.vs[t]);
+        const int e = (int)(bits >> 23) - 127;
+        // a power of two, not far below the largest; keys of a scale below 0 turn the order
+        plain = plain && here.ok[t] && (bits & 0x807FFFFFu) == 0 && e >= -126 && e > scale_log - 64 && e < 128 && here.ks[t] >= 0.f;
+        lv[t] = (float)e;
+        back[t] = power2(min(max(scale_log - e, 0), 64));
+        c[t] = here.ks[t] * c_scale;
+      }
+      if (!plain) {
+#pragma unroll
+        for (int t = 0; t < ST; ++t) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) s[mt][t] *= c[t];
+          c[t] = 1.f;
+        }
+        int seen[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) seen[mt] = p.end;
+        mask_step<DJ, MT, ST>(p, step, lane, seen, here, s, v, st);
+#pragma unroll
+        for (int t = 0; t < ST; ++t) {
+          const float size = fabsf(here.vs[t]);
+          const float l = size > 0.f ? log2_scale(size) : -INFINITY;
+          const uint32_t turn = here.vs[t] < 0.f ? 0x80808080u : 0u;
+          const bool none = l < (float)(scale_log - 64);
+          lv[t] = none ? (float)scale_log : l;
+          back[t] = exp2_fast((float)scale_log - lv[t]);
+#pragma unroll
+          for (int h = 0; h < DJ; ++h) v[t][h] = none ? u32x4{0, 0, 0, 0} : v[t][h] ^ turn;
+        }
+      }
+      float top[MT];
+      bool higher = false;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        top[mt] = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < ST; ++t) {
+          const float x = maximum(maximum(maximum(s[mt][t][0], s[mt][t][1]), s[mt][t][2]), s[mt][t][3]);
+          top[mt] = maximum(top[mt], __builtin_fmaf(x, c[t], lv[t]));
+        }
+        higher = higher || top[mt] > st.m[mt] + kTop;
+      }
+      if (__ballot(higher)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const float m = fmaxf(st.m[mt], query_max(top[mt]) - kStart);
+          const float keep = exp2_fast(st.m[mt] - (m == -INFINITY ? 0.f : m));
+          st.m[mt] = m;
+          st.l[mt] *= keep;
+#pragma unroll
+          for (int i = 0; i < 4 * DJ; ++i) st.o[mt][i] *= keep;
+        }
+      }
+      u32x4 hi[MT], lo[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const float base = st.m[mt] == -INFINITY ? 0.f : st.m[mt];
+#pragma unroll
+        for (int t = 0; t < ST; ++t) {
+          const float b = lv[t] - base;
+          float z[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) z[r] = exp2_fast(__builtin_fmaf(s[mt][t][r], c[t], b));
+          st.l[mt] = __builtin_fmaf((z[0] + z[1]) + (z[2] + z[3]), back[t], st.l[mt]);
+          f16x2 h0 = {(_Float16)z[0], (_Float16)z[1]}, h1 = {(_Float16)z[2], (_Float16)z[3]};
+          hi[mt][2 * t] = __builtin_bit_cast(uint32_t, h0);
+          hi[mt][2 * t + 1] = __builtin_bit_cast(uint32_t, h1);
+          if constexpr (F16) {
+            const f16x2 r0 = {(_Float16)(z[0] - (float)h0[0]), (_Float16)(z[1] - (float)h0[1])};
+            const f16x2 r1 = {(_Float16)(z[2] - (float)h1[0]), (_Float16)(z[3] - (float)h1[1])};
+            lo[mt][2 * t] = __builtin_bit_cast(uint32_t, r0);
+            lo[mt][2 * t + 1] = __builtin_bit_cast(uint32_t, r1);
+          }
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < DJ; ++h)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const u32x4 vv = widen8<true>(v[0][h][x], v[1][h][x]);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            st.o[mt][h * 4 + x] = mfma<true>(vv, hi[mt], st.o[mt][h * 4 + x]);
+            if constexpr (F16) st.o[mt][h * 4 + x] = mfma<true>(vv, lo[mt], st.o[mt][h * 4 + x]);
+          }
+        }
+      load_tiles<DJ, ST, false>(a.pool.v_codes, next, byte, v);
+      if (!more) break;
+      here = next;
+      step = next_step;
+    }
+  }
+  // the waves' sums together, a group of 16 query rows and 64 dims at a time; left with
+  // the statistics that attend_part leaves, of the scores alone
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    st.l[mt] = pair_sum16(st.l[mt], st.l[mt]);
+    st.l[mt] = pair_sum32(st.l[mt], st.l[mt]);
+  }
+  if (lane < 16) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) lds.ml[wave][mt * 16 + lane] = f32x2{st.m[mt], st.l[mt]};
+  }
+  __syncthreads();
+  const int n = threadIdx.x / 16, d4 = threadIdx.x % 16 * 4;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int m_local = mt * 16 + n, m = p.m0 + m_local;
+    float top = -INFINITY, total = 0.f, f[kWaves];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds.ml[w][m_local][0]);
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      f[w] = exp2_fast(lds.ml[w][m_local][0] - base - kTop);
+      total += lds.ml[w][m_local][1] * f[w];
+    }
+    const uint64_t slot = (uint64_t)part.slot * a.unit_rows.d + m_local;
+    const bool there = m_local < (int)a.unit_rows.d && m < a.m_rows;
+    if (d4 == 0 && there) a.ws_ml[slot] = f32x2{top + kTop - (float)scale_log, total};
+    const float unit = power2(scale_log);
+#pragma unroll
+    for (int h = 0; h < DJ; ++h) {
+      __syncthreads();
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        *(f32x4*)&lds.o[wave][lane % 16][16 * x + 4 * (lane / 16)] = st.o[mt][h * 4 + x];
+      __syncthreads();
+      f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) o += *(const f32x4*)&lds.o[w][n][d4] * f[w];
+      if (there) *(f32x4*)(a.ws_o + slot * D + 64 * h + d4) = o * unit;
+    }
+  }
+}
+
+// The first workgroups take the prefix (KIND 1 and 2: one unit of as many groups of
+// 16 query rows to a head; 0: many), the others the rows' own tokens, MT groups of
+// query rows to a unit.  One launch: the rows' workgroups take the places of the
+// prefix's as these end.
+template <int DJ, bool F16, int KIND, int MT, bool ONCE>
+__global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, KIND > MT ? KIND : MT)) void shared_kernel(Attention a, Attention b,
+                                                                                       uint32_t prefix_blocks) {
+  if (blockIdx.x >= prefix_blocks) return attend_part<DJ, F16, MT, ONCE, Sums::kLeft>(b, blockIdx.x - prefix_blocks);
+  if constexpr (KIND == 0)
+    attend_many<DJ, F16>(a, blockIdx.x);
+  else
+    attend_part<DJ, F16, KIND, true, Sums::kShared>(a, blockIdx.x);
 }
 
 // Joins the sums over the prefix (a) with those over a row's own tokens (b), a
@@ -778,6 +1049,7 @@ void launch_score(const Select& s, uint64_t n_rows, uint32_t dtype, hipStream_t 
 struct SharedShape {
   Shape own;
   int mt, step;
+  bool many;
   int32_t m_rows, m_groups, unit_rows;
   uint32_t n_units, parts, n_rows, join_blocks;
   uint64_t own_o, ml, own_ml, own_of, bytes;
@@ -792,19 +1064,20 @@ bool make_shared_shape(uint64_t n_seqs, uint64_t heads, uint64_t prefix_pages, u
   if (m && heads > 0x7FFFFFFFull / m) return false;
   const int dj = (int)head_dim / 64;
   s->m_rows = (int32_t)m;
-  s->mt = m <= 16 ? 1 : m <= 32 || dj > 2 ? 2 : 4;
-  s->step = step_tiles(dj, s->mt);
+  s->many = m > 32;
+  s->mt = m <= 16 ? 1 : m <= 32 ? 2 : many_tiles(dj);
+  s->step = s->many ? 2 : step_tiles(dj, s->mt);
   const uint64_t per_unit = 16ull * s->mt;
   s->m_groups = (int32_t)((m + per_unit - 1) / per_unit);
   s->unit_rows = (int32_t)std::min<uint64_t>(m, per_unit);
   const uint64_t units = heads * s->m_groups;
   s->n_units = (uint32_t)units;
   const uint64_t steps = (prefix_pages * page_tokens / kTile + s->step - 1) / s->step;
-  const uint64_t slots = (uint64_t)workgroups_per_unit(dj, s->mt) * cus;
+  const uint64_t slots = (uint64_t)workgroups_per_unit(dj, s->many ? s->own.mt : s->mt) * cus / (s->many ? 1 : 2);
   s->parts = 1;
   if (units)
     s->parts = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>({slots / units, (steps + kWaves - 1) / kWaves, (uint64_t)kMaxParts}));
-  if (units * s->parts > max_grid(kThreads)) return false;
+  if (units * s->parts + s->own.n_parts > max_grid(kThreads)) return false;
   const uint64_t shared_slots = units * s->parts * s->unit_rows, own_slots = (uint64_t)s->own.n_parts * s->own.unit_rows;
   s->own_o = shared_slots * head_dim * 4;
   s->ml = s->own_o + own_slots * head_dim * 4;
@@ -816,32 +1089,28 @@ bool make_shared_shape(uint64_t n_seqs, uint64_t heads, uint64_t prefix_pages, u
   return s->join_blocks <= max_grid(kThreads);
 }
 
-template <int DJ, bool F16, int MT>
-void launch_prefix(const Attention& a, uint32_t blocks, hipStream_t st) {
-  if (a.m_groups.d == 1)
-    hipLaunchKernelGGL((prefix_kernel<DJ, F16, MT, true>), dim3(blocks), dim3(kThreads), 0, st, a);
-  else
-    hipLaunchKernelGGL((prefix_kernel<DJ, F16, MT, false>), dim3(blocks), dim3(kThreads), 0, st, a);
-}
-
 template <int DJ, bool F16>
 void launch_shared(const Attention& a, const Attention& b, const SharedShape& s, const Divisor& rows_of_head,
                    hipStream_t st) {
-  const uint32_t blocks = s.n_units * s.parts;
-  if (s.mt == 1) launch_prefix<DJ, F16, 1>(a, blocks, st);
-  if (s.mt == 2) launch_prefix<DJ, F16, 2>(a, blocks, st);
-  if constexpr (DJ <= 2)
-    if (s.mt == 4) launch_prefix<DJ, F16, 4>(a, blocks, st);
-  const dim3 own(s.own.n_parts), join(s.join_blocks);
+  const uint32_t prefix = s.n_units * s.parts;
+  const dim3 grid(prefix + s.own.n_parts), join(s.join_blocks), threads(kThreads);
+  const bool several = b.m_groups.d > 1;  // units of own query rows; those of the prefix are many then
   if (s.own.mt == 1) {
-    hipLaunchKernelGGL((own_kernel<DJ, F16, 1, true>), own, dim3(kThreads), 0, st, b);
-    hipLaunchKernelGGL((join_shared_kernel<DJ, F16, 1>), join, dim3(kThreads), 0, st, a, b, rows_of_head, s.n_rows, s.step);
-  } else {
-    if (b.m_groups.d == 1)
-      hipLaunchKernelGGL((own_kernel<DJ, F16, kQueryTiles, true>), own, dim3(kThreads), 0, st, b);
+    if (s.many)
+      hipLaunchKernelGGL((shared_kernel<DJ, F16, 0, 1, true>), grid, threads, 0, st, a, b, prefix);
+    else if (s.mt == 1)
+      hipLaunchKernelGGL((shared_kernel<DJ, F16, 1, 1, true>), grid, threads, 0, st, a, b, prefix);
     else
-      hipLaunchKernelGGL((own_kernel<DJ, F16, kQueryTiles, false>), own, dim3(kThreads), 0, st, b);
-    hipLaunchKernelGGL((join_shared_kernel<DJ, F16, kQueryTiles>), join, dim3(kThreads), 0, st, a, b, rows_of_head, s.n_rows, s.step);
+      hipLaunchKernelGGL((shared_kernel<DJ, F16, 2, 1, true>), grid, threads, 0, st, a, b, prefix);
+    hipLaunchKernelGGL((join_shared_kernel<DJ, F16, 1>), join, threads, 0, st, a, b, rows_of_head, s.n_rows, s.step);
+  } else {
+    if (several)
+      hipLaunchKernelGGL((shared_kernel<DJ, F16, 0, kQueryTiles, false>), grid, threads, 0, st, a, b, prefix);
+    else if (s.many)
+      hipLaunchKernelGGL((shared_kernel<DJ, F16, 0, kQueryTiles, true>), grid, threads, 0, st, a, b, prefix);
+    else
+      hipLaunchKernelGGL((shared_kernel<DJ, F16, 2, kQueryTiles, true>), grid, threads, 0, st, a, b, prefix);
+    hipLaunchKernelGGL((join_shared_kernel<DJ, F16, kQueryTiles>), join, threads, 0, st, a, b, rows_of_head, s.n_rows, s.step);
   }
 }
 

@@ -406,6 +406,11 @@ def test_no_page_left_out_has_a_larger_score(kv):
 # ------------------------------------------------------ shared prefixes ----
 
 
+# Half a step of the weights in the second product: 11 bits for outputs of 8, else 16
+# (a relative error of 2^-11 at most, an eighth of the output's own).
+WEIGHT = {torch.bfloat16: 2.0 ** -11, torch.float16: 2.0 ** -16}
+
+
 def shared_pool(kv, seqs, heads, prefix_pages, own_pages, pt, d, seed=0, n_pages=4096):
     """Pages of random codes; tables of a prefix and of own pages over them."""
     p = noise(kv, seqs, heads, own_pages, pt, d, seed, n_pages)
@@ -422,7 +427,8 @@ def check_shared(kv, p, prefix_lengths, lengths, q, scale=None, counts=None, gpu
     torch.cuda.synchronize()
     fi = torch.finfo(q.dtype)
     o, err = lorc.attention_shared(p.k, p.v, p.pt, p.prefix, prefix_lengths, p.pages, lengths, q.double().numpy(),
-                                   p.d ** -0.5 if scale is None else scale, c, rounding=fi.eps / 2, tiny=fi.tiny * fi.eps / 2)
+                                   p.d ** -0.5 if scale is None else scale, c, rounding=fi.eps / 2, tiny=fi.tiny * fi.eps / 2,
+                                   weight=WEIGHT[q.dtype])
     close(out.cpu(), None, (o, None, err, None))
     return out
 
@@ -714,5 +720,5 @@ def test_pool_past_32_bits(kv):
     out = kv.ibp_kv_attention_shared(cache, gpu(ids[0]), gpu(np.array([n], np.int32)), gpu(ids[:, :, ::-1]), gpu(np.array([[33]], np.int32)), q.cuda())
     torch.cuda.synchronize()
     o_, err = lorc.attention_shared(small.k, small.v, pt, small.pages[0], np.array([n]), small.pages[:, :, ::-1], np.array([[33]]),
-                                    q.double().numpy(), d ** -0.5, rounding=2.0 ** -8, tiny=0)
+                                    q.double().numpy(), d ** -0.5, rounding=2.0 ** -8, tiny=0.0, weight=WEIGHT[torch.bfloat16])
     close(out.cpu(), None, (o_, None, err, None))

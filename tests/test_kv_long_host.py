@@ -135,7 +135,8 @@ def test_shared_oracle_is_attention_of_whole_rows():
     out, err = lorc.attention_shared(*pools, pt, prefix, np.array([48, 48]), pages, lengths, q, 0.05, rounding=0.0)
     whole = np.concatenate([np.broadcast_to(prefix, (seqs, heads, 3)), pages], 2)
     want, _, err2, _ = orc.attention(*pools, pt, whole, lengths + 48, q, 0.05)
-    assert np.allclose(out, want, rtol=1e-12, atol=1e-12) and np.allclose(err, err2, rtol=1e-9)
+    assert np.allclose(out, want, rtol=1e-12, atol=1e-12)
+    assert (err >= err2).all() and np.allclose(err, err2, rtol=0.05)
 
 
 # ------------------------------------------------------------ the library --
