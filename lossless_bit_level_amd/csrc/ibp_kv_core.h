@@ -482,7 +482,9 @@ __device__ __forceinline__ void append_tile(const Pool& pool, const Rows& rows, 
       v_max = fmaxf(v_max, s_max[1][w + n]);
     }
   }
-  if (!live) return;
+  if constexpr (!Turn::kTurns)
+    if (!live) return;
+  const bool there = Turn::kTurns ? live : true;  // a turned page's waves stay for its outline
   int ke = scale_exponent(k_max), ve = scale_exponent(v_max);
   if (held) {
     ke = max(ke, held_exponent(k_was));
@@ -494,7 +496,7 @@ __device__ __forceinline__ void append_tile(const Pool& pool, const Rows& rows, 
   const float k_inv = power2(-ke), v_inv = power2(-ve);
   const float k_ratio = k_was * k_inv, v_ratio = v_was * v_inv;
   const bool k_plain = !k_odd && ke > kExpMin && ke < kExpMax, v_plain = !v_odd && ve > kExpMin && ve < kExpMax;
-  if (tile == 0 && lane == 0) {
+  if (there && tile == 0 && lane == 0) {
     pool.k_scales[id] = k_scale;
     pool.v_scales[id] = v_scale;
   }
@@ -503,6 +505,7 @@ __device__ __forceinline__ void append_tile(const Pool& pool, const Rows& rows, 
   uint8_t* vp = pool.v_codes + base + lane * 16;
 
   const bool k_old = kt < first;
+  u32x4 kc[DJ];
 #pragma unroll
   for (int j = 0; j < DJ; ++j) {
     u32x4 c;
@@ -513,15 +516,17 @@ __device__ __forceinline__ void append_tile(const Pool& pool, const Rows& rows, 
       else
         c[i] = codes_of<F16>(kx[j][i / 2][i % 2 * 2], kx[j][i / 2][i % 2 * 2 + 1], k_plain, k_scale, k_inv);
     }
-    if (k_old) {
+    if (there && k_old) {
       c = *(const u32x4*)(kp + j * kUnit);
       if (k_ratio != 1.f) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[i] = rescale4(c[i], k_ratio);
       }
     }
-    __builtin_nontemporal_store(c, (u32x4*)(kp + j * kUnit));
+    if (there) __builtin_nontemporal_store(c, (u32x4*)(kp + j * kUnit));
+    kc[j] = c;
   }
+  if constexpr (Turn::kTurns) turn.template outline<DJ>(kc, wave, lane, tile, tiles, min(end - at, kTile), there, (uint32_t)id, k_scale);
 
   uint32_t* tile_words = s_tile[wave];
 #pragma unroll
@@ -548,7 +553,7 @@ __device__ __forceinline__ void append_tile(const Pool& pool, const Rows& rows, 
 #pragma unroll
   for (int j = 0; j < DJ; ++j) {
     u32x4 c = *(const u32x4*)(tile_words + j * 256 + lane * 4);
-    if (old) {
+    if (there && old) {
       const u32x4 was = *(const u32x4*)(vp + j * kUnit);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -556,7 +561,7 @@ __device__ __forceinline__ void append_tile(const Pool& pool, const Rows& rows, 
         c[i] = (c[i] & ~old) | (w & old);
       }
     }
-    __builtin_nontemporal_store(c, (u32x4*)(vp + j * kUnit));
+    if (there) __builtin_nontemporal_store(c, (u32x4*)(vp + j * kUnit));
   }
 }
 // ----------------------------------------------------------- attention ----

@@ -9,8 +9,6 @@ namespace {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
-// ------------------------------------------------------------- rotation ----
-
 struct Angles {
   const float* cos;
   const float* sin;
@@ -18,6 +16,133 @@ struct Angles {
   uint32_t n_positions;
   int32_t half;  // pairs
 };
+
+// ------------------------------------------------ largest and smallest ----
+
+// NaN wins.
+__device__ __forceinline__ f16x2 pair_max(f16x2 a, f16x2 b) { return __builtin_elementwise_maximum(a, b); }
+__device__ __forceinline__ f16x2 pair_min(f16x2 a, f16x2 b) { return __builtin_elementwise_minimum(a, b); }
+
+// Smallest e with a <= 127 * 2^e (127 = 1.984375 * 2^6), for a > 0.
+__device__ __forceinline__ int whole_exponent(float a) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, a);
+  return (int)(b >> 23) - 127 - 6 + ((b & 0x7FFFFFu) > 0x7E0000u ? 1 : 0);
+}
+
+// What lanes l and l ^ 16 (l ^ 32) hold, the same in both.
+struct Pair16 {
+  f16x2 a, b;
+};
+__device__ __forceinline__ Pair16 both16(f16x2 x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto y = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return {__builtin_bit_cast(f16x2, (uint32_t)y[0]), __builtin_bit_cast(f16x2, (uint32_t)y[1])};
+}
+__device__ __forceinline__ Pair16 both32(f16x2 x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto y = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return {__builtin_bit_cast(f16x2, (uint32_t)y[0]), __builtin_bit_cast(f16x2, (uint32_t)y[1])};
+}
+
+// The largest and the smallest so far of the numbers of four codes (a word) in each
+// of several tokens; NaN where one was.
+struct Bounds4 {
+  f16x2 hi[2], lo[2];
+  __device__ __forceinline__ void clear() {
+    hi[0] = hi[1] = f16x2{-INFINITY, -INFINITY};
+    lo[0] = lo[1] = f16x2{INFINITY, INFINITY};
+  }
+  // Two words, since an instruction takes the largest of three.
+  __device__ __forceinline__ void take(uint32_t a, uint32_t b) {
+    const f16x2 a0 = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.f, false));
+    const f16x2 a1 = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.f, true));
+    const f16x2 b0 = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.f, false));
+    const f16x2 b1 = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.f, true));
+    hi[0] = pair_max(pair_max(hi[0], a0), b0);
+    hi[1] = pair_max(pair_max(hi[1], a1), b1);
+    lo[0] = pair_min(pair_min(lo[0], a0), b0);
+    lo[1] = pair_min(pair_min(lo[1], a1), b1);
+  }
+  __device__ __forceinline__ void join(const Bounds4& x) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      hi[h] = pair_max(hi[h], x.hi[h]);
+      lo[h] = pair_min(lo[h], x.lo[h]);
+    }
+  }
+  __device__ __forceinline__ float largest() const {  // magnitude: hi >= lo
+    const f16x2 x = pair_max(pair_max(hi[0], -lo[0]), pair_max(hi[1], -lo[1]));
+    return __builtin_elementwise_maximum((float)x[0], (float)x[1]);
+  }
+};
+
+// Four numbers in units of 1 / per, rounded up, or down.
+template <bool UP>
+__device__ __forceinline__ uint32_t whole4(const f16x2 (&x)[2], float per) {
+  uint32_t word = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const float y = (float)x[b / 2][b % 2] * per;
+    word |= (uint32_t)((int)(UP ? __builtin_ceilf(y) : __builtin_floorf(y)) & 255) << (8 * b);
+  }
+  return word;
+}
+
+// Bounds of the keys of a tile, four dims to a lane, through the wave's words in LDS:
+// kc are the lane's codes of token lane % 16, dims 64 j + 16 (lane / 16) + 0..15, as
+// pages have them; the tile has `tokens` of them (none: at most 0).  A lane reads its
+// dims of a run of tokens and joins them with the lanes that have the others.
+constexpr int kKeyPitch = 64 + 4;  // words of 16 dims, so that lanes of different dims read different banks
+
+template <int DJ>
+__device__ __forceinline__ Bounds4 tile_bounds(const u32x4 (&kc)[DJ], uint32_t* words, int lane, int tokens) {
+  constexpr int kLanes = 16 * DJ, kParts = kWave / kLanes;  // of a token, of the tokens
+  constexpr int kRun = kTile / kParts;
+#pragma unroll
+  for (int j = 0; j < DJ; ++j) *(u32x4*)(words + (4 * j + lane / 16) * kKeyPitch + 4 * (lane % 16)) = kc[j];
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  const int r = lane % kLanes, from = min(lane / kLanes, kParts - 1) * kRun;
+  Bounds4 x;
+  x.clear();
+  if (tokens > 0) {
+    auto word = [&](int i) { return words[r / 4 * kKeyPitch + 4 * min(from + i, tokens - 1) + r % 4]; };
+#pragma unroll
+    for (int i = 0; i < kRun; i += 2) x.take(word(i), word(i + 1));  // past the tile's tokens the last one again
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if constexpr (DJ == 1) {
+      const Pair16 y = both16(x.hi[h]), z = both16(x.lo[h]);
+      x.hi[h] = pair_max(y.a, y.b);
+      x.lo[h] = pair_min(z.a, z.b);
+    }
+    if constexpr (DJ <= 2) {
+      const Pair16 y = both32(x.hi[h]), z = both32(x.lo[h]);
+      x.hi[h] = pair_max(y.a, y.b);
+      x.lo[h] = pair_min(z.a, z.b);
+    }
+  }
+  __builtin_amdgcn_wave_barrier();  // the wave's reads are before what it writes next
+  return x;
+}
+
+// Writes the outline of a page from its bounds.
+template <int DJ>
+__device__ __forceinline__ void write_outline(const ibp_kv_outlines& o, const Bounds4& x, int lane, uint32_t id, float k_scale) {
+  constexpr int D = 64 * DJ;
+  const float top = x.largest();
+  const bool bad = __ballot(top != top) != 0 || !finite(k_scale);
+  const int e = max(whole_exponent(wave_max(top)), -15);
+  const float per = bad ? 0.f : power2(-e);
+  if (lane == 0) o.scales[id] = bad ? NAN : k_scale * power2(e);
+  if (lane >= 16 * DJ) return;
+  uint32_t* to = (uint32_t*)(o.codes + (uint64_t)id * (2 * D)) + lane;
+  to[0] = bad ? 0u : whole4<true>(x.hi, per);
+  to[D / 4] = bad ? 0u : whole4<false>(x.lo, per);
+}
+
+// ------------------------------------------------------------- rotation ----
 
 // Where the other number of a pair is: half a rotation away, which with all dims
 // of an even number of 64s rotated is in the same lane's registers, or next to it.
@@ -51,6 +176,7 @@ template <Pairs PAIRS>
 struct Turn {
   static constexpr bool kTurns = true;
   Angles t;
+  ibp_kv_outlines o;  // codes null: none
 
   __device__ __forceinline__ int position(const Rows& rows, uint32_t seq, int token, int place) const {
     return t.positions ? t.positions[(uint64_t)seq * (uint32_t)rows.n_new + (uint32_t)token] : place;
@@ -100,6 +226,23 @@ struct Turn {
     }
   }
 
+  // The outline of the page whose tile a wave has just made (codes kc, as tile_bounds
+  // takes them); a page's waves meet in LDS.  All waves of the workgroup call this.
+  template <int DJ>
+  __device__ __forceinline__ void outline(const u32x4 (&kc)[DJ], int wave, int lane, int tile, int tiles, int tokens, bool there,
+                                          uint32_t id, float k_scale) const {
+    if (!o.codes) return;
+    __shared__ __attribute__((aligned(16))) uint32_t s_keys[kWaves][4 * DJ * kKeyPitch];
+    Bounds4 x = tile_bounds<DJ>(kc, s_keys[wave], lane, tokens);
+    if (tiles > 1) {
+      *(u32x4*)(s_keys[wave] + 4 * lane) = __builtin_bit_cast(u32x4, x);
+      __syncthreads();
+      if (tile == 0)
+        for (int n = 1; n < tiles; ++n) x.join(__builtin_bit_cast(Bounds4, *(const u32x4*)(s_keys[wave + n] + 4 * lane)));
+    }
+    if (there && tile == 0) write_outline<DJ>(o, x, lane, id, k_scale);
+  }
+
   // The lane's numbers of a key, dims 64 j + 16 g + 0..15, turned.  `key`: its dim
   // 0; kx: what the lane has of it.
   template <int DJ, bool F16>
@@ -146,10 +289,13 @@ struct Turn {
   }
 };
 
+constexpr uint32_t kHeadRun = 4;  // heads of a token that a thread turns by the same angles
+
 struct Queries {
   Strided q, out;
-  Divisor q_heads, group, n_new;
-  uint32_t n_items;  // 16 numbers of a query each
+  Divisor runs, group, n_new;  // runs of kHeadRun heads
+  uint32_t q_heads;
+  uint32_t n_items;  // 16 numbers of a run of queries each
 };
 
 template <bool F16>
@@ -165,42 +311,63 @@ __device__ __forceinline__ void store8(uint16_t* p, bool wide, const Floats8& f,
   }
 }
 
-// 16 numbers of a query: eight pairs, or what is not rotated.
+// 16 numbers of each query of a run: eight pairs, or what is not rotated.
 template <int DJ, bool F16, Pairs PAIRS>
 __device__ __forceinline__ void turn_query(const Queries& a, const Rows& rows, const Turn<PAIRS>& turn, uint32_t x) {
   constexpr uint32_t kItems = 4 * DJ;
   if (x >= a.n_items) return;
   const uint32_t y = x / kItems;
   const int item = (int)(x - y * kItems), half = turn.t.half;
-  const uint32_t t = quotient(y, a.q_heads), head = y - t * a.q_heads.d;
+  const uint32_t t = quotient(y, a.runs), head = (y - t * a.runs.d) * kHeadRun;
   const uint32_t seq = quotient(t, a.n_new), i = t - seq * a.n_new.d;
-  const uint32_t row = seq * rows.heads.d + quotient(head, a.group);
-  const int count = new_count(rows, seq), place = row_length(rows, row) - count + (int)i;
-  const bool there = (int)i < count && place >= 0;
   const bool rotated = PAIRS == Pairs::kNeighbour ? 16 * item < 2 * half : 8 * item < half;
   int d0 = 16 * item, d1 = d0 + 8;
   if (PAIRS != Pairs::kNeighbour) {
     d0 = rotated ? 8 * item : 2 * half + 16 * (item - half / 8);
     d1 = rotated ? d0 + half : d0 + 8;
   }
-  const uint16_t* p = a.q.data + (int64_t)seq * a.q.seq + (int64_t)i * a.q.token + (int64_t)head * a.q.head;
-  uint16_t* to = a.out.data + (int64_t)seq * a.out.seq + (int64_t)i * a.out.token + (int64_t)head * a.out.head;
-  Floats8 f, g;
-  if (there) {
-    f = floats_of<F16>(load8(p + d0, a.q.wide));
-    g = floats_of<F16>(load8(p + d1, a.q.wide));
-    if (rotated) {
-      const int pos = turn.position(rows, seq, (int)i, place);
-      if constexpr (PAIRS == Pairs::kNeighbour) {
-        turn.neighbours(pos, d0, f);
-        turn.neighbours(pos, d1, g);
-      } else {
-        turn.pairs(pos, d0, f, g);
-      }
+  const int count = new_count(rows, seq);
+  u32x4 v[kHeadRun][2];
+  int place[kHeadRun];
+  bool there[kHeadRun];
+#pragma unroll
+  for (uint32_t h = 0; h < kHeadRun; ++h) {
+    const uint32_t at = min(head + h, a.q_heads - 1);
+    place[h] = row_length(rows, seq * rows.heads.d + quotient(at, a.group)) - count + (int)i;
+    there[h] = (int)i < count && place[h] >= 0;
+    v[h][0] = v[h][1] = u32x4{0, 0, 0, 0};
+    if (there[h]) {
+      const uint16_t* p = a.q.data + (int64_t)seq * a.q.seq + (int64_t)i * a.q.token + (int64_t)at * a.q.head;
+      v[h][0] = load8(p + d0, a.q.wide);
+      v[h][1] = load8(p + d1, a.q.wide);
     }
   }
-  store8<F16>(to + d0, a.out.wide, f, there);
-  store8<F16>(to + d1, a.out.wide, g, there);
+  // heads of a sequence are at the same place but where their rows differ
+  float c[8], s[8];
+  int known = 0;
+  bool any = false;
+#pragma unroll
+  for (uint32_t h = 0; h < kHeadRun; ++h) {
+    if (head + h >= a.q_heads) break;
+    Floats8 f = floats_of<F16>(v[h][0]), g = floats_of<F16>(v[h][1]);
+    if (there[h] && rotated) {
+      const int pos = turn.position(rows, seq, (int)i, place[h]);
+      if (!any || pos != known) turn.angles(pos, PAIRS == Pairs::kNeighbour ? d0 / 2 : d0, c, s);
+      known = pos;
+      any = true;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        float& first = PAIRS == Pairs::kNeighbour ? (n < 4 ? f.x[2 * n % 8] : g.x[2 * n % 8]) : f.x[n];
+        float& second = PAIRS == Pairs::kNeighbour ? (n < 4 ? f.x[2 * n % 8 + 1] : g.x[2 * n % 8 + 1]) : g.x[n];
+        const float p = first, q = second;
+        first = turned_first(p, q, c[n], s[n]);
+        second = turned_second(p, q, c[n], s[n]);
+      }
+    }
+    uint16_t* to = a.out.data + (int64_t)seq * a.out.seq + (int64_t)i * a.out.token + (int64_t)(head + h) * a.out.head;
+    store8<F16>(to + d0, a.out.wide, f, there[h]);
+    store8<F16>(to + d1, a.out.wide, g, there[h]);
+  }
 }
 
 // The first workgroups append, the others rotate the queries.
@@ -217,114 +384,59 @@ __global__ __launch_bounds__(kThreads) void append_rotated_kernel(Pool pool, Row
 
 // -------------------------------------------------------------- outline ----
 
-__device__ __forceinline__ f16x2 pair_max(f16x2 a, f16x2 b) { return __builtin_elementwise_max(a, b); }
-__device__ __forceinline__ f16x2 pair_min(f16x2 a, f16x2 b) { return __builtin_elementwise_min(a, b); }
-
-template <int CTRL>
-__device__ __forceinline__ f16x2 swapped(f16x2 x) {
-  return __builtin_bit_cast(f16x2, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
-}
-
-// Smallest e with a <= 127 * 2^e (127 = 1.984375 * 2^6), for a > 0.
-__device__ __forceinline__ int whole_exponent(float a) {
-  const uint32_t b = __builtin_bit_cast(uint32_t, a);
-  return (int)(b >> 23) - 127 - 6 + ((b & 0x7FFFFFu) > 0x7E0000u ? 1 : 0);
-}
-
-// 16 dims of a page's keys to four lanes, which have a quarter of its tokens each:
-// neighbouring lanes read 64 bytes of neighbouring tokens.  e4m3 codes are exact in
-// 16 bits, two to an instruction.  What a page has no token for is read as its last
-// token, which changes neither the largest nor the smallest.
+// A wave takes up to 64 pages of a row (wave_pages) one after the other, a tile at a
+// time: it has their ids and scales at once, and the next tiles are on their way while
+// one is looked at.  e4m3 codes are exact in 16 bits, two to an instruction.
 template <int DJ>
-__global__ __launch_bounds__(kThreads) void outline_kernel(Pool pool, Rows rows, ibp_kv_outlines o,
-                                                           Divisor pages_per_row, uint32_t n_tasks) {
-  constexpr int D = 64 * DJ;
-  constexpr int kLanes = 16 * DJ, kPages = kWave / kLanes;  // of a wave
+__global__ __launch_bounds__(kThreads) void outline_kernel(Pool pool, Rows rows, ibp_kv_outlines o, Divisor chunks,
+                                                           uint32_t n_chunks, int wave_pages) {
+  constexpr int kAhead = DJ <= 2 ? 4 : 2;  // tiles on their way
+  __shared__ __attribute__((aligned(16))) uint32_t s_keys[kWaves][4 * DJ * kKeyPitch];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const int sub = lane / kLanes, r = lane % kLanes, tq = r % 4;
-  const uint32_t task = (blockIdx.x * kWaves + wave) * kPages + sub;
-  const uint32_t line = quotient(min(task, n_tasks - 1), rows.heads);
-  const uint32_t head = min(task, n_tasks - 1) - line * rows.heads.d;
-  const uint32_t seq = quotient(line, pages_per_row), row = seq * rows.heads.d + head;
+  const uint32_t task = blockIdx.x * kWaves + wave;
+  if (task >= n_chunks) return;
+  const uint32_t row = quotient(task, chunks), seq = quotient(row, rows.heads);
   const int end = row_length(rows, row), count = new_count(rows, seq);
-  const int page_shift = 4 + (int)pool.tile_shift;
-  const int page = (max(end - count, 0) >> page_shift) + (int)(line - seq * pages_per_row.d);
-  const int n = min(end - (page << page_shift), 16 << pool.tile_shift);  // tokens
-  const bool reached = sub < kPages && task < n_tasks && count > 0 && page < (int)rows.max_pages && n > 0;
-  uint32_t id = ~0u;
-  if (reached) id = (uint32_t)rows.pages[(uint64_t)row * rows.max_pages + page];
-  const bool live = id < pool.n_pages;
-  f16x2 hi[8], lo[8];
-  uint32_t odd = 0;
+  const int page_shift = 4 + (int)pool.tile_shift, tiles = 1 << pool.tile_shift;
+  const int held = (end + (1 << page_shift) - 1) >> page_shift;
+  const int from = (max(end - count, 0) >> page_shift) + (int)(task - row * chunks.d) * wave_pages;
+  const int pages = count > 0 ? min(held - from, wave_pages) : 0;
+  if (pages <= 0) return;
+  uint32_t ids = ~0u;
+  if (lane < pages) ids = (uint32_t)rows.pages[(uint64_t)row * rows.max_pages + (uint32_t)(from + lane)];
+  float scales = 0.f;
+  if (ids < pool.n_pages) scales = pool.k_scales[ids];
+  // tile 0 of the first of the pages, and so on; the last one again past the last
+  const int units = uniform(min(pages << pool.tile_shift, ((end + kTile - 1) / kTile) - (from << pool.tile_shift)));
+  auto id_of = [&](int unit) { return (uint32_t)__builtin_amdgcn_readlane((int)ids, unit >> pool.tile_shift); };
+  u32x4 w[kAhead][DJ];
+  auto load = [&](int unit, u32x4 (&to)[DJ]) {
+    unit = min(unit, units - 1);
+    const uint32_t id = id_of(unit), at = id < pool.n_pages ? id : 0u;
+    const uint8_t* p = pool.k_codes + (uint64_t)at * pool.page_bytes + (uint32_t)((unit & (tiles - 1)) * (DJ * kUnit));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) hi[i] = lo[i] = f16x2{0, 0};
-  float scale = 0.f;
-  if (live) {
-    scale = pool.k_scales[id];
-    const uint8_t* p = pool.k_codes + (uint64_t)id * pool.page_bytes + (r / 4) * 256;
-    for (int tile = 0; tile * kTile < n; ++tile) {
-      u32x4 w[4];
+    for (int j = 0; j < DJ; ++j) to[j] = __builtin_nontemporal_load((const u32x4*)(p + j * kUnit + lane * 16));
+  };
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = __builtin_nontemporal_load((const u32x4*)(p + tile * (kTile * D) + 16 * min(4 * i + tq, n - 1 - tile * kTile)));
+  for (int i = 0; i < kAhead; ++i) load(i, w[i]);
+  Bounds4 x;
+  x.clear();
+  for (int first = 0; first < units; first += kAhead) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          odd |= (w[i][x] & 0x7F7F7F7Fu) + 0x01010101u;
-          const f16x2 a = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i][x], 1.f, false));
-          const f16x2 b = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i][x], 1.f, true));
-          const bool first = i == 0 && tile == 0;
-          hi[2 * x] = first ? a : pair_max(hi[2 * x], a);
-          hi[2 * x + 1] = first ? b : pair_max(hi[2 * x + 1], b);
-          lo[2 * x] = first ? a : pair_min(lo[2 * x], a);
-          lo[2 * x + 1] = first ? b : pair_min(lo[2 * x + 1], b);
+    for (int i = 0; i < kAhead; ++i) {
+      const int unit = first + i;
+      if (unit < units) {
+        x.join(tile_bounds<DJ>(w[i], s_keys[wave], lane, end - (from << page_shift) - unit * kTile));
+        if ((unit & (tiles - 1)) == tiles - 1 || unit == units - 1) {
+          const uint32_t id = id_of(unit);
+          if (id < pool.n_pages)
+            write_outline<DJ>(o, x, lane, id, __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, scales), unit >> pool.tile_shift)));
+          x.clear();
         }
+      }
+      load(unit + kAhead, w[i]);
     }
   }
-  f16x2 top = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    hi[i] = pair_max(hi[i], swapped<0xB1>(hi[i]));
-    lo[i] = pair_min(lo[i], swapped<0xB1>(lo[i]));
-    hi[i] = pair_max(hi[i], swapped<0x4E>(hi[i]));
-    lo[i] = pair_min(lo[i], swapped<0x4E>(lo[i]));
-    top = pair_max(top, pair_max(hi[i], -lo[i]));  // of a magnitude: hi >= lo
-  }
-  float amax = fmaxf((float)top[0], (float)top[1]);
-  amax = fmaxf(amax, row_rotate<0x124>(amax));
-  amax = fmaxf(amax, row_rotate<0x128>(amax));
-  if constexpr (DJ > 1) {
-    const f32x2 y = both16(amax);
-    amax = fmaxf(y[0], y[1]);
-  }
-  if constexpr (DJ > 2) {
-    const f32x2 y = both32(amax);
-    amax = fmaxf(y[0], y[1]);
-  }
-  const uint64_t odds = __ballot((odd & 0x80808080u) != 0 || !finite(scale));
-  if (!live) return;
-  const uint64_t mine = kLanes == 64 ? ~0ull : ((1ull << kLanes) - 1ull) << (sub * kLanes);
-  const bool bad = (odds & mine) != 0;
-  const int e = max(whole_exponent(amax), -15);
-  const float per = bad ? 0.f : power2(-e);
-  if (r == 0) o.scales[id] = bad ? NAN : scale * power2(e);
-  if (tq > 1) return;
-  // lanes 0 of four write the largest, rounded up, which is the negative rounded down of
-  // the negative, lanes 1 the smallest
-  u32x4 c;
-#pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    uint32_t word = 0;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const f16x2 h = tq ? lo[2 * x + b / 2] : -hi[2 * x + b / 2];
-      const int whole = (int)__builtin_floorf((float)h[b % 2] * per);
-      word |= (uint32_t)((tq ? whole : -whole) & 255) << (8 * b);
-    }
-    c[x] = bad ? 0u : word;
-  }
-  *(u32x4*)(o.codes + (uint64_t)id * (2 * D) + tq * D + (r / 4) * 16) = c;
 }
 
 // ------------------------------------------------------------ selection ----
@@ -995,36 +1107,46 @@ uint64_t touched_pages(uint64_t n_new, uint64_t page_tokens, uint64_t max_pages)
 
 template <int DJ, bool F16, Pairs PAIRS>
 void launch_append_rotated(const Pool& pool, const Rows& rows, const Strided& k, const Strided& v, uint32_t per_row,
-                           uint32_t tasks, const Angles& t, const Queries& q, hipStream_t st) {
+                           uint32_t tasks, const Angles& t, const ibp_kv_outlines& o, const Queries& q, hipStream_t st) {
   const uint32_t per_group = kWaves >> pool.tile_shift;
   const uint32_t append = (tasks + per_group - 1) / per_group;
   const uint32_t turn = (q.n_items + kThreads - 1) / kThreads;
   hipLaunchKernelGGL((append_rotated_kernel<DJ, F16, PAIRS>), dim3(append + turn), dim3(kThreads), 0, st, pool, rows, k, v,
-                     make_divisor(per_row), tasks, Turn<PAIRS>{t}, q, append);
+                     make_divisor(per_row), tasks, Turn<PAIRS>{t, o}, q, append);
 }
 
 template <int DJ, bool F16>
 void launch_append_pairs(const Pool& pool, const Rows& rows, const Strided& k, const Strided& v, uint32_t per_row,
-                         uint32_t tasks, const Angles& t, bool interleaved, const Queries& q, hipStream_t st) {
-  if (interleaved) return launch_append_rotated<DJ, F16, Pairs::kNeighbour>(pool, rows, k, v, per_row, tasks, t, q, st);
+                         uint32_t tasks, const Angles& t, bool interleaved, const ibp_kv_outlines& o, const Queries& q,
+                         hipStream_t st) {
+  if (interleaved) return launch_append_rotated<DJ, F16, Pairs::kNeighbour>(pool, rows, k, v, per_row, tasks, t, o, q, st);
   if constexpr (DJ % 2 == 0)
-    if (t.half == 32 * DJ) return launch_append_rotated<DJ, F16, Pairs::kLane>(pool, rows, k, v, per_row, tasks, t, q, st);
-  launch_append_rotated<DJ, F16, Pairs::kFar>(pool, rows, k, v, per_row, tasks, t, q, st);
+    if (t.half == 32 * DJ) return launch_append_rotated<DJ, F16, Pairs::kLane>(pool, rows, k, v, per_row, tasks, t, o, q, st);
+  launch_append_rotated<DJ, F16, Pairs::kFar>(pool, rows, k, v, per_row, tasks, t, o, q, st);
 }
 
+// Waves to a compute unit that the pages of an outline call are spread over: two
+// contexts of 131k and 91k tokens x 8 heads (257 MB) take 58.6 us so, 60.1 with 24,
+// 63 with 32 and 64.5 with 64, since each begins with a chain of three loads.
+constexpr int kOutlineWaves = 16;
+
 int launch_outline(const ibp_kv_cache* cache, const ibp_kv_outlines* o, const Rows& rows, uint64_t n_rows,
-                   uint64_t n_new, hipStream_t st) {
+                   uint64_t n_new, int cus, hipStream_t st) {
   const Pool pool = make_pool(cache);
   const int dj = (int)cache->head_dim / 64;
   const uint64_t per_row = touched_pages(n_new, cache->page_tokens, rows.max_pages);
-  const uint64_t tasks = n_rows * per_row, per_group = (uint64_t)kWaves * (kWave / (16 * dj));
-  const dim3 grid((uint32_t)((tasks + per_group - 1) / per_group));
-  const Divisor d = make_divisor((uint32_t)per_row);
+  const uint64_t waves = (uint64_t)kOutlineWaves * cus;
+  const uint64_t wave_pages = std::min<uint64_t>(std::max<uint64_t>((n_rows * per_row + waves - 1) / waves, 1), kWave);
+  const uint64_t chunks = (per_row + wave_pages - 1) / wave_pages, tasks = n_rows * chunks;
+  const dim3 grid((uint32_t)((tasks + kWaves - 1) / kWaves)), threads(kThreads);
+  const Divisor d = make_divisor((uint32_t)chunks);
+  const uint32_t n = (uint32_t)tasks;
+  const int wp = (int)wave_pages;
   switch (dj) {
-    case 1: hipLaunchKernelGGL(outline_kernel<1>, grid, dim3(kThreads), 0, st, pool, rows, *o, d, (uint32_t)tasks); break;
-    case 2: hipLaunchKernelGGL(outline_kernel<2>, grid, dim3(kThreads), 0, st, pool, rows, *o, d, (uint32_t)tasks); break;
-    case 3: hipLaunchKernelGGL(outline_kernel<3>, grid, dim3(kThreads), 0, st, pool, rows, *o, d, (uint32_t)tasks); break;
-    default: hipLaunchKernelGGL(outline_kernel<4>, grid, dim3(kThreads), 0, st, pool, rows, *o, d, (uint32_t)tasks); break;
+    case 1: hipLaunchKernelGGL(outline_kernel<1>, grid, threads, 0, st, pool, rows, *o, d, n, wp); break;
+    case 2: hipLaunchKernelGGL(outline_kernel<2>, grid, threads, 0, st, pool, rows, *o, d, n, wp); break;
+    case 3: hipLaunchKernelGGL(outline_kernel<3>, grid, threads, 0, st, pool, rows, *o, d, n, wp); break;
+    default: hipLaunchKernelGGL(outline_kernel<4>, grid, threads, 0, st, pool, rows, *o, d, n, wp); break;
   }
   return launched();
 }
@@ -1161,10 +1283,12 @@ int ibp_kv_append_rotated(const ibp_kv_cache* cache, const ibp_kv_table* table, 
     // items, and with the pages' workgroups the grid
     const uint64_t most = 0x7FFFFFFFull / (cache->head_dim / 16) / table->n_seqs;
     if (n_new > most || q_heads > most / n_new) return IBP_ERR_INVALID_ARGUMENT;
-    queries.n_items = (uint32_t)(table->n_seqs * n_new * q_heads * (cache->head_dim / 16));
+    const uint64_t runs = (q_heads + kHeadRun - 1) / kHeadRun;
+    queries.n_items = (uint32_t)(table->n_seqs * n_new * runs * (cache->head_dim / 16));
+    queries.runs = make_divisor((uint32_t)runs);
+    queries.q_heads = (uint32_t)q_heads;
     queries.q = make_strided(q);
     queries.out = make_strided(q_out);
-    queries.q_heads = make_divisor((uint32_t)q_heads);
     queries.group = make_divisor((uint32_t)(q_heads / table->kv_heads));
     queries.n_new = make_divisor((uint32_t)n_new);
   }
@@ -1186,19 +1310,18 @@ int ibp_kv_append_rotated(const ibp_kv_cache* cache, const ibp_kv_table* table, 
   hipStream_t st = (hipStream_t)stream;
   const uint32_t pr = (uint32_t)std::max<uint64_t>(per_row, 1), n = (uint32_t)tasks;
   const bool il = rotation->interleaved != 0;
+  const ibp_kv_outlines o = outlines ? *outlines : ibp_kv_outlines{nullptr, nullptr};
   switch (cache->head_dim / 64 * 2 + dtype) {
-    case 2: launch_append_pairs<1, false>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
-    case 3: launch_append_pairs<1, true>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
-    case 4: launch_append_pairs<2, false>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
-    case 5: launch_append_pairs<2, true>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
-    case 6: launch_append_pairs<3, false>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
-    case 7: launch_append_pairs<3, true>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
-    case 8: launch_append_pairs<4, false>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
-    default: launch_append_pairs<4, true>(pool, rows, ks, vs, pr, n, t, il, queries, st); break;
+    case 2: launch_append_pairs<1, false>(pool, rows, ks, vs, pr, n, t, il, o, queries, st); break;
+    case 3: launch_append_pairs<1, true>(pool, rows, ks, vs, pr, n, t, il, o, queries, st); break;
+    case 4: launch_append_pairs<2, false>(pool, rows, ks, vs, pr, n, t, il, o, queries, st); break;
+    case 5: launch_append_pairs<2, true>(pool, rows, ks, vs, pr, n, t, il, o, queries, st); break;
+    case 6: launch_append_pairs<3, false>(pool, rows, ks, vs, pr, n, t, il, o, queries, st); break;
+    case 7: launch_append_pairs<3, true>(pool, rows, ks, vs, pr, n, t, il, o, queries, st); break;
+    case 8: launch_append_pairs<4, false>(pool, rows, ks, vs, pr, n, t, il, o, queries, st); break;
+    default: launch_append_pairs<4, true>(pool, rows, ks, vs, pr, n, t, il, o, queries, st); break;
   }
-  rc = launched();
-  if (rc || !outlines || !tasks) return rc;
-  return launch_outline(cache, outlines, rows, n_rows, n_new, st);
+  return launched();
 }
 
 int ibp_kv_outline(const ibp_kv_cache* cache, const ibp_kv_outlines* outlines, const ibp_kv_table* table,
@@ -1214,7 +1337,8 @@ int ibp_kv_outline(const ibp_kv_cache* cache, const ibp_kv_outlines* outlines, c
   if (too_many(n_rows, touched_pages(n_new, cache->page_tokens, table->max_pages), kWaves)) return IBP_ERR_INVALID_ARGUMENT;
   rc = pending_hip_error();
   if (rc) return rc;
-  return launch_outline(cache, outlines, make_rows(table, cache->page_tokens, n_new, counts), n_rows, n_new, (hipStream_t)stream);
+  return launch_outline(cache, outlines, make_rows(table, cache->page_tokens, n_new, counts), n_rows, n_new, compute_units(),
+                        (hipStream_t)stream);
 }
 
 uint64_t ibp_kv_select_workspace_bytes(const ibp_kv_cache* cache, const ibp_kv_table* table) {
