@@ -1355,7 +1355,8 @@ struct Cut {
   uint32_t last, ties;
 };
 
-// The `want` heaviest of the keys in [low, high] (of the thread's own).
+// The `want` heaviest of the keys in [low, high] (of the thread's own); the first `used`
+// of a thread's keys are looked at.
 // The weight of the last page to stay is found from counts in LDS: the keys
 // between the smallest and the largest are counted in 1024 equal ranges, the
 // range that holds the wanted one is cut into 1024 again, and so on.  (Bisecting
@@ -1363,7 +1364,7 @@ struct Cut {
 // 768 rows spent 47 us on it.)
 template <int THREADS, int R>
 __device__ __forceinline__ Cut cut_of(ChoiceLds<THREADS, R>& s, uint32_t low, uint32_t high, uint32_t want, int wave,
-                                      int lane) {
+                                      int lane, int used = R) {
   constexpr int kW = THREADS / kWave;
   constexpr int kMine = kRanges / kWave;  // of a lane that adds them up
   Cut cut = {kStays - 1u, 0};
@@ -1393,6 +1394,7 @@ __device__ __forceinline__ Cut cut_of(ChoiceLds<THREADS, R>& s, uint32_t low, ui
       if (round < 2) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
+          if (i >= used) break;
           const uint32_t above_low = s.key[i][threadIdx.x] - low;
           if (above_low <= high - low) {
             atomicAdd(&count[above_low >> shift], 1u);

@@ -480,152 +480,233 @@ __device__ __forceinline__ Selection selection_of(const Select& s, uint32_t row)
 
 // Groups of 16 pages that a wave has in registers.
 constexpr int score_groups(int dj) { return dj <= 2 ? 4 : 2; }
-constexpr int score_pages(int dj) { return 16 * score_groups(dj) * kWaves; }  // of a workgroup
+constexpr int score_pages(int dj, int threads) { return 16 * score_groups(dj) * (threads / kWave); }  // of a workgroup at a time
 
-// Scores of a run of a row's pages.  S of 16 queries and 16 pages is a product of
-// 8-bit matrices: a query's whole numbers in two limbs of at most 127, those of
-// positive numbers against the largest and those of negative ones against the
-// smallest of each dim.  With the sums of the upper limbs shifted by 7 the lower
-// ones add on top; all is exact in 32 bits (16256 * 127 * 256 < 2^30).
+// Scores of a row's pages.  S of 16 queries and 16 pages is a product of 8-bit
+// matrices: a query's whole numbers in two limbs of at most 127, those of positive
+// numbers against the largest and those of negative ones against the smallest of each
+// dim.  With the sums of the upper limbs shifted by 7 the lower ones add on top; all is
+// exact in 32 bits (16256 * 127 * 256 < 2^30).
+template <int DJ>
+struct ScoreLds {
+  __attribute__((aligned(16))) uint32_t limbs[DJ][2][2][kWave][4];  // as the lanes of the matrix instructions take them
+  float unit[16];                                                   // 0: no query
+};
+
+// Whose pages and queries.
+struct ScoreRow {
+  __amdgpu_buffer_rsrc_t pages;  // ends with the row
+  uint32_t seq, head;
+  int count, origin;
+};
+
+__device__ __forceinline__ ScoreRow score_row(const Select& s, const Selection& c, uint32_t row) {
+  ScoreRow r;
+  r.pages = row_buffer(s.rows.pages + (uint64_t)row * s.rows.max_pages, s.rows.max_pages * 4u);
+  r.seq = quotient(row, s.rows.heads);
+  r.head = row - r.seq * s.rows.heads.d;
+  r.count = new_count(s.rows, r.seq);
+  r.origin = c.len - r.count;
+  return r;
+}
+
+// 16 queries to four waves: wave w has 4 w .. 4 w + 3, 16 lanes each; lane x has dims
+// 64 j + 4 x + 0..3.
+template <int DJ>
+struct Queries16 {
+  uint16_t q[DJ][4];
+  int token;  // -1: no such row
+};
+
+template <int DJ>
+__device__ __forceinline__ Queries16<DJ> load_queries(const Select& s, const ScoreRow& r, int m0, int wave, int lane) {
+  Queries16<DJ> y;
+  const int n = wave * 4 + lane / 16, x = lane % 16, m = m0 + n;
+  const int t = (int)quotient((uint32_t)m, s.group);
+  y.token = n < 16 && m < s.m_rows ? t : -1;
+#pragma unroll
+  for (int j = 0; j < DJ; ++j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y.q[j][i] = 0;
+    if (y.token >= 0) {
+      const uint16_t* src = s.q.data + (int64_t)r.seq * s.q.seq + (int64_t)t * s.q.token +
+                            ((int64_t)r.head * s.group.d + (m - t * (int)s.group.d)) * s.q.head + 64 * j + 4 * x;
+      if (s.q.wide) {
+        const u16x4 h = *(const u16x4*)src;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y.q[j][i] = h[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y.q[j][i] = src[i];
+      }
+    }
+  }
+  return y;
+}
+
 template <int DJ, bool F16>
-__global__ __launch_bounds__(kThreads) void score_kernel(Select s) {
-  constexpr int D = 64 * DJ;
-  constexpr int P = score_groups(DJ);
-  __shared__ __attribute__((aligned(16))) uint32_t s_limbs[DJ][2][2][kWave][4];
-  __shared__ float s_unit[16];  // 0: no query
-  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const uint32_t row = quotient(blockIdx.x, s.chunks);
-  const Selection c = selection_of(s, row);
-  const uint32_t from = (blockIdx.x - row * s.chunks.d) * score_pages(DJ);
-  if (!c.full || !c.want || from >= c.hi || from + score_pages(DJ) <= c.lo) return;
-  const uint32_t seq = quotient(row, s.rows.heads), head = row - seq * s.rows.heads.d;
-  const int count = new_count(s.rows, seq), origin = c.len - count;
+__device__ __forceinline__ void write_limbs(const Queries16<DJ>& y, const ScoreRow& r, ScoreLds<DJ>& lds, int wave, int lane) {
+  const int n = wave * 4 + lane / 16, x = lane % 16;
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < DJ; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, y.q[j][i] & 0x7FFFu);
+  float amax = not_finite<F16>(top) ? INFINITY : to_float<F16>((uint16_t)top);
+  amax = fmaxf(amax, row_rotate<0x121>(amax));
+  amax = fmaxf(amax, row_rotate<0x122>(amax));
+  amax = fmaxf(amax, row_rotate<0x124>(amax));
+  amax = fmaxf(amax, row_rotate<0x128>(amax));
+  // 127 * 128 * 2^e is 127 * 2^(e + 7)
+  const bool counts = y.token >= 0 && y.token < r.count && r.origin + y.token >= 0 && finite(amax);
+  const int e = counts ? max(whole_exponent(amax) - 7, -126) : 0;
+  const float per = power2(-e);
+  if (x == 0) lds.unit[n] = counts ? power2(e) : 0.f;
+#pragma unroll
+  for (int j = 0; j < DJ; ++j) {
+    uint32_t words[2][2] = {{0, 0}, {0, 0}};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int whole = counts ? (int)__builtin_rintf(to_float<F16>(y.q[j][i]) * per) : 0;
+      const int upper = (whole + 64) >> 7, lower = whole - 128 * upper;
+      const int side = whole < 0 ? 1 : 0;
+      const uint32_t u = (uint32_t)(upper & 255) << (8 * i), l = (uint32_t)(lower & 255) << (8 * i);
+      words[0][0] |= side ? 0u : u;
+      words[0][1] |= side ? 0u : l;
+      words[1][0] |= side ? u : 0u;
+      words[1][1] |= side ? l : 0u;
+    }
+#pragma unroll
+    for (int end = 0; end < 2; ++end)
+#pragma unroll
+      for (int limb = 0; limb < 2; ++limb) lds.limbs[j][end][limb][x / 4 * 16 + n][x % 4] = words[end][limb];
+  }
+}
 
-  // the wave's outlines are on their way while the queries are read
-  const int32_t* pages = s.rows.pages + (uint64_t)row * s.rows.max_pages;
-  const uint32_t first = from + wave * (16 * P);
+// The outlines of pages first + 16 p + lane % 16.  Ids are asked for before the row's
+// length is known.
+template <int DJ>
+struct PageSet {
+  static constexpr int P = score_groups(DJ);
   u32x4 b[P][DJ][2];
   float scale[P];
   bool live[P];
+};
+
+template <int DJ>
+struct PageIds {
+  uint32_t id[score_groups(DJ)];
+};
+
+template <int DJ>
+__device__ __forceinline__ PageIds<DJ> load_ids(const ScoreRow& r, uint32_t first, int lane) {
+  PageIds<DJ> x;
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
+  for (int p = 0; p < score_groups(DJ); ++p)
+    x.id[p] = __builtin_amdgcn_raw_buffer_load_b32(r.pages, (int)(first + 16 * p + lane % 16) * 4, 0, 0);
+  return x;
+}
+
+template <int DJ>
+__device__ __forceinline__ PageSet<DJ> load_outlines(const Select& s, const Selection& c, const PageIds<DJ>& ids, uint32_t first,
+                                                     int lane) {
+  constexpr int D = 64 * DJ;
+  PageSet<DJ> x;
+#pragma unroll
+  for (int p = 0; p < x.P; ++p) {
     const uint32_t page = first + 16 * p + lane % 16;
-    const uint32_t id = page < c.hi ? (uint32_t)pages[page] : ~0u;
-    live[p] = id < s.n_pages;
-    const uint32_t at = live[p] ? id : 0u;
-    scale[p] = 0.f;
+    x.live[p] = page >= c.lo && page < c.hi && ids.id[p] < s.n_pages;
+    const uint32_t at = x.live[p] ? ids.id[p] : 0u;
+    x.scale[p] = 0.f;
     if (s.n_pages == 0) continue;
-    scale[p] = s.outline_scales[at];
+    x.scale[p] = s.outline_scales[at];
     const int8_t* codes = s.codes + (uint64_t)at * (2 * D) + (lane / 16) * 16;
 #pragma unroll
     for (int j = 0; j < DJ; ++j)
 #pragma unroll
-      for (int end = 0; end < 2; ++end) b[p][j][end] = *(const u32x4*)(codes + end * D + 64 * j);
+      for (int end = 0; end < 2; ++end) x.b[p][j][end] = *(const u32x4*)(codes + end * D + 64 * j);
   }
+  return x;
+}
+
+// The largest so far over the queries in LDS: the lane has queries 4 (lane / 16) + r of
+// page lane % 16 of each group.
+template <int DJ>
+__device__ __forceinline__ void take_queries(const PageSet<DJ>& x, const ScoreLds<DJ>& lds, int lane, float (&best)[PageSet<DJ>::P]) {
+  constexpr int P = PageSet<DJ>::P;
+  i32x4 sum[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) sum[p] = i32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int limb = 0; limb < 2; ++limb) {
+#pragma unroll
+    for (int j = 0; j < DJ; ++j)
+#pragma unroll
+      for (int end = 0; end < 2; ++end) {
+        const i32x4 a = *(const i32x4*)lds.limbs[j][end][limb][lane];
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          sum[p] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, __builtin_bit_cast(i32x4, x.b[p][j][end]), sum[p], 0, 0, 0);
+      }
+    if (limb == 0) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) sum[p] <<= 7;
+    }
+  }
+  float unit[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) unit[r] = lds.unit[4 * (lane / 16) + r];
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) best[p] = unit[r] > 0.f ? fmaxf(best[p], (float)sum[p][r] * unit[r]) : best[p];
+}
+
+// The score of page first + lane, for lanes below 16 P.
+template <int DJ>
+__device__ __forceinline__ float score_of_lane(const PageSet<DJ>& x, float (&best)[PageSet<DJ>::P], int lane) {
+  float mine = 0.f;
+#pragma unroll
+  for (int p = 0; p < x.P; ++p) {
+    f32x2 y = both16(best[p]);
+    y = both32(fmaxf(y[0], y[1]));
+    const float score = x.live[p] ? fmaxf(y[0], y[1]) * x.scale[p] : -INFINITY;
+    if (p == 0 || lane / 16 == p) mine = score;
+  }
+  return mine;
+}
+
+// Scores of a run of a row's pages, into the workspace.
+template <int DJ, bool F16>
+__global__ __launch_bounds__(kThreads) void score_kernel(Select s) {
+  constexpr int P = PageSet<DJ>::P;
+  __shared__ ScoreLds<DJ> lds;
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const uint32_t row = quotient(blockIdx.x, s.chunks);
+  const uint32_t from = (blockIdx.x - row * s.chunks.d) * score_pages(DJ, kThreads), first = from + wave * (16 * P);
+  // Queries and ids before the row's length is known; the queries first, since loads
+  // return in order and the outlines are on their way while the limbs are made.
+  const Selection c = selection_of(s, row);
+  const ScoreRow r = score_row(s, c, row);
+  Queries16<DJ> q = load_queries<DJ>(s, r, 0, wave, lane);
+  const PageIds<DJ> ids = load_ids<DJ>(r, first, lane);
+  if (!c.full || !c.want || from >= c.hi || from + score_pages(DJ, kThreads) <= c.lo) return;
+  const PageSet<DJ> x = load_outlines<DJ>(s, c, ids, first, lane);
   float best[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) best[p] = -INFINITY;
-
   for (int m0 = 0; m0 < s.m_rows; m0 += 16) {
-    // wave w: queries 4 w .. 4 w + 3, 16 lanes each; lane x: dims 64 j + 4 x + 0..3
-    const int n = wave * 4 + lane / 16, x = lane % 16, m = m0 + n;
-    const int t = (int)quotient((uint32_t)m, s.group);
-    const bool there = m < s.m_rows && t < count && origin + t >= 0;
-    uint16_t q[DJ][4];
-    uint32_t top = 0;
-    if (m0) __syncthreads();
-#pragma unroll
-    for (int j = 0; j < DJ; ++j) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[j][i] = 0;
-      if (there) {
-        const uint16_t* src = s.q.data + (int64_t)seq * s.q.seq + (int64_t)t * s.q.token +
-                              ((int64_t)head * s.group.d + (m - t * (int)s.group.d)) * s.q.head + 64 * j + 4 * x;
-        if (s.q.wide) {
-          const u16x4 h = *(const u16x4*)src;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) q[j][i] = h[i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) q[j][i] = src[i];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = max(top, q[j][i] & 0x7FFFu);
+    if (m0) {
+      q = load_queries<DJ>(s, r, m0, wave, lane);
+      __syncthreads();
     }
-    float amax = to_float<F16>((uint16_t)top);
-    const bool plain = !not_finite<F16>(top);
-    amax = plain ? amax : INFINITY;
-    amax = fmaxf(amax, row_rotate<0x121>(amax));
-    amax = fmaxf(amax, row_rotate<0x122>(amax));
-    amax = fmaxf(amax, row_rotate<0x124>(amax));
-    amax = fmaxf(amax, row_rotate<0x128>(amax));
-    // 127 * 128 * 2^e is 127 * 2^(e + 7)
-    const bool counts = there && finite(amax);
-    const int e = counts ? max(whole_exponent(amax) - 7, -126) : 0;
-    const float per = power2(-e);
-    if (x == 0) s_unit[n] = counts ? power2(e) : 0.f;
-#pragma unroll
-    for (int j = 0; j < DJ; ++j) {
-      uint32_t words[2][2] = {{0, 0}, {0, 0}};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int whole = counts ? (int)__builtin_rintf(to_float<F16>(q[j][i]) * per) : 0;
-        const int upper = (whole + 64) >> 7, lower = whole - 128 * upper;
-        const int side = whole < 0 ? 1 : 0;
-        const uint32_t u = (uint32_t)(upper & 255) << (8 * i), l = (uint32_t)(lower & 255) << (8 * i);
-        words[0][0] |= side ? 0u : u;
-        words[0][1] |= side ? 0u : l;
-        words[1][0] |= side ? u : 0u;
-        words[1][1] |= side ? l : 0u;
-      }
-#pragma unroll
-      for (int end = 0; end < 2; ++end)
-#pragma unroll
-        for (int limb = 0; limb < 2; ++limb) s_limbs[j][end][limb][x / 4 * 16 + n][x % 4] = words[end][limb];
-    }
+    write_limbs<DJ, F16>(q, r, lds, wave, lane);
     __syncthreads();
-    float unit[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) unit[r] = s_unit[4 * (lane / 16) + r];
-    i32x4 sum[P];
-#pragma unroll
-    for (int p = 0; p < P; ++p) sum[p] = i32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int limb = 0; limb < 2; ++limb) {
-#pragma unroll
-      for (int j = 0; j < DJ; ++j)
-#pragma unroll
-        for (int end = 0; end < 2; ++end) {
-          const i32x4 a = *(const i32x4*)s_limbs[j][end][limb][lane];
-#pragma unroll
-          for (int p = 0; p < P; ++p)
-            sum[p] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, __builtin_bit_cast(i32x4, b[p][j][end]), sum[p], 0, 0, 0);
-        }
-      if (limb == 0) {
-#pragma unroll
-        for (int p = 0; p < P; ++p) sum[p] <<= 7;
-      }
-    }
-    // the lane has queries 4 (lane / 16) + r of page lane % 16
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) best[p] = unit[r] > 0.f ? fmaxf(best[p], (float)sum[p][r] * unit[r]) : best[p];
+    take_queries<DJ>(x, lds, lane, best);
   }
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    f32x2 y = both16(best[p]);
-    y = both32(fmaxf(y[0], y[1]));
-    best[p] = live[p] ? fmaxf(y[0], y[1]) * scale[p] : -INFINITY;
-  }
-  // lanes 16 p .. 16 p + 15 write group p
-  float mine = best[0];
-#pragma unroll
-  for (int p = 1; p < P; ++p)
-    if (lane / 16 == p) mine = best[p];
+  const float mine = score_of_lane<DJ>(x, best, lane);
   const uint32_t page = first + lane;
-  if (lane < 16 * P && page < c.hi) s.scores[(uint64_t)row * s.rows.max_pages + page] = mine;
+  if (lane < 16 * P && page >= c.lo && page < c.hi) s.scores[(uint64_t)row * s.rows.max_pages + page] = mine;
 }
 
 // Writes what stays, in order, and -1 past it.
@@ -636,40 +717,123 @@ __device__ __forceinline__ void fill_rest(const Select& s, uint32_t row, uint32_
   }
 }
 
-// One workgroup per row of up to THREADS * R pages.
+// The key of page p of a row, for cut_of; `score`: if it is one to be chosen from.
+__device__ __forceinline__ uint32_t page_key(const Selection& c, uint32_t p, float score) {
+  if (c.want && p - c.lo < c.hi - c.lo) return weight_key(score);
+  return p < c.held && (!c.full || p < c.lo || p >= c.hi) ? kStays : 0u;
+}
+
+// Chooses and writes: id[i] is that of the thread's page i.  Through buffers that end
+// with the row: what does not stay is written past it, which is to say not at all.
+template <int THREADS, int R>
+__device__ __forceinline__ void write_selection(const Select& s, const Selection& c, ChoiceLds<THREADS, R>& lds, uint32_t row,
+                                                uint32_t low, uint32_t high, const uint32_t (&id)[R], int wave, int lane) {
+  const int used = (int)((c.held + THREADS - 1) / THREADS);
+  const Cut cut = cut_of<THREADS, R>(lds, low, high, c.want, wave, lane, used);
+  count_chunks<THREADS, R>(lds, cut, wave, lane);
+  const uint64_t at = (uint64_t)row * s.keep;
+  const auto pages_out = row_buffer(s.pages_out + at, s.keep * 4u), places_out = row_buffer(s.places_out + at, s.keep * 4u);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (i < used) {
+      const Stay x = stay_of<THREADS, R>(lds, cut, i, lds.key[i][threadIdx.x], wave);
+      const int to = x.stays ? (int)x.before * 4 : -4;
+      __builtin_amdgcn_raw_buffer_store_b32(id[i], pages_out, to, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b32((uint32_t)i * THREADS + threadIdx.x, places_out, to, 0, 0);
+    }
+  }
+  fill_rest(s, row, c.left, THREADS);
+}
+
+// One workgroup per row of up to THREADS * R pages, their scores in the workspace.
 template <int THREADS, int R>
 __global__ __launch_bounds__(THREADS) void select_kernel(Select s) {
   __shared__ ChoiceLds<THREADS, R> lds;
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const uint32_t row = blockIdx.x;
+  const uint64_t at = (uint64_t)row * s.rows.max_pages;
+  const auto scores = row_buffer(s.scores + at, s.rows.max_pages * 4u), pages = row_buffer(s.rows.pages + at, s.rows.max_pages * 4u);
+  uint32_t w[R], id[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) w[i] = __builtin_amdgcn_raw_buffer_load_b32(scores, (int)threadIdx.x * 4 + i * THREADS * 4, 0, 0);
+#pragma unroll
+  for (int i = 0; i < R; ++i) id[i] = __builtin_amdgcn_raw_buffer_load_b32(pages, (int)threadIdx.x * 4 + i * THREADS * 4, 0, 0);
   const Selection c = selection_of(s, row);
   if (threadIdx.x == 0) s.lengths_out[row] = c.len - (int)((c.held - c.left) << s.page_shift);
-  const uint64_t at = (uint64_t)row * s.rows.max_pages;
-  const uint32_t span = c.want ? c.hi - c.lo : 0u;
   uint32_t low = 0xFFFFFFFFu, high = 0;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const uint32_t p = (uint32_t)i * THREADS + threadIdx.x;
-    uint32_t key = p < c.held && (!c.full || p < c.lo || p >= c.hi) ? kStays : 0u;
-    if (p - c.lo < span) {
-      key = weight_key(s.scores[at + p]);
+    const uint32_t key = page_key(c, p, __builtin_bit_cast(float, w[i]));
+    if (c.want && p - c.lo < c.hi - c.lo) {
       low = min(low, key);
       high = max(high, key);
     }
     lds.key[i][threadIdx.x] = key;
   }
-  const Cut cut = cut_of<THREADS, R>(lds, low, high, c.want, wave, lane);
-  count_chunks<THREADS, R>(lds, cut, wave, lane);
+  write_selection<THREADS, R>(s, c, lds, row, low, high, id, wave, lane);
+}
+
+// Rows of up to THREADS * R pages, scored and chosen from in one launch.
+template <int DJ, bool F16, int THREADS, int R>
+__global__ __launch_bounds__(THREADS) void select_short_kernel(Select s) {
+  constexpr int P = PageSet<DJ>::P;
+  constexpr int kAtOnce = score_pages(DJ, THREADS), kTimes = THREADS * R / kAtOnce;
+  __shared__ ScoreLds<DJ> score;
+  __shared__ ChoiceLds<THREADS, R> lds;
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const uint32_t row = blockIdx.x;
+  const Selection c = selection_of(s, row);
+  const ScoreRow r = score_row(s, c, row);
+  Queries16<DJ> q = load_queries<DJ>(s, r, 0, wave, lane);
+  PageIds<DJ> ids = load_ids<DJ>(r, wave * (16 * P), lane);
+  uint32_t id[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const uint32_t p = (uint32_t)i * THREADS + threadIdx.x;
-    const Stay x = stay_of<THREADS, R>(lds, cut, i, lds.key[i][threadIdx.x], wave);
-    if (x.stays) {
-      s.pages_out[(uint64_t)row * s.keep + x.before] = s.rows.pages[at + p];
-      s.places_out[(uint64_t)row * s.keep + x.before] = (int32_t)p;
+  for (int i = 0; i < R; ++i) id[i] = __builtin_amdgcn_raw_buffer_load_b32(r.pages, (int)threadIdx.x * 4 + i * THREADS * 4, 0, 0);
+  if (threadIdx.x == 0) s.lengths_out[row] = c.len - (int)((c.held - c.left) << s.page_shift);
+  uint32_t low = 0xFFFFFFFFu, high = 0;
+  if (c.want) {
+    const int times = (int)min((c.hi + kAtOnce - 1) / kAtOnce, (uint32_t)kTimes);
+    for (int i = 0; i < times; ++i) {
+      const uint32_t first = i * kAtOnce + wave * (16 * P);
+      const PageSet<DJ> x = load_outlines<DJ>(s, c, ids, first, lane);
+      ids = load_ids<DJ>(r, first + kAtOnce, lane);
+      float best[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) best[p] = -INFINITY;
+      for (int m0 = 0; m0 < s.m_rows; m0 += 16) {
+        if (i || m0) {  // more than 16 queries take turns in LDS
+          if (s.m_rows > 16) {
+            q = load_queries<DJ>(s, r, m0, wave, lane);
+            __syncthreads();
+          }
+        }
+        if (s.m_rows > 16 || i == 0) {
+          if (wave < 4) write_limbs<DJ, F16>(q, r, score, wave, lane);
+          __syncthreads();
+        }
+        take_queries<DJ>(x, score, lane, best);
+      }
+      const float mine = score_of_lane<DJ>(x, best, lane);
+      const uint32_t p = first + lane;
+      if (lane < 16 * P) lds.key[p / THREADS][p % THREADS] = page_key(c, p, mine);
     }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const uint32_t p = (uint32_t)i * THREADS + threadIdx.x;
+      if (p - c.lo < c.hi - c.lo) {
+        low = min(low, lds.key[i][threadIdx.x]);
+        high = max(high, lds.key[i][threadIdx.x]);
+      } else if (p >= (uint32_t)times * kAtOnce) {  // not scored
+        lds.key[i][threadIdx.x] = page_key(c, p, 0.f);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < R; ++i) lds.key[i][threadIdx.x] = page_key(c, (uint32_t)i * THREADS + threadIdx.x, 0.f);
   }
-  fill_rest(s, row, c.left, THREADS);
+  write_selection<THREADS, R>(s, c, lds, row, low, high, id, wave, lane);
 }
 
 // Rows of any length: the score is found digit by digit (8 bits at a time, from
@@ -1157,13 +1321,28 @@ bool too_many(uint64_t n_rows, uint64_t per_row, uint64_t per_group) {
   return per_row && (per_row > 0x7FFFFFFFull / n_rows || n_rows * per_row / per_group >= max_grid(kThreads));
 }
 
-template <int DJ>
-void launch_score(const Select& s, uint64_t n_rows, uint32_t dtype, hipStream_t st) {
-  const dim3 grid((uint32_t)n_rows * s.chunks.d);
-  if (dtype == IBP_KV_FP16)
-    hipLaunchKernelGGL((score_kernel<DJ, true>), grid, dim3(kThreads), 0, st, s);
+// Rows that are chosen from as they are scored, and the scores of the others.
+constexpr uint64_t kShortPages = 1024;
+uint64_t select_bytes(uint64_t n_rows, uint64_t max_pages) { return max_pages <= kShortPages ? 0 : n_rows * max_pages * 4; }
+
+template <int DJ, bool F16>
+void launch_select(const Select& s, uint64_t n_rows, uint64_t max_pages, hipStream_t st) {
+  const dim3 rows((uint32_t)n_rows);
+  // Rows of few pages are scored and chosen from in one launch: 8 rows of 251 pages 8 us,
+  // 12 as two; 16 x 32 rows of up to 256 pages 12 us, 20 as two.  (With 1024 threads and all
+  // pages at once the latter take 19 us, 72 rows of 50 to 500 pages the same 10 us.)
+  if (max_pages <= kShortPages) {
+    hipLaunchKernelGGL((select_short_kernel<DJ, F16, 256, 4>), rows, dim3(256), 0, st, s);
+    return;
+  }
+  if (s.keep > s.sink + s.recent && max_pages > s.keep)  // else there is nothing to choose
+    hipLaunchKernelGGL((score_kernel<DJ, F16>), dim3((uint32_t)n_rows * s.chunks.d), dim3(kThreads), 0, st, s);
+  if (max_pages <= 4096)
+    hipLaunchKernelGGL((select_kernel<1024, 4>), rows, dim3(1024), 0, st, s);
+  else if (max_pages <= 16384)
+    hipLaunchKernelGGL((select_kernel<1024, 16>), rows, dim3(1024), 0, st, s);
   else
-    hipLaunchKernelGGL((score_kernel<DJ, false>), grid, dim3(kThreads), 0, st, s);
+    hipLaunchKernelGGL(select_long_kernel, rows, dim3(kThreads), 0, st, s);
 }
 
 // The prefix of a call, as units of the query rows of all sequences, each cut into
@@ -1344,7 +1523,7 @@ int ibp_kv_outline(const ibp_kv_cache* cache, const ibp_kv_outlines* outlines, c
 uint64_t ibp_kv_select_workspace_bytes(const ibp_kv_cache* cache, const ibp_kv_table* table) {
   uint64_t n_rows = 0;
   if (check_cache(cache) || !table || check_table(table, cache->page_tokens, &n_rows)) return 0;
-  return n_rows * table->max_pages * 4;
+  return select_bytes(n_rows, table->max_pages);
 }
 
 int ibp_kv_select(const ibp_kv_cache* cache, const ibp_kv_outlines* outlines, const ibp_kv_table* table,
@@ -1369,19 +1548,19 @@ int ibp_kv_select(const ibp_kv_cache* cache, const ibp_kv_outlines* outlines, co
     return IBP_ERR_LAYOUT;
   const uint64_t group = q_heads / table->kv_heads;
   if (n_new && group > (1ull << 24) / n_new) return IBP_ERR_INVALID_ARGUMENT;
-  const uint64_t bytes = n_rows * table->max_pages * 4;
+  const uint64_t table_bytes = n_rows * table->max_pages * 4, bytes = select_bytes(n_rows, table->max_pages);
   if (bytes && (!workspace || workspace_bytes < bytes)) return IBP_ERR_INVALID_ARGUMENT;
   if (keep_pages > (1ull << 60) / n_rows) return IBP_ERR_INVALID_ARGUMENT;
   const uint64_t kept = n_rows * keep_pages * 4;
   const void* in[3] = {table->pages, table->lengths, workspace};
   void* outs[3] = {pages_out, places_out, lengths_out};
-  const uint64_t in_size[3] = {bytes, n_rows * 4, bytes}, out_size[3] = {kept, kept, n_rows * 4};
+  const uint64_t in_size[3] = {table_bytes, n_rows * 4, bytes}, out_size[3] = {kept, kept, n_rows * 4};
   for (int i = 0; i < 3; ++i)
     for (int j = 0; j < 3; ++j)
       if (overlap(in[i], in_size[i], outs[j], out_size[j]) || (i < j && overlap(outs[i], out_size[i], outs[j], out_size[j])))
         return IBP_ERR_INVALID_ARGUMENT;
   const int dj = (int)cache->head_dim / 64;
-  const uint64_t chunks = (table->max_pages + score_pages(dj) - 1) / score_pages(dj);
+  const uint64_t at_once = (uint64_t)score_pages(dj, kThreads), chunks = (table->max_pages + at_once - 1) / at_once;
   if (n_rows > max_grid(1024) || chunks > max_grid(kThreads) / n_rows) return IBP_ERR_INVALID_ARGUMENT;
   rc = pending_hip_error();
   if (rc) return rc;
@@ -1403,25 +1582,16 @@ int ibp_kv_select(const ibp_kv_cache* cache, const ibp_kv_outlines* outlines, co
   s.lengths_out = lengths_out;
   s.places_out = places_out;
   hipStream_t st = (hipStream_t)stream;
-  // rows with room for no more than keep_pages keep what they have
-  if (table->max_pages > keep_pages && keep_pages > sink_pages + recent_pages) {
-    switch (dj) {
-      case 1: launch_score<1>(s, n_rows, dtype, st); break;
-      case 2: launch_score<2>(s, n_rows, dtype, st); break;
-      case 3: launch_score<3>(s, n_rows, dtype, st); break;
-      default: launch_score<4>(s, n_rows, dtype, st); break;
-    }
-    if ((rc = launched())) return rc;
+  switch (dj * 2 + dtype) {
+    case 2: launch_select<1, false>(s, n_rows, table->max_pages, st); break;
+    case 3: launch_select<1, true>(s, n_rows, table->max_pages, st); break;
+    case 4: launch_select<2, false>(s, n_rows, table->max_pages, st); break;
+    case 5: launch_select<2, true>(s, n_rows, table->max_pages, st); break;
+    case 6: launch_select<3, false>(s, n_rows, table->max_pages, st); break;
+    case 7: launch_select<3, true>(s, n_rows, table->max_pages, st); break;
+    case 8: launch_select<4, false>(s, n_rows, table->max_pages, st); break;
+    default: launch_select<4, true>(s, n_rows, table->max_pages, st); break;
   }
-  const dim3 grid((uint32_t)n_rows);
-  if (table->max_pages <= 1024)
-    hipLaunchKernelGGL((select_kernel<256, 4>), grid, dim3(256), 0, st, s);
-  else if (table->max_pages <= 4096)
-    hipLaunchKernelGGL((select_kernel<1024, 4>), grid, dim3(1024), 0, st, s);
-  else if (table->max_pages <= 16384)
-    hipLaunchKernelGGL((select_kernel<1024, 16>), grid, dim3(1024), 0, st, s);
-  else
-    hipLaunchKernelGGL(select_long_kernel, grid, dim3(kThreads), 0, st, s);
   return launched();
 }
 

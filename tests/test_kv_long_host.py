@@ -235,7 +235,7 @@ def test_select_refusals(kv):
              wo=FAR[5], ws=FAR[6], ws_bytes=0):
         """With no bytes of workspace, so that nothing is launched."""
         return f(cache(kv) if c is None else c, outlines(kv) if o is None else o,
-                 table(kv, m=9, pages=FAR[1], lengths=FAR[2]) if t is None else t, dtype, heads, n, tensor(kv) if q is None else q, counts,
+                 table(kv, m=2000, pages=FAR[1], lengths=FAR[2]) if t is None else t, dtype, heads, n, tensor(kv) if q is None else q, counts,
                  keep, sink, recent, po, lo, wo, ws, ws_bytes, None)
     assert call() == INV                                      # the workspace
     assert f(None, outlines(kv), table(kv), 0, 4, 1, tensor(kv), None, 3, 1, 1, *FAR[3:7], 1 << 40, None) == INV
@@ -260,10 +260,12 @@ def test_select_refusals(kv):
     for names in (dict(po=FAR[1]), dict(lo=FAR[2]), dict(wo=FAR[6] + 64), dict(po=FAR[5] + 8), dict(lo=FAR[3] + 4)):
         assert overlapping(**names) == INV
     assert call(heads=1 << 26, ws_bytes=1 << 40) == INV
-    big = table(kv, n=1 << 22, h=1, m=9, pages=FAR[1], lengths=FAR[2])
+    big = table(kv, n=1 << 22, h=1, m=2000, pages=FAR[1], lengths=FAR[2])
     assert call(t=big, heads=1, ws_bytes=1 << 40, po=FAKE + (7 << 44), lo=FAKE + (8 << 44), wo=FAKE + (9 << 44), ws=FAKE + (10 << 44)) == INV
-    assert kv.long_lib().ibp_kv_select_workspace_bytes(cache(kv), table(kv, m=9)) == 2 * 2 * 9 * 4
-    assert kv.long_lib().ibp_kv_select_workspace_bytes(cache(kv, pt=24), table(kv, m=9)) == 0
+    need = kv.long_lib().ibp_kv_select_workspace_bytes
+    assert need(cache(kv), table(kv, m=1025)) == 2 * 2 * 1025 * 4
+    assert need(cache(kv), table(kv, m=1024)) == 0      # rows that are chosen from as they are scored
+    assert need(cache(kv, pt=24), table(kv, m=2000)) == 0
 
 
 def test_attention_shared_refusals(kv):
