@@ -544,6 +544,9 @@ __device__ __forceinline__ Queries16<DJ> load_queries(const Select& s, const Sco
   return y;
 }
 
+// Groups of 16 queries whose limbs are in LDS at a time: 32 KB.
+constexpr int query_slots(int dj) { return dj <= 2 ? 4 : 2; }
+
 template <int DJ, bool F16>
 __device__ __forceinline__ void write_limbs(const Queries16<DJ>& y, const ScoreRow& r, ScoreLds<DJ>& lds, int wave, int lane) {
   const int n = wave * 4 + lane / 16, x = lane % 16;
@@ -676,11 +679,36 @@ __device__ __forceinline__ float score_of_lane(const PageSet<DJ>& x, float (&bes
   return mine;
 }
 
+// The limbs of queries m0 .. of the row, as many as there are slots; the first four waves
+// make them, all wait.
+template <int DJ, bool F16>
+__device__ __forceinline__ void fill_slots(const Select& s, const ScoreRow& r, ScoreLds<DJ> (&lds)[query_slots(DJ)], int m0,
+                                           int wave, int lane, Queries16<DJ> (&q)[query_slots(DJ)]) {
+#pragma unroll
+  for (int i = 0; i < query_slots(DJ); ++i)
+    if (wave < 4 && m0 + 16 * i < s.m_rows) write_limbs<DJ, F16>(q[i], r, lds[i], wave, lane);
+  __syncthreads();
+}
+
+template <int DJ>
+__device__ __forceinline__ void load_slots(const Select& s, const ScoreRow& r, int m0, int wave, int lane,
+                                           Queries16<DJ> (&q)[query_slots(DJ)]) {
+#pragma unroll
+  for (int i = 0; i < query_slots(DJ); ++i)
+    if (m0 + 16 * i < s.m_rows) q[i] = load_queries<DJ>(s, r, m0 + 16 * i, wave, lane);
+}
+
+template <int DJ>
+__device__ __forceinline__ void take_slots(const Select& s, const PageSet<DJ>& x, const ScoreLds<DJ> (&lds)[query_slots(DJ)], int m0,
+                                           int lane, float (&best)[PageSet<DJ>::P]) {
+  for (int i = 0; i < query_slots(DJ) && m0 + 16 * i < s.m_rows; ++i) take_queries<DJ>(x, lds[i], lane, best);
+}
+
 // Scores of a run of a row's pages, into the workspace.
 template <int DJ, bool F16>
 __global__ __launch_bounds__(kThreads) void score_kernel(Select s) {
-  constexpr int P = PageSet<DJ>::P;
-  __shared__ ScoreLds<DJ> lds;
+  constexpr int P = PageSet<DJ>::P, kSlots = query_slots(DJ);
+  __shared__ ScoreLds<DJ> lds[kSlots];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const uint32_t row = quotient(blockIdx.x, s.chunks);
   const uint32_t from = (blockIdx.x - row * s.chunks.d) * score_pages(DJ, kThreads), first = from + wave * (16 * P);
@@ -688,21 +716,21 @@ __global__ __launch_bounds__(kThreads) void score_kernel(Select s) {
   // return in order and the outlines are on their way while the limbs are made.
   const Selection c = selection_of(s, row);
   const ScoreRow r = score_row(s, c, row);
-  Queries16<DJ> q = load_queries<DJ>(s, r, 0, wave, lane);
+  Queries16<DJ> q[kSlots];
+  load_slots<DJ>(s, r, 0, wave, lane, q);
   const PageIds<DJ> ids = load_ids<DJ>(r, first, lane);
   if (!c.full || !c.want || from >= c.hi || from + score_pages(DJ, kThreads) <= c.lo) return;
   const PageSet<DJ> x = load_outlines<DJ>(s, c, ids, first, lane);
   float best[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) best[p] = -INFINITY;
-  for (int m0 = 0; m0 < s.m_rows; m0 += 16) {
+  for (int m0 = 0; m0 < s.m_rows; m0 += 16 * kSlots) {
     if (m0) {
-      q = load_queries<DJ>(s, r, m0, wave, lane);
+      load_slots<DJ>(s, r, m0, wave, lane, q);
       __syncthreads();
     }
-    write_limbs<DJ, F16>(q, r, lds, wave, lane);
-    __syncthreads();
-    take_queries<DJ>(x, lds, lane, best);
+    fill_slots<DJ, F16>(s, r, lds, m0, wave, lane, q);
+    take_slots<DJ>(s, x, lds, m0, lane, best);
   }
   const float mine = score_of_lane<DJ>(x, best, lane);
   const uint32_t page = first + lane;
@@ -779,13 +807,15 @@ template <int DJ, bool F16, int THREADS, int R>
 __global__ __launch_bounds__(THREADS) void select_short_kernel(Select s) {
   constexpr int P = PageSet<DJ>::P;
   constexpr int kAtOnce = score_pages(DJ, THREADS), kTimes = THREADS * R / kAtOnce;
-  __shared__ ScoreLds<DJ> score;
+  constexpr int kSlots = query_slots(DJ);
+  __shared__ ScoreLds<DJ> score[kSlots];
   __shared__ ChoiceLds<THREADS, R> lds;
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const uint32_t row = blockIdx.x;
   const Selection c = selection_of(s, row);
   const ScoreRow r = score_row(s, c, row);
-  Queries16<DJ> q = load_queries<DJ>(s, r, 0, wave, lane);
+  Queries16<DJ> q[kSlots];
+  load_slots<DJ>(s, r, 0, wave, lane, q);
   PageIds<DJ> ids = load_ids<DJ>(r, wave * (16 * P), lane);
   uint32_t id[R];
 #pragma unroll
@@ -801,18 +831,14 @@ __global__ __launch_bounds__(THREADS) void select_short_kernel(Select s) {
       float best[P];
 #pragma unroll
       for (int p = 0; p < P; ++p) best[p] = -INFINITY;
-      for (int m0 = 0; m0 < s.m_rows; m0 += 16) {
-        if (i || m0) {  // more than 16 queries take turns in LDS
-          if (s.m_rows > 16) {
-            q = load_queries<DJ>(s, r, m0, wave, lane);
-            __syncthreads();
-          }
-        }
-        if (s.m_rows > 16 || i == 0) {
-          if (wave < 4) write_limbs<DJ, F16>(q, r, score, wave, lane);
+      for (int m0 = 0; m0 < s.m_rows; m0 += 16 * kSlots) {
+        const bool turns = s.m_rows > 16 * kSlots;  // the slots are filled again for each run of pages
+        if (turns && (i || m0)) {
+          load_slots<DJ>(s, r, m0, wave, lane, q);
           __syncthreads();
         }
-        take_queries<DJ>(x, score, lane, best);
+        if (turns || i == 0) fill_slots<DJ, F16>(s, r, score, m0, wave, lane, q);
+        take_slots<DJ>(s, x, score, m0, lane, best);
       }
       const float mine = score_of_lane<DJ>(x, best, lane);
       const uint32_t p = first + lane;

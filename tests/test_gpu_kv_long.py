@@ -277,7 +277,7 @@ def check_select(kv, p, o, lengths, q, keep, sink=1, recent=1, counts=None, gpu_
 @pytest.mark.parametrize("d", [64, 128, 192, 256])
 @pytest.mark.parametrize("pt", [16, 64])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("group,new", [(1, 1), (3, 1), (16, 1), (5, 5), (8, 4), (17, 2)])
+@pytest.mark.parametrize("group,new", [(1, 1), (3, 1), (16, 1), (5, 5), (8, 4), (35, 2)])
 def test_select(kv, d, pt, dtype, group, new):
     """Rows from none to more than a workgroup scores; one query to several
     groups of 16."""
@@ -289,6 +289,20 @@ def test_select(kv, d, pt, dtype, group, new):
     lengths[3, 1] = m * pt - pt - 1
     for keep, sink, recent in ((3, 0, 2), (9, 1, 2), (40, 2, 5), (139, 1, 2), (150, 0, 2)):
         check_select(kv, p, o, lengths, q, keep, sink, recent)
+
+
+@pytest.mark.parametrize("m", [300, 1100])
+@pytest.mark.parametrize("d", [64, 256])
+def test_select_many_queries(kv, d, m):
+    """More queries than LDS holds at a time, over several runs of pages; some
+    of a row's queries do not exist."""
+    seqs, heads, group, new = 2, 1, 13, 8
+    p = noise(kv, seqs, heads, m, 16, d, seed=m, n_pages=50)
+    o = outlined(p)
+    q = queries(1, seqs, new, heads * group, d, "fp16")
+    q[0, 1:7] *= 0.1
+    for counts in (None, [8, 3]):
+        check_select(kv, p, o, grid(seqs, heads, [m * 16, m * 16 - 100]), q, 20, 1, 2, counts=counts)
 
 
 @pytest.mark.parametrize("d", [64, 192])
