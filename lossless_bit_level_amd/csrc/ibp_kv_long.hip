@@ -1019,7 +1019,8 @@ __device__ __forceinline__ void attend_many(const Attention& a, uint32_t block) 
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) top_scale = fmaxf(top_scale, lds.top[w]);
-  const int scale_log = uniform(held_exponent(fmaxf(top_scale, 0x1p-126f)));  // L
+  const uint32_t top_bits = __builtin_bit_cast(uint32_t, fmaxf(top_scale, 0x1p-126f));
+  const int scale_log = uniform(min((int)(top_bits >> 23) - 127 + ((top_bits & 0x7FFFFFu) ? 1 : 0), 127));  // L
   const float c_scale = fabsf(a.scale);
 
   State<DJ, MT> st;

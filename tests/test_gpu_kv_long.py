@@ -446,7 +446,15 @@ def check_shared(kv, p, prefix_lengths, lengths, q, scale=None, counts=None, gpu
     o, err = lorc.attention_shared(p.k, p.v, p.pt, p.prefix, prefix_lengths, p.pages, lengths, q.double().numpy(),
                                    p.d ** -0.5 if scale is None else scale, c, rounding=fi.eps / 2, tiny=fi.tiny * fi.eps / 2,
                                    weight=WEIGHT[q.dtype])
-    close(out.cpu(), None, (o, None, err, None))
+    got = out.cpu()
+    # past the type's largest number an infinity, which a number within its error of that
+    # may be as well
+    far, near = np.abs(o) - err > fi.max, np.abs(o) + err > fi.max
+    infinite = near & np.isinf(got.double().numpy()) & (np.signbit(got.double().numpy()) == np.signbit(o))
+    assert infinite[far].all()
+    got[torch.from_numpy(infinite)] = 0
+    o[infinite] = 0
+    close(got, None, (o, None, err, None))
     return out
 
 
@@ -537,6 +545,58 @@ def test_attention_shared_nan(kv):
     p.upload()
     assert kv.ibp_kv_attention_shared(p.cache, gpu(p.prefix), gpu(np.array([100], np.int32)), p.gpu_pages,
                                       gpu(np.array([[60], [15], [20]], np.int32)), q.cuda()).isnan().all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("seqs", [3, 40])
+@pytest.mark.parametrize("scale", [0.02, -0.05])
+def test_attention_shared_scales_of_every_kind(kv, dtype, seqs, scale):
+    """Scales that are no powers of two, negative, zero, far apart; few and many
+    query rows."""
+    heads, group, pt, d = 2, 3, 16, 128
+    p = shared_pool(kv, seqs, heads, 40, 6, pt, d, seed=9)
+    rng = np.random.default_rng(4)
+    p.v[1] = rng.choice(np.array([1, 1, 1, 0.75, 3, 2.0 ** -30, 2.0 ** -70, 2.0 ** -126, 0, -0.0, -0.5, -3, 2.0 ** 20], np.float32), p.n_pages)
+    p.k[1] = rng.choice(np.array([1, 1, 0.5, -1, -0.3, 0, 1.7], np.float32), p.n_pages)
+    p.upload()
+    q = queries(2, seqs, 1, heads * group, d, dtype)
+    check_shared(kv, p, [640, 333], grid(seqs, heads, [(i * 7) % 90 + 1 for i in range(seqs)]), q, scale=scale)
+
+
+@pytest.mark.parametrize("seqs", [2, 40])
+def test_attention_shared_queries_not_finite(kv, seqs):
+    """They are NaN whole, and no other query is."""
+    p = shared_pool(kv, seqs, 1, 30, 4, 16, 64, seed=1)
+    q = queries(1, seqs, 1, 4, 64, "bf16")
+    q[0, 0, 1, 5], q[1, 0, 2, 0], q[1, 0, 3] = float("inf"), float("nan"), torch.finfo(q.dtype).max
+    out = kv.ibp_kv_attention_shared(p.cache, gpu(p.prefix), gpu(np.array([470], np.int32)), p.gpu_pages, gpu(grid(seqs, 1, [30] * seqs)),
+                                     q.cuda())
+    nan = np_of(out.isnan())
+    assert nan[0, 0, 1].all() and nan[1, 0, 2].all()
+    rest = np.ones(nan.shape[:3], bool)
+    rest[0, 0, 1] = rest[1, 0, 2] = rest[1, 0, 3] = False
+    assert not nan[rest].any()
+
+
+def test_attention_shared_tables_without_pages(kv):
+    """A prefix, rows, or both, of no pages at all."""
+    p = shared_pool(kv, 3, 2, 8, 4, 16, 64, seed=2)
+    q = queries(1, 3, 1, 4, 64, "fp16")
+    whole, own, prefix = p.pages, p.gpu_pages, p.prefix
+    p.prefix = prefix[:, :0]
+    check_shared(kv, p, [100, 0], grid(3, 2, [30, 1, 64]), q)
+    p.prefix, p.pages, p.gpu_pages = prefix, whole[:, :, :0], own[:, :, :0].contiguous()
+    assert not check_shared(kv, p, [100, 9], grid(3, 2, [30, 1, 64]), q).any()     # no place: the tokens do not exist
+    o = outlined(p)
+    got = kv.ibp_kv_select(p.cache, o.t, p.gpu_pages, gpu(grid(3, 2, [30, 1, 64])), q.cuda(), 4)
+    assert (got[0] == -1).all() and not got[1].any() and (got[2] == -1).all()
+    kv.ibp_kv_outline(p.cache, o.t, p.gpu_pages, gpu(grid(3, 2, [30, 1, 64])))
+    cos, sin = tables(70, 32)
+    k = queries(2, 3, 1, 2, 64, "fp16").cuda()
+    turned = kv.ibp_kv_append_rotated(p.cache, p.gpu_pages, gpu(grid(3, 2, [30, 1, 64])), k, k, gpu(cos), gpu(sin), q=q.cuda(), outlines=o.t)
+    torch.cuda.synchronize()
+    assert not turned.any()
+    o.check()
 
 
 def test_attention_shared_equals_attention_of_whole_rows(kv):
@@ -657,6 +717,8 @@ def test_graph_of_a_long_decoding_step(kv):
         s["pages"], s["left"], s["places"] = kv.ibp_kv_select(s["cache"], s["o"], p.gpu_pages, s["lengths"], turned, keep, workspace=ws[0])
         s["sparse"], _ = kv.ibp_kv_attention(s["cache"], s["pages"], s["left"], turned)
         s["out"] = kv.ibp_kv_attention_shared(s["cache"], prefix, pl, p.gpu_pages, s["lengths"], turned, workspace=ws[1])
+        many = turned.repeat(20, 1, 1, 1)
+        s["many"] = kv.ibp_kv_attention_shared(s["cache"], prefix, pl, p.gpu_pages.repeat(20, 1, 1), s["lengths"].repeat(20, 1), many)
 
     step(some)
     torch.cuda.synchronize()
@@ -676,7 +738,7 @@ def test_graph_of_a_long_decoding_step(kv):
         step(eager)
         torch.cuda.synchronize()
         for s in states:
-            for name in ("pages", "left", "places", "sparse", "out", "lengths"):
+            for name in ("pages", "left", "places", "sparse", "out", "many", "lengths"):
                 assert torch.equal(s[name], eager[name]), (i, name)
             for x, y in zip((*s["t"], *s["o"]), (*eager["t"], *eager["o"])):
                 assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), i
