@@ -1,6 +1,20 @@
 // libibp_kv_long: appends with rotated positions, outlines and selection of
 // pages, and attention over a shared prefix, on the 8-bit KV pages of libibp_kv,
 // for AMD Instinct MI355X (gfx950, CDNA4).  Calls: include/ibp_kv_long.h.
+//
+// Times below are of one launch by kernel trace unless something else is said; rates
+// count the bytes that the operation cannot do without.  A large copy reaches 6.1 TB/s
+// on this card, a large bf16 product 1.35 PFLOP/s.
+//
+//   append_rotated   as append, the rotation between its loads and its conversions, the
+//                    outline from the codes it has in registers; queries in further
+//                    workgroups of the launch: HBM, 5.0 TB/s
+//   outline          a wave for a run of a row's pages: HBM and the start of the waves, 4.3 TB/s
+//   select           rows of few pages in one launch, a workgroup each; of more in two,
+//                    scores by workgroups of 256 pages: a chain of dependent loads
+//   attention_shared the prefix's units and the rows' in one launch, joined by a second:
+//                    HBM with few query rows, with many the instructions of the softmax
+//                    and the matrix products
 #include "ibp_kv_core.h"
 
 #include "ibp_kv_long.h"
@@ -370,7 +384,10 @@ __device__ __forceinline__ void turn_query(const Queries& a, const Rows& rows, c
   }
 }
 
-// The first workgroups append, the others rotate the queries.
+// The first workgroups append, the others rotate the queries.  4 prompts of 4096 tokens x
+// 32 heads of 128 dims, with as many query heads and outlines: 682 MB in 137 us, 5.0 TB/s
+// (of what is moved, 759 MB with the angles, 5.5); with the outlines in a launch of their
+// own 157 us.  One user's token: 5.6 us.
 template <int DJ, bool F16, Pairs PAIRS>
 __global__ __launch_bounds__(kThreads) void append_rotated_kernel(Pool pool, Rows rows, Strided k, Strided v,
                                                                   Divisor pages_per_row, uint32_t n_tasks,
@@ -387,6 +404,9 @@ __global__ __launch_bounds__(kThreads) void append_rotated_kernel(Pool pool, Row
 // A wave takes up to 64 pages of a row (wave_pages) one after the other, a tile at a
 // time: it has their ids and scales at once, and the next tiles are on their way while
 // one is looked at.  e4m3 codes are exact in 16 bits, two to an instruction.
+// Two contexts of 131k and 91k tokens x 8 heads of 128 dims: 257 MB in 58.6 us, 4.4 TB/s,
+// of which reading the codes alone takes 48.  (A wave for two pages: 62 us; four lanes to
+// 16 dims, so that a load takes 64 bytes of a place: 68 us.)
 template <int DJ>
 __global__ __launch_bounds__(kThreads) void outline_kernel(Pool pool, Rows rows, ibp_kv_outlines o, Divisor chunks,
                                                            uint32_t n_chunks, int wave_pages) {
@@ -704,7 +724,9 @@ __device__ __forceinline__ void take_slots(const Select& s, const PageSet<DJ>& x
   for (int i = 0; i < query_slots(DJ) && m0 + 16 * i < s.m_rows; ++i) take_queries<DJ>(x, lds[i], lane, best);
 }
 
-// Scores of a run of a row's pages, into the workspace.
+// Scores of a run of a row's pages, into the workspace.  Bound by its chain of loads,
+// lengths and ids, then outlines: two contexts of 131k and 91k tokens x 8 heads (28 MB)
+// 11.2 us.
 template <int DJ, bool F16>
 __global__ __launch_bounds__(kThreads) void score_kernel(Select s) {
   constexpr int P = PageSet<DJ>::P, kSlots = query_slots(DJ);
@@ -773,7 +795,9 @@ __device__ __forceinline__ void write_selection(const Select& s, const Selection
   fill_rest(s, row, c.left, THREADS);
 }
 
-// One workgroup per row of up to THREADS * R pages, their scores in the workspace.
+// One workgroup per row of up to THREADS * R pages, their scores in the workspace: 16
+// rows of 8192 and 5664 pages 9.4 us, the rounds of the choice and the barriers between.
+// (With ids asked for once it is known what stays 13 us.)
 template <int THREADS, int R>
 __global__ __launch_bounds__(THREADS) void select_kernel(Select s) {
   __shared__ ChoiceLds<THREADS, R> lds;
@@ -802,7 +826,9 @@ __global__ __launch_bounds__(THREADS) void select_kernel(Select s) {
   write_selection<THREADS, R>(s, c, lds, row, low, high, id, wave, lane);
 }
 
-// Rows of up to THREADS * R pages, scored and chosen from in one launch.
+// Rows of up to THREADS * R pages, scored and chosen from in one launch: 16 x 32 rows of
+// 180 to 256 pages (30 MB) 11.5 us, which is the chain lengths and ids, outlines, limbs,
+// products, rounds of the choice, stores.
 template <int DJ, bool F16, int THREADS, int R>
 __global__ __launch_bounds__(THREADS) void select_short_kernel(Select s) {
   constexpr int P = PageSet<DJ>::P;
@@ -956,6 +982,14 @@ __global__ __launch_bounds__(kThreads) void select_long_kernel(Select s) {
 // below the largest so far: in fp16 that is 11 bits of each weight of at least
 // 2^-21 of the largest.  Outputs of bf16 have 8; for those of fp16 what the
 // rounding cuts off goes through the product as well.
+//
+// 96 x 64 queries of 128 dims over 32,768 tokens x 8 heads, and own rows of 70 to 700
+// tokens: 134 us for both, 0.78 PFLOP/s, with the matrix cores busy for 36% of the time
+// (40% while there is work) and the vector units for half of it: a step of 64 x 32
+// scores is 64 matrix instructions (1043 cycles) and some 320 others (1400 cycles), of
+// which two waves to a SIMD overlap half.  The softmax's instructions cost a quarter of
+// it; the exponentials alone, the loads and the order of the instructions nothing that
+// shows.  One exponential and 16-bit terms as in attend_part: 260 us.
 constexpr float kTop = 15.f, kStart = 7.f;
 constexpr int many_tiles(int dj) { return dj <= 2 ? 4 : 2; }  // groups of 16 query rows
 
@@ -1207,6 +1241,8 @@ __device__ __forceinline__ void attend_many(const Attention& a, uint32_t block) 
   }
 }
 
+// With few query rows bound by HBM: 16 x 32 rows of 256 to 512 tokens behind 4096 (86 MB)
+// 17.2 us; as two launches 24.
 // The first workgroups take the prefix (KIND 1 and 2: one unit of as many groups of
 // 16 query rows to a head; 0: many), the others the rows' own tokens, MT groups of
 // query rows to a unit.  One launch: the rows' workgroups take the places of the
@@ -1222,7 +1258,7 @@ __global__ __launch_bounds__(kThreads, workgroups_per_unit(DJ, KIND > MT ? KIND 
 }
 
 // Joins the sums over the prefix (a) with those over a row's own tokens (b), a
-// query row to each wave.
+// query row to each wave.  3.5 to 8 us: its loads wait for each other.
 template <int DJ, bool F16, int MT>
 __global__ __launch_bounds__(kThreads) void join_shared_kernel(Attention a, Attention b, Divisor rows_of_head,
                                                                uint32_t n_rows, int shared_step_tiles) {
