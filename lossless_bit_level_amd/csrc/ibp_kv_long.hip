@@ -9,7 +9,8 @@
 //   append_rotated   as append, the rotation between its loads and its conversions, the
 //                    outline from the codes it has in registers; queries in further
 //                    workgroups of the launch: HBM, 5.0 TB/s
-//   outline          a wave for a run of a row's pages: HBM and the start of the waves, 4.3 TB/s
+//   outline          a wave for a run of a row's pages: HBM and half as much in vector
+//                    instructions, 4.8 TB/s
 //   select           rows of few pages in one launch, a workgroup each; of more in two,
 //                    scores by workgroups of 256 pages: a chain of dependent loads
 //   attention_shared the prefix's units and the rows' in one launch, joined by a second:
@@ -90,16 +91,17 @@ struct Bounds4 {
   }
 };
 
-// Four numbers in units of 1 / per, rounded up, or down.
+// Four numbers in units of 1 / per, at most 127 of them, rounded up, or down.  128 more is
+// a positive number, which one instruction makes a byte of.
 template <bool UP>
 __device__ __forceinline__ uint32_t whole4(const f16x2 (&x)[2], float per) {
   uint32_t word = 0;
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
-    const float y = (float)x[b / 2][b % 2] * per;
-    word |= (uint32_t)((int)(UP ? __builtin_ceilf(y) : __builtin_floorf(y)) & 255) << (8 * b);
+    const float y = __builtin_fmaf((float)x[b / 2][b % 2], per, 128.f);  // exact
+    word = __builtin_amdgcn_cvt_pk_u8_f32(UP ? __builtin_ceilf(y) : __builtin_floorf(y), b, word);
   }
-  return word;
+  return word ^ 0x80808080u;
 }
 
 // Bounds of the keys of a tile, four dims to a lane, through the wave's words in LDS:
@@ -120,9 +122,15 @@ __device__ __forceinline__ Bounds4 tile_bounds(const u32x4 (&kc)[DJ], uint32_t* 
   Bounds4 x;
   x.clear();
   if (tokens > 0) {
-    auto word = [&](int i) { return words[r / 4 * kKeyPitch + 4 * min(from + i, tokens - 1) + r % 4]; };
+    const uint32_t* mine = words + r / 4 * kKeyPitch + r % 4;
+    if (tokens >= kTile) {
 #pragma unroll
-    for (int i = 0; i < kRun; i += 2) x.take(word(i), word(i + 1));  // past the tile's tokens the last one again
+      for (int i = 0; i < kRun; i += 2) x.take(mine[4 * (from + i)], mine[4 * (from + i + 1)]);
+    } else {  // past the tile's tokens the last one again
+      auto word = [&](int i) { return mine[4 * min(from + i, tokens - 1)]; };
+#pragma unroll
+      for (int i = 0; i < kRun; i += 2) x.take(word(i), word(i + 1));
+    }
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -145,9 +153,10 @@ __device__ __forceinline__ Bounds4 tile_bounds(const u32x4 (&kc)[DJ], uint32_t* 
 template <int DJ>
 __device__ __forceinline__ void write_outline(const ibp_kv_outlines& o, const Bounds4& x, int lane, uint32_t id, float k_scale) {
   constexpr int D = 64 * DJ;
-  const float top = x.largest();
-  const bool bad = __ballot(top != top) != 0 || !finite(k_scale);
-  const int e = max(whole_exponent(wave_max(top)), -15);
+  // magnitudes are in the order of their bits, NaN of either sign above them
+  const uint32_t top = (uint32_t)uniform((int)wave_max(__builtin_bit_cast(uint32_t, x.largest())));
+  const bool bad = top > 0x7F800000u || !finite(k_scale);
+  const int e = max(whole_exponent(__builtin_bit_cast(float, top)), -15);
   const float per = bad ? 0.f : power2(-e);
   if (lane == 0) o.scales[id] = bad ? NAN : k_scale * power2(e);
   if (lane >= 16 * DJ) return;
@@ -401,15 +410,16 @@ __global__ __launch_bounds__(kThreads) void append_rotated_kernel(Pool pool, Row
 
 // -------------------------------------------------------------- outline ----
 
-// A wave takes up to 64 pages of a row (wave_pages) one after the other, a tile at a
-// time: it has their ids and scales at once, and the next tiles are on their way while
-// one is looked at.  e4m3 codes are exact in 16 bits, two to an instruction.
-// Two contexts of 131k and 91k tokens x 8 heads of 128 dims: 257 MB in 58.6 us, 4.4 TB/s,
-// of which reading the codes alone takes 48.  (A wave for two pages: 62 us; four lanes to
-// 16 dims, so that a load takes 64 bytes of a place: 68 us.)
+// A row's waves share its pages evenly, up to 64 to a wave, which takes them one after
+// the other, a tile at a time: it has their ids and scales at once, and the next tiles
+// are on their way while one is looked at.  e4m3 codes are exact in 16 bits, two to an instruction.
+// Two contexts of 131k and 91k tokens x 8 heads of 128 dims: 257 MB in 54 us, 4.8 TB/s,
+// of which reading the codes alone takes 48; a tile is 100 vector instructions, with 150
+// it took 60.  (A wave for two pages at most: 62 us; four lanes to 16 dims, so that a load
+// takes 64 bytes of a place: 68 us, both of those with 150.)
 template <int DJ>
 __global__ __launch_bounds__(kThreads) void outline_kernel(Pool pool, Rows rows, ibp_kv_outlines o, Divisor chunks,
-                                                           uint32_t n_chunks, int wave_pages) {
+                                                           uint32_t n_chunks) {
   constexpr int kAhead = DJ <= 2 ? 4 : 2;  // tiles on their way
   __shared__ __attribute__((aligned(16))) uint32_t s_keys[kWaves][4 * DJ * kKeyPitch];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
@@ -419,7 +429,9 @@ __global__ __launch_bounds__(kThreads) void outline_kernel(Pool pool, Rows rows,
   const int end = row_length(rows, row), count = new_count(rows, seq);
   const int page_shift = 4 + (int)pool.tile_shift, tiles = 1 << pool.tile_shift;
   const int held = (end + (1 << page_shift) - 1) >> page_shift;
-  const int from = (max(end - count, 0) >> page_shift) + (int)(task - row * chunks.d) * wave_pages;
+  const int touched = max(end - count, 0) >> page_shift;
+  const int wave_pages = (int)quotient((uint32_t)(held - touched) + chunks.d - 1u, chunks);
+  const int from = touched + (int)(task - row * chunks.d) * wave_pages;
   const int pages = count > 0 ? min(held - from, wave_pages) : 0;
   if (pages <= 0) return;
   uint32_t ids = ~0u;
@@ -1353,8 +1365,8 @@ void launch_append_pairs(const Pool& pool, const Rows& rows, const Strided& k, c
 }
 
 // Waves to a compute unit that the pages of an outline call are spread over: two
-// contexts of 131k and 91k tokens x 8 heads (257 MB) take 58.6 us so, 60.1 with 24,
-// 63 with 32 and 64.5 with 64, since each begins with a chain of three loads.
+// contexts of 131k and 91k tokens x 8 heads (257 MB) take 54.0 us so, 53.7 with 12, 63.5
+// with 8, 57.0 with 24 and 59.9 with 32, since each begins with a chain of three loads.
 constexpr int kOutlineWaves = 16;
 
 int launch_outline(const ibp_kv_cache* cache, const ibp_kv_outlines* o, const Rows& rows, uint64_t n_rows,
@@ -1368,12 +1380,11 @@ int launch_outline(const ibp_kv_cache* cache, const ibp_kv_outlines* o, const Ro
   const dim3 grid((uint32_t)((tasks + kWaves - 1) / kWaves)), threads(kThreads);
   const Divisor d = make_divisor((uint32_t)chunks);
   const uint32_t n = (uint32_t)tasks;
-  const int wp = (int)wave_pages;
   switch (dj) {
-    case 1: hipLaunchKernelGGL(outline_kernel<1>, grid, threads, 0, st, pool, rows, *o, d, n, wp); break;
-    case 2: hipLaunchKernelGGL(outline_kernel<2>, grid, threads, 0, st, pool, rows, *o, d, n, wp); break;
-    case 3: hipLaunchKernelGGL(outline_kernel<3>, grid, threads, 0, st, pool, rows, *o, d, n, wp); break;
-    default: hipLaunchKernelGGL(outline_kernel<4>, grid, threads, 0, st, pool, rows, *o, d, n, wp); break;
+    case 1: hipLaunchKernelGGL(outline_kernel<1>, grid, threads, 0, st, pool, rows, *o, d, n); break;
+    case 2: hipLaunchKernelGGL(outline_kernel<2>, grid, threads, 0, st, pool, rows, *o, d, n); break;
+    case 3: hipLaunchKernelGGL(outline_kernel<3>, grid, threads, 0, st, pool, rows, *o, d, n); break;
+    default: hipLaunchKernelGGL(outline_kernel<4>, grid, threads, 0, st, pool, rows, *o, d, n); break;
   }
   return launched();
 }
