@@ -249,6 +249,34 @@ def test_outline_of_every_largest_code(kv):
     o.check()
 
 
+@pytest.mark.parametrize("pt,d,m,new", [(16, 64, 5000, None), (16, 128, 4097, 60001), (32, 128, 3001, None), (32, 192, 2500, 70000),
+                                        (64, 256, 1501, None), (16, 64, 70000, None)])
+def test_outline_many_pages_to_a_wave(kv, pt, d, m, new):
+    """Rows of so many pages that a wave takes several, up to 64, which end at any
+    place of a run; rows of different lengths; holes; pages that rows share."""
+    p = noise(kv, 2, 2, m, pt, d, seed=m, n_pages=300)
+    p.k[0][5, 3 * d + 1] = 0x7F
+    p.k[1][9] = np.inf
+    p.upload()
+    p.pages %= 290
+    p.pages[:, :, ::97] = -1
+    lengths = np.array([[m * pt - 3, m * pt // 3 + 1], [(m - 1) * pt + 1, 5 * pt - 2]], np.int32)
+    for row, last in enumerate(((lengths - 1) // pt).reshape(-1)):
+        p.pages.reshape(4, m)[row, last] = 290 + row              # the one page of a row that is not full
+    o = Outlines(p)
+    n = m * pt if new is None else new
+    for s in range(2):
+        for h in range(2):
+            first = max(int(lengths[s, h]) - n, 0) // pt
+            last = (int(lengths[s, h]) - 1) // pt
+            ids = np.unique(p.pages[s, h, first:last])            # each of them once is enough
+            ids = np.concatenate((ids[ids >= 0], p.pages[s, h, last:last + 1])).astype(np.int32)[None, None]
+            tokens = (ids.size - 1) * pt + int(lengths[s, h]) - last * pt
+            lorc.outline(*p.k, orc.k_place(pt, d), pt, ids, np.array([[tokens]]), o.codes, o.scales, tokens)
+    kv.ibp_kv_outline(p.cache, o.t, gpu(p.pages), gpu(lengths), n_new=new)
+    o.check()
+
+
 # ------------------------------------------------------------ selection ----
 
 
