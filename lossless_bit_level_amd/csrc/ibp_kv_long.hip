@@ -394,7 +394,7 @@ __device__ __forceinline__ void turn_query(const Queries& a, const Rows& rows, c
 }
 
 // The first workgroups append, the others rotate the queries.  4 prompts of 4096 tokens x
-// 32 heads of 128 dims, with as many query heads and outlines: 682 MB in 137 us, 5.0 TB/s
+// 32 heads of 128 dims, with as many query heads and outlines: 682 MB in 136 us, 5.0 TB/s
 // (of what is moved, 759 MB with the angles, 5.5); with the outlines in a launch of their
 // own 157 us.  One user's token: 5.6 us.
 template <int DJ, bool F16, Pairs PAIRS>
@@ -996,10 +996,12 @@ __global__ __launch_bounds__(kThreads) void select_long_kernel(Select s) {
 // rounding cuts off goes through the product as well.
 //
 // 96 x 64 queries of 128 dims over 32,768 tokens x 8 heads, and own rows of 70 to 700
-// tokens: 134 us for both, 0.78 PFLOP/s, with the matrix cores busy for 36% of the time
-// (40% while there is work) and the vector units for half of it: a step of 64 x 32
+// tokens: calls back to back 126 us with 8 of joining, 0.83 PFLOP/s (a traced launch 133
+// to 150), with the matrix cores busy for 36% of the time (40% while there is work) and
+// the vector units for half of it: a step of 64 x 32
 // scores is 64 matrix instructions (1043 cycles) and some 320 others (1400 cycles), of
-// which two waves to a SIMD overlap half.  The softmax's instructions cost a quarter of
+// which two waves to a SIMD overlap half.  (Own rows' workgroups before the prefix's, so
+// that their loads run beside its arithmetic: 3 to 8 us more.)  The softmax's instructions cost a quarter of
 // it; the exponentials alone, the loads and the order of the instructions nothing that
 // shows.  One exponential and 16-bit terms as in attend_part: 260 us.
 constexpr float kTop = 15.f, kStart = 7.f;

@@ -772,6 +772,42 @@ def test_graph_of_a_long_decoding_step(kv):
                 assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), i
 
 
+def test_two_calls_at_once(kv):
+    """Calls on two streams over one cache, with workspaces of their own: each
+    gives what it gives alone."""
+    seqs, heads, group, d, pt, m = 9, 2, 5, 128, 16, 1100
+    p = shared_pool(kv, seqs, heads, 300, m, pt, d, seed=11)
+    o = outlined(p)
+    prefix, pl = gpu(p.prefix), torch.full((heads,), 300 * pt - 7, dtype=torch.int32, device="cuda")
+    lengths = [gpu(grid(seqs, heads, [m * pt - 40 * i - j for i in range(seqs)])) for j in range(2)]
+    q = [queries(j, seqs, 1, heads * group, d, "bf16").cuda() for j in range(2)]
+    angles = [gpu(t) for t in tables(m * pt, 64)]
+    own = gpu(np.arange(seqs * heads, dtype=np.int32).reshape(seqs, heads, 1))
+
+    def calls(j, cache, outlines, stream=None):
+        k = q[j][:, :, :heads]
+        turned = kv.ibp_kv_append_rotated(cache, own, gpu(grid(seqs, heads, [5 + j] * seqs)), k, k, *angles, q=q[j],
+                                          outlines=outlines, stream=stream)
+        chosen = kv.ibp_kv_select(p.cache, o.t, p.gpu_pages, lengths[j], q[j], 50, 1, 1, stream=stream)
+        return (turned, *chosen, kv.ibp_kv_attention_shared(p.cache, prefix, pl, p.gpu_pages, lengths[j], q[j], stream=stream))
+
+    def spare():  # what the appends write, each call's own
+        t = [x.clone() for x in p.t]
+        return kv.ibp_kv_cache(*t, pt, d), tuple(x.clone() for x in o.t)
+    alone = []
+    for j in range(2):
+        alone.append(calls(j, *spare()))
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        room = [spare() for _ in range(2)]
+        torch.cuda.synchronize()
+        got = [calls(j, *room[j], stream=streams[j]) for j in range(2)]
+        torch.cuda.synchronize()
+        for x, y in zip(got, alone):
+            assert all(torch.equal(a, b) for a, b in zip(x, y))
+
+
 def test_long_calls_have_no_gradient(kv):
     p = filled(kv, 1, 2, 10, 16, 64, [100], seed=1)
     o = outlined(p)
