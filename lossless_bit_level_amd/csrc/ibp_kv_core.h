@@ -1452,14 +1452,15 @@ __device__ __forceinline__ Cut cut_of(ChoiceLds<THREADS, R>& s, uint32_t low, ui
   return cut;
 }
 
-// Counts of what stays before each 64 pages.
+// Counts of what stays before each 64 pages; the first `used` of a thread's keys.
 template <int THREADS, int R>
-__device__ __forceinline__ void count_chunks(ChoiceLds<THREADS, R>& s, const Cut& cut, int wave, int lane) {
+__device__ __forceinline__ void count_chunks(ChoiceLds<THREADS, R>& s, const Cut& cut, int wave, int lane, int used = R) {
   constexpr int kW = THREADS / kWave;
   constexpr int kUnroll = R < 8 ? R : 8;
-  constexpr int kChunks = R * kW;
+  const int chunks = used * kW;
 #pragma unroll kUnroll
   for (int i = 0; i < R; ++i) {
+    if (i >= used) continue;
     const uint32_t key = s.key[i][threadIdx.x];
     uint32_t n = (uint32_t)__popcll(__ballot(key > cut.last));
     if (cut.ties) n += (uint32_t)__popcll(__ballot(key == cut.last)) << 16;
@@ -1470,13 +1471,13 @@ __device__ __forceinline__ void count_chunks(ChoiceLds<THREADS, R>& s, const Cut
     uint32_t x[4], sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[i] = 4 * lane + i < kChunks ? s.chunk[4 * lane + i] : 0u;
+      x[i] = 4 * lane + i < chunks ? s.chunk[4 * lane + i] : 0u;
       sum += x[i];
     }
     uint32_t before = wave_scan(sum) - sum;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (4 * lane + i < kChunks) s.chunk[4 * lane + i] = before;
+      if (4 * lane + i < chunks) s.chunk[4 * lane + i] = before;
       before += x[i];
     }
   }

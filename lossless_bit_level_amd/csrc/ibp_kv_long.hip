@@ -786,30 +786,31 @@ __device__ __forceinline__ uint32_t page_key(const Selection& c, uint32_t p, flo
 }
 
 // Chooses and writes: id[i] is that of the thread's page i.  Through buffers that end
-// with the row: what does not stay is written past it, which is to say not at all.
+// with the row, whatever the scores were.
 template <int THREADS, int R>
 __device__ __forceinline__ void write_selection(const Select& s, const Selection& c, ChoiceLds<THREADS, R>& lds, uint32_t row,
-                                                uint32_t low, uint32_t high, const uint32_t (&id)[R], int wave, int lane) {
-  const int used = (int)((c.held + THREADS - 1) / THREADS);
+                                                uint32_t low, uint32_t high, const uint32_t (&id)[R], int wave, int lane, int used) {
   const Cut cut = cut_of<THREADS, R>(lds, low, high, c.want, wave, lane, used);
-  count_chunks<THREADS, R>(lds, cut, wave, lane);
+  count_chunks<THREADS, R>(lds, cut, wave, lane, used);
   const uint64_t at = (uint64_t)row * s.keep;
   const auto pages_out = row_buffer(s.pages_out + at, s.keep * 4u), places_out = row_buffer(s.places_out + at, s.keep * 4u);
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     if (i < used) {
       const Stay x = stay_of<THREADS, R>(lds, cut, i, lds.key[i][threadIdx.x], wave);
-      const int to = x.stays ? (int)x.before * 4 : -4;
-      __builtin_amdgcn_raw_buffer_store_b32(id[i], pages_out, to, 0, 0);
-      __builtin_amdgcn_raw_buffer_store_b32((uint32_t)i * THREADS + threadIdx.x, places_out, to, 0, 0);
+      if (x.stays) {
+        __builtin_amdgcn_raw_buffer_store_b32(id[i], pages_out, (int)x.before * 4, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32((uint32_t)i * THREADS + threadIdx.x, places_out, (int)x.before * 4, 0, 0);
+      }
     }
   }
   fill_rest(s, row, c.left, THREADS);
 }
 
 // One workgroup per row of up to THREADS * R pages, their scores in the workspace: 16
-// rows of 8192 and 5664 pages 9.4 us, the rounds of the choice and the barriers between.
-// (With ids asked for once it is known what stays 13 us.)
+// rows of 8192 and 5664 pages 7.6 us, the rounds of the choice and the barriers between.
+// (With ids asked for once it is known what stays 13 us; where all pages of a row of the
+// largest size were looked at, and what does not stay written past the row's end, 9.4.)
 template <int THREADS, int R>
 __global__ __launch_bounds__(THREADS) void select_kernel(Select s) {
   __shared__ ChoiceLds<THREADS, R> lds;
@@ -825,17 +826,20 @@ __global__ __launch_bounds__(THREADS) void select_kernel(Select s) {
   const Selection c = selection_of(s, row);
   if (threadIdx.x == 0) s.lengths_out[row] = c.len - (int)((c.held - c.left) << s.page_shift);
   uint32_t low = 0xFFFFFFFFu, high = 0;
+  const int used = (int)((c.held + THREADS - 1) / THREADS);
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const uint32_t p = (uint32_t)i * THREADS + threadIdx.x;
-    const uint32_t key = page_key(c, p, __builtin_bit_cast(float, w[i]));
-    if (c.want && p - c.lo < c.hi - c.lo) {
-      low = min(low, key);
-      high = max(high, key);
+    if (i < used) {
+      const uint32_t p = (uint32_t)i * THREADS + threadIdx.x;
+      const uint32_t key = page_key(c, p, __builtin_bit_cast(float, w[i]));
+      if (c.want && p - c.lo < c.hi - c.lo) {
+        low = min(low, key);
+        high = max(high, key);
+      }
+      lds.key[i][threadIdx.x] = key;
     }
-    lds.key[i][threadIdx.x] = key;
   }
-  write_selection<THREADS, R>(s, c, lds, row, low, high, id, wave, lane);
+  write_selection<THREADS, R>(s, c, lds, row, low, high, id, wave, lane, used);
 }
 
 // Rows of up to THREADS * R pages, scored and chosen from in one launch: 16 x 32 rows of
@@ -860,6 +864,7 @@ __global__ __launch_bounds__(THREADS) void select_short_kernel(Select s) {
   for (int i = 0; i < R; ++i) id[i] = __builtin_amdgcn_raw_buffer_load_b32(r.pages, (int)threadIdx.x * 4 + i * THREADS * 4, 0, 0);
   if (threadIdx.x == 0) s.lengths_out[row] = c.len - (int)((c.held - c.left) << s.page_shift);
   uint32_t low = 0xFFFFFFFFu, high = 0;
+  const int used = (int)((c.held + THREADS - 1) / THREADS);
   if (c.want) {
     const int times = (int)min((c.hi + kAtOnce - 1) / kAtOnce, (uint32_t)kTimes);
     for (int i = 0; i < times; ++i) {
@@ -886,6 +891,7 @@ __global__ __launch_bounds__(THREADS) void select_short_kernel(Select s) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const uint32_t p = (uint32_t)i * THREADS + threadIdx.x;
+      if (i >= used) continue;
       if (p - c.lo < c.hi - c.lo) {
         low = min(low, lds.key[i][threadIdx.x]);
         high = max(high, lds.key[i][threadIdx.x]);
@@ -894,10 +900,9 @@ __global__ __launch_bounds__(THREADS) void select_short_kernel(Select s) {
       }
     }
   } else {
-#pragma unroll
-    for (int i = 0; i < R; ++i) lds.key[i][threadIdx.x] = page_key(c, (uint32_t)i * THREADS + threadIdx.x, 0.f);
+    for (int i = 0; i < used; ++i) lds.key[i][threadIdx.x] = page_key(c, (uint32_t)i * THREADS + threadIdx.x, 0.f);
   }
-  write_selection<THREADS, R>(s, c, lds, row, low, high, id, wave, lane);
+  write_selection<THREADS, R>(s, c, lds, row, low, high, id, wave, lane, used);
 }
 
 // Rows of any length: the score is found digit by digit (8 bits at a time, from
