@@ -993,9 +993,12 @@ __global__ __launch_bounds__(kThreads) void select_long_kernel(Select s) {
 //     z_j = exp2(s_j + log2(vs_j) - M),
 // so that the second product takes z as it is, with the codes; its largest is what
 // M follows.  The softmax's sum needs exp2(s_j) alone: with L the logarithm of the
-// part's largest scale, rounded up, a tile's sum of z times 2^L / vs is that in
-// units of 2^(M - L).  (Pages whose scale is below 2^(L - 64) count as zeros, and
-// their weight counts.)  z is held between 2^-24 and 2^kTop, M a step of 2^kStart
+// part's largest scale a tile's sum of z times 2^L / vs is that in units of
+// 2^(M - L).  (Pages whose scale is below 2^(L - 64) count as zeros, and
+// their weight counts.)  This is for scales that are powers of two, as an append
+// writes them, and 0; a part with others takes attend_part's softmax and second
+// product.
+// z is held between 2^-24 and 2^kTop, M a step of 2^kStart
 // below the largest so far: in fp16 that is 11 bits of each weight of at least
 // 2^-21 of the largest.  Outputs of bf16 have 8; for those of fp16 what the
 // rounding cuts off goes through the product as well.
@@ -1008,7 +1011,7 @@ __global__ __launch_bounds__(kThreads) void select_long_kernel(Select s) {
 // which two waves to a SIMD overlap half.  (Own rows' workgroups before the prefix's, so
 // that their loads run beside its arithmetic: 3 to 8 us more.)  The softmax's instructions cost a quarter of
 // it; the exponentials alone, the loads and the order of the instructions nothing that
-// shows.  One exponential and 16-bit terms as in attend_part: 260 us.
+// shows.  With attend_part's softmax and 16-bit terms for every part: 171 us.
 constexpr float kTop = 15.f, kStart = 7.f;
 constexpr int many_tiles(int dj) { return dj <= 2 ? 4 : 2; }  // groups of 16 query rows
 
@@ -1021,115 +1024,67 @@ struct ManyLds {
     float o[kWaves][16][64 + 4];
   };
   f32x2 ml[kWaves][MT * 16];
-  float top[kWaves];
+  uint32_t top[kWaves];
 };
 
-// Logarithm of a scale above 0; exact for powers of two.
-__device__ __forceinline__ float log2_scale(float x) {
-  const uint32_t b = __builtin_bit_cast(uint32_t, x);
-  if ((b & 0x7FFFFFu) == 0 && b >= 0x00800000u) return (float)((int)(b >> 23) - 127);
-  return log2_fast(x * 0x1p64f) - 64.f;
-}
-
-template <int DJ, bool F16>
-__device__ __forceinline__ void attend_many(const Attention& a, uint32_t block) {
-  constexpr int D = 64 * DJ, MT = many_tiles(DJ), ST = 2;
-  __shared__ __attribute__((aligned(16))) ManyLds<DJ, MT> lds;
-  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const Part part = part_of_shared(a, block);
-  const Plan p = plan_shared<MT, ST>(a, part);
-  const int first = part.index * p.part_steps, last = min(first + p.part_steps, p.steps);
-  if (first >= last) return;
-
-  // the queries, negated where the scale is below 0, so that the largest product gives
-  // the largest score
-  const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
-  for (int i = wave; i < MT * DJ; i += kWaves) {
-    const int mt = i / DJ, j = i % DJ, m = p.m0 + mt * 16 + lane % 16;
-    u32x4 x[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    if (m < a.m_rows) {
-      const uint16_t* src = row_of_all(a.q, a, p, m) + 64 * j + 16 * (lane / 16);
-      x[0] = load8(src, a.q.wide);
-      x[1] = load8(src + 8, a.q.wide);
-    }
-    lds.q[mt][j][0][lane] = x[0] ^ sign;
-    lds.q[mt][j][1][lane] = x[1] ^ sign;
-  }
-  // the largest scale
-  const int tiles_of_page = 1 << a.pool.tile_shift;
-  float top_scale = 0.f;
-  {
-    const int from = first * ST / tiles_of_page, to = (min(last * ST, p.tiles) + tiles_of_page - 1) / tiles_of_page;
-    const int32_t* pages = a.rows.pages + (uint64_t)p.row * a.rows.max_pages;
-    for (int i = from + (int)threadIdx.x; i < to; i += kThreads) {
-      const uint32_t id = (uint32_t)pages[i];
-      const float x = id < a.pool.n_pages ? fabsf(a.pool.v_scales[id]) : 0.f;
-      top_scale = fmaxf(top_scale, finite(x) ? x : 0.f);
-    }
-  }
-  top_scale = wave_max(top_scale);
-  if (lane == 0) lds.top[wave] = top_scale;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) top_scale = fmaxf(top_scale, lds.top[w]);
-  const uint32_t top_bits = __builtin_bit_cast(uint32_t, fmaxf(top_scale, 0x1p-126f));
-  const int scale_log = uniform(min((int)(top_bits >> 23) - 127 + ((top_bits & 0x7FFFFFu) ? 1 : 0), 127));  // L
+// The steps of a wave, from `step` on.  POWERS: with z, in units of 2^L.
+template <int DJ, bool F16, bool POWERS>
+__device__ __forceinline__ void many_steps(const Attention& a, const Plan& p, const ManyLds<DJ, many_tiles(DJ)>& lds, int step, int last,
+                                           int lane, int scale_log, State<DJ, many_tiles(DJ)>& st) {
+  constexpr int MT = many_tiles(DJ), ST = 2;
+  if (step >= last) return;
   const float c_scale = fabsf(a.scale);
-
-  State<DJ, MT> st;
+  u32x4 k[ST][DJ], v[ST][DJ];
+  Where<ST> here = find_step<DJ, ST>(a, p, step, ids_of_step<ST>(a, p, step));
+  Ids<ST> ids = ids_of_step<ST>(a, p, min(step + kWaves, last - 1));
+  load_tiles<DJ, ST, false>(a.pool.k_codes, here, lane * 16, k);
+  load_tiles<DJ, ST, false>(a.pool.v_codes, here, lane * 16, v);
+  while (true) {
+    const int next_step = step + kWaves;
+    const bool more = next_step < last;
+    const int byte = more ? lane * 16 : 0;
+    arrive<ST>(here, ids);
+    Where<ST> next = find_step<DJ, ST>(a, p, more ? next_step : step, ids);
+    ids = ids_of_step<ST>(a, p, min(next_step + kWaves, last - 1));
+    f32x4 s[MT][ST];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    st.m[mt] = -INFINITY;
-    st.l[mt] = 0.f;
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int i = 0; i < 4 * DJ; ++i) st.o[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-
-  int step = first + wave;
-  if (step < last) {
-    u32x4 k[ST][DJ], v[ST][DJ];
-    Where<ST> here = find_step<DJ, ST>(a, p, step, ids_of_step<ST>(a, p, step));
-    Ids<ST> ids = ids_of_step<ST>(a, p, min(step + kWaves, last - 1));
-    load_tiles<DJ, ST, false>(a.pool.k_codes, here, lane * 16, k);
-    load_tiles<DJ, ST, false>(a.pool.v_codes, here, lane * 16, v);
-    while (true) {
-      const int next_step = step + kWaves;
-      const bool more = next_step < last;
-      const int byte = more ? lane * 16 : 0;
-      arrive<ST>(here, ids);
-      Where<ST> next = find_step<DJ, ST>(a, p, more ? next_step : step, ids);
-      ids = ids_of_step<ST>(a, p, min(next_step + kWaves, last - 1));
-      f32x4 s[MT][ST];
+      for (int t = 0; t < ST; ++t) s[mt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+    for (int j = 0; j < DJ; ++j)
 #pragma unroll
-        for (int t = 0; t < ST; ++t) s[mt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int half = 0; half < 2; ++half) {
+        u32x4 kk[ST];
 #pragma unroll
-      for (int j = 0; j < DJ; ++j)
+        for (int t = 0; t < ST; ++t) kk[t] = widen8<F16>(k[t][j][2 * half], k[t][j][2 * half + 1]);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          u32x4 kk[ST];
+        for (int mt = 0; mt < MT; ++mt) {
+          const u32x4 q = lds.q[mt][j][half][lane];
 #pragma unroll
-          for (int t = 0; t < ST; ++t) kk[t] = widen8<F16>(k[t][j][2 * half], k[t][j][2 * half + 1]);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const u32x4 q = lds.q[mt][j][half][lane];
-#pragma unroll
-            for (int t = 0; t < ST; ++t) s[mt][t] = mfma<F16>(kk[t], q, s[mt][t]);
-          }
+          for (int t = 0; t < ST; ++t) s[mt][t] = mfma<F16>(kk[t], q, s[mt][t]);
         }
-      load_tiles<DJ, ST, false>(a.pool.k_codes, next, byte, k);
-      float c[ST], lv[ST], back[ST];
-      bool plain = (step + 1) * (kTile * ST) <= p.full;
+      }
+    load_tiles<DJ, ST, false>(a.pool.k_codes, next, byte, k);
+    bool plain = (step + 1) * (kTile * ST) <= p.full;
+    float c[ST];
+#pragma unroll
+    for (int t = 0; t < ST; ++t) {
+      plain = plain && here.ok[t];
+      c[t] = here.ks[t] * c_scale;
+    }
+    int seen[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) seen[mt] = p.end;
+    if constexpr (POWERS) {
+      float lv[ST], back[ST];
 #pragma unroll
       for (int t = 0; t < ST; ++t) {
-        const uint32_t bits = __builtin_bit_cast(uint32_t, here.vs[t]);
-        const int e = (int)(bits >> 23) - 127;
-        // a power of two, not far below the largest; keys of a scale below 0 turn the order
-        plain = plain && here.ok[t] && (bits & 0x807FFFFFu) == 0 && e >= -126 && e > scale_log - 64 && e < 128 && here.ks[t] >= 0.f;
+        const int e = (int)(__builtin_bit_cast(uint32_t, here.vs[t]) >> 23) - 127;
+        // keys of a scale below 0 turn the order
+        plain = plain && here.vs[t] > 0.f && e >= scale_log - 64 && here.ks[t] >= 0.f;
         lv[t] = (float)e;
         back[t] = power2(min(max(scale_log - e, 0), 64));
-        c[t] = here.ks[t] * c_scale;
       }
       if (!plain) {
 #pragma unroll
@@ -1138,20 +1093,14 @@ __device__ __forceinline__ void attend_many(const Attention& a, uint32_t block) 
           for (int mt = 0; mt < MT; ++mt) s[mt][t] *= c[t];
           c[t] = 1.f;
         }
-        int seen[MT];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) seen[mt] = p.end;
         mask_step<DJ, MT, ST>(p, step, lane, seen, here, s, v, st);
 #pragma unroll
-        for (int t = 0; t < ST; ++t) {
-          const float size = fabsf(here.vs[t]);
-          const float l = size > 0.f ? log2_scale(size) : -INFINITY;
-          const uint32_t turn = here.vs[t] < 0.f ? 0x80808080u : 0u;
-          const bool none = l < (float)(scale_log - 64);
-          lv[t] = none ? (float)scale_log : l;
-          back[t] = exp2_fast((float)scale_log - lv[t]);
+        for (int t = 0; t < ST; ++t) {  // holes, scales of 0 and those far below the largest
+          const bool none = here.vs[t] == 0.f || lv[t] < (float)(scale_log - 64);
+          lv[t] = none ? (float)scale_log : lv[t];
+          back[t] = none ? 1.f : back[t];
 #pragma unroll
-          for (int h = 0; h < DJ; ++h) v[t][h] = none ? u32x4{0, 0, 0, 0} : v[t][h] ^ turn;
+          for (int h = 0; h < DJ; ++h) v[t][h] = none ? u32x4{0, 0, 0, 0} : v[t][h];
         }
       }
       float top[MT];
@@ -1210,12 +1159,80 @@ __device__ __forceinline__ void attend_many(const Attention& a, uint32_t block) 
             if constexpr (F16) st.o[mt][h * 4 + x] = mfma<true>(vv, lo[mt], st.o[mt][h * 4 + x]);
           }
         }
-      load_tiles<DJ, ST, false>(a.pool.v_codes, next, byte, v);
-      if (!more) break;
-      here = next;
-      step = next_step;
+    } else {
+#pragma unroll
+      for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) s[mt][t] *= c[t];
+      if (!plain) mask_step<DJ, MT, ST>(p, step, lane, seen, here, s, v, st);
+      Probs<MT, ST> pr;
+      softmax<DJ, MT, ST>(a, p, step, lane, here, s, nullptr, nullptr, st, pr);
+      gather_values<DJ, MT, ST>(v, pr, st);
+    }
+    load_tiles<DJ, ST, false>(a.pool.v_codes, next, byte, v);
+    if (!more) return;
+    here = next;
+    step = next_step;
+  }
+}
+
+template <int DJ, bool F16>
+__device__ __forceinline__ void attend_many(const Attention& a, uint32_t block) {
+  constexpr int D = 64 * DJ, MT = many_tiles(DJ), ST = 2;
+  __shared__ __attribute__((aligned(16))) ManyLds<DJ, MT> lds;
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const Part part = part_of_shared(a, block);
+  const Plan p = plan_shared<MT, ST>(a, part);
+  const int first = part.index * p.part_steps, last = min(first + p.part_steps, p.steps);
+  if (first >= last) return;
+
+  // the queries, negated where the scale is below 0, so that the largest product gives
+  // the largest score
+  const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
+  for (int i = wave; i < MT * DJ; i += kWaves) {
+    const int mt = i / DJ, j = i % DJ, m = p.m0 + mt * 16 + lane % 16;
+    u32x4 x[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    if (m < a.m_rows) {
+      const uint16_t* src = row_of_all(a.q, a, p, m) + 64 * j + 16 * (lane / 16);
+      x[0] = load8(src, a.q.wide);
+      x[1] = load8(src + 8, a.q.wide);
+    }
+    lds.q[mt][j][0][lane] = x[0] ^ sign;
+    lds.q[mt][j][1][lane] = x[1] ^ sign;
+  }
+  // the largest scale, as bits; all ones: one of them is no power of two, nor 0
+  const int tiles_of_page = 1 << a.pool.tile_shift;
+  uint32_t top_scale = 0;
+  {
+    const int from = first * ST / tiles_of_page, to = (min(last * ST, p.tiles) + tiles_of_page - 1) / tiles_of_page;
+    const int32_t* pages = a.rows.pages + (uint64_t)p.row * a.rows.max_pages;
+    for (int i = from + (int)threadIdx.x; i < to; i += kThreads) {
+      const uint32_t id = (uint32_t)pages[i];
+      const uint32_t x = id < a.pool.n_pages ? __builtin_bit_cast(uint32_t, a.pool.v_scales[id]) : 0u;
+      top_scale = max(top_scale, (x & 0x807FFFFFu) || x >= 0x7F800000u ? ~0u : x);
     }
   }
+  top_scale = wave_max(top_scale);
+  if (lane == 0) lds.top[wave] = top_scale;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) top_scale = max(top_scale, lds.top[w]);
+  const bool powers = uniform(top_scale != ~0u);
+  const int scale_log = uniform(powers && top_scale ? (int)(top_scale >> 23) - 127 : 0);  // L
+
+  State<DJ, MT> st;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    st.m[mt] = -INFINITY;
+    st.l[mt] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4 * DJ; ++i) st.o[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  if (powers)
+    many_steps<DJ, F16, true>(a, p, lds, first + wave, last, lane, scale_log, st);
+  else
+    many_steps<DJ, F16, false>(a, p, lds, first + wave, last, lane, scale_log, st);
+  const float lift = powers ? kTop : 0.f;  // of the statistics
   // the waves' sums together, a group of 16 query rows and 64 dims at a time; left with
   // the statistics that attend_part leaves, of the scores alone
 #pragma unroll
@@ -1238,12 +1255,12 @@ __device__ __forceinline__ void attend_many(const Attention& a, uint32_t block) 
     const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      f[w] = exp2_fast(lds.ml[w][m_local][0] - base - kTop);
+      f[w] = exp2_fast(lds.ml[w][m_local][0] - base - lift);
       total += lds.ml[w][m_local][1] * f[w];
     }
     const uint64_t slot = (uint64_t)part.slot * a.unit_rows.d + m_local;
     const bool there = m_local < (int)a.unit_rows.d && m < a.m_rows;
-    if (d4 == 0 && there) a.ws_ml[slot] = f32x2{top + kTop - (float)scale_log, total};
+    if (d4 == 0 && there) a.ws_ml[slot] = f32x2{top + lift - (float)scale_log, total};
     const float unit = power2(scale_log);
 #pragma unroll
     for (int h = 0; h < DJ; ++h) {
