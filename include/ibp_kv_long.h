@@ -134,9 +134,7 @@ uint64_t ibp_kv_attention_shared_workspace_bytes(const ibp_kv_cache *cache,
  * Scores, statistics, sums, what a query may not see, and scales that are not
  * finite are as for ibp_kv_attention.  With more than 32 query rows to a head over
  * all sequences (n_seqs * n_new * group) the prefix's weights enter the second
- * product with 11 bits for outputs of bf16, which have 8, and values of pages whose
- * scale is below 2^-64 of the prefix's largest count as zeros.  No weights are
- * counted.
+ * product with 11 bits for outputs of bf16, which have 8.  No weights are counted.
  *
  * workspace: as for ibp_kv_attention; about head_dim * 4 bytes for each query row
  * and part, of the prefix and of the rows.

@@ -994,10 +994,11 @@ __global__ __launch_bounds__(kThreads) void select_long_kernel(Select s) {
 // so that the second product takes z as it is, with the codes; its largest is what
 // M follows.  The softmax's sum needs exp2(s_j) alone: with L the logarithm of the
 // part's largest scale a tile's sum of z times 2^L / vs is that in units of
-// 2^(M - L).  (Pages whose scale is below 2^(L - 64) count as zeros, and
-// their weight counts.)  This is for scales that are powers of two, as an append
-// writes them, and 0; a part with others takes attend_part's softmax and second
-// product.
+// 2^(M - L).  This is for scales that are powers of two, as an append writes them,
+// and at most 2^kNear apart: a part with others takes attend_part's softmax and
+// second product.  (Were a page of a smaller scale, one of zeros say, to count with
+// another scale than its own, its scores would raise M above what the products of
+// the other pages reach.)
 // z is held between 2^-24 and 2^kTop, M a step of 2^kStart
 // below the largest so far: in fp16 that is 11 bits of each weight of at least
 // 2^-21 of the largest.  Outputs of bf16 have 8; for those of fp16 what the
@@ -1013,6 +1014,7 @@ __global__ __launch_bounds__(kThreads) void select_long_kernel(Select s) {
 // it; the exponentials alone, the loads and the order of the instructions nothing that
 // shows.  With attend_part's softmax and 16-bit terms for every part: 171 us.
 constexpr float kTop = 15.f, kStart = 7.f;
+constexpr int kNear = 64;
 constexpr int many_tiles(int dj) { return dj <= 2 ? 4 : 2; }  // groups of 16 query rows
 
 __device__ __forceinline__ float maximum(float a, float b) { return __builtin_elementwise_maximum(a, b); }
@@ -1024,11 +1026,13 @@ struct ManyLds {
     float o[kWaves][16][64 + 4];
   };
   f32x2 ml[kWaves][MT * 16];
-  uint32_t top[kWaves];
+  struct {
+    uint32_t high, low;
+  } scales[kWaves];
 };
 
-// The steps of a wave, from `step` on.  POWERS: with z, in units of 2^L.
-template <int DJ, bool F16, bool POWERS>
+// The steps of a wave, from `step` on.  NEAR: with z, in units of 2^L.
+template <int DJ, bool F16, bool NEAR>
 __device__ __forceinline__ void many_steps(const Attention& a, const Plan& p, const ManyLds<DJ, many_tiles(DJ)>& lds, int step, int last,
                                            int lane, int scale_log, State<DJ, many_tiles(DJ)>& st) {
   constexpr int MT = many_tiles(DJ), ST = 2;
@@ -1076,15 +1080,15 @@ __device__ __forceinline__ void many_steps(const Attention& a, const Plan& p, co
     int seen[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) seen[mt] = p.end;
-    if constexpr (POWERS) {
+    if constexpr (NEAR) {
       float lv[ST], back[ST];
 #pragma unroll
       for (int t = 0; t < ST; ++t) {
-        const int e = (int)(__builtin_bit_cast(uint32_t, here.vs[t]) >> 23) - 127;
-        // keys of a scale below 0 turn the order
-        plain = plain && here.vs[t] > 0.f && e >= scale_log - 64 && here.ks[t] >= 0.f;
+        plain = plain && here.ks[t] >= 0.f;  // keys of a scale below 0 turn the order
+        // a hole's place has any scale, and its weights are 0
+        const int e = here.ok[t] ? (int)(__builtin_bit_cast(uint32_t, here.vs[t]) >> 23) - 127 : scale_log;
         lv[t] = (float)e;
-        back[t] = power2(min(max(scale_log - e, 0), 64));
+        back[t] = power2(scale_log - e);
       }
       if (!plain) {
 #pragma unroll
@@ -1094,14 +1098,6 @@ __device__ __forceinline__ void many_steps(const Attention& a, const Plan& p, co
           c[t] = 1.f;
         }
         mask_step<DJ, MT, ST>(p, step, lane, seen, here, s, v, st);
-#pragma unroll
-        for (int t = 0; t < ST; ++t) {  // holes, scales of 0 and those far below the largest
-          const bool none = here.vs[t] == 0.f || lv[t] < (float)(scale_log - 64);
-          lv[t] = none ? (float)scale_log : lv[t];
-          back[t] = none ? 1.f : back[t];
-#pragma unroll
-          for (int h = 0; h < DJ; ++h) v[t][h] = none ? u32x4{0, 0, 0, 0} : v[t][h];
-        }
       }
       float top[MT];
       bool higher = false;
@@ -1200,25 +1196,31 @@ __device__ __forceinline__ void attend_many(const Attention& a, uint32_t block) 
     lds.q[mt][j][0][lane] = x[0] ^ sign;
     lds.q[mt][j][1][lane] = x[1] ^ sign;
   }
-  // the largest scale, as bits; all ones: one of them is no power of two, nor 0
+  // the largest and the smallest scale, as bits; all ones: one of them is no power of two
   const int tiles_of_page = 1 << a.pool.tile_shift;
-  uint32_t top_scale = 0;
+  uint32_t high = 0, low = ~0u;
   {
     const int from = first * ST / tiles_of_page, to = (min(last * ST, p.tiles) + tiles_of_page - 1) / tiles_of_page;
     const int32_t* pages = a.rows.pages + (uint64_t)p.row * a.rows.max_pages;
     for (int i = from + (int)threadIdx.x; i < to; i += kThreads) {
       const uint32_t id = (uint32_t)pages[i];
-      const uint32_t x = id < a.pool.n_pages ? __builtin_bit_cast(uint32_t, a.pool.v_scales[id]) : 0u;
-      top_scale = max(top_scale, (x & 0x807FFFFFu) || x >= 0x7F800000u ? ~0u : x);
+      if (id >= a.pool.n_pages) continue;
+      const uint32_t x = __builtin_bit_cast(uint32_t, a.pool.v_scales[id]);
+      high = max(high, (x & 0x807FFFFFu) || x == 0 || x >= 0x7F800000u ? ~0u : x);
+      low = min(low, x);
     }
   }
-  top_scale = wave_max(top_scale);
-  if (lane == 0) lds.top[wave] = top_scale;
+  high = wave_max(high);
+  low = ~wave_max(~low);
+  if (lane == 0) lds.scales[wave] = {high, low};
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) top_scale = max(top_scale, lds.top[w]);
-  const bool powers = uniform(top_scale != ~0u);
-  const int scale_log = uniform(powers && top_scale ? (int)(top_scale >> 23) - 127 : 0);  // L
+  for (int w = 0; w < kWaves; ++w) {
+    high = max(high, lds.scales[w].high);
+    low = min(low, lds.scales[w].low);
+  }
+  const bool near = uniform(high != ~0u && (int)(high >> 23) - (int)(low >> 23) <= kNear);
+  const int scale_log = uniform(near && high ? (int)(high >> 23) - 127 : 0);  // L
 
   State<DJ, MT> st;
 #pragma unroll
@@ -1228,11 +1230,11 @@ __device__ __forceinline__ void attend_many(const Attention& a, uint32_t block) 
 #pragma unroll
     for (int i = 0; i < 4 * DJ; ++i) st.o[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  if (powers)
+  if (near)
     many_steps<DJ, F16, true>(a, p, lds, first + wave, last, lane, scale_log, st);
   else
     many_steps<DJ, F16, false>(a, p, lds, first + wave, last, lane, scale_log, st);
-  const float lift = powers ? kTop : 0.f;  // of the statistics
+  const float lift = near ? kTop : 0.f;  // of the statistics
   // the waves' sums together, a group of 16 query rows and 64 dims at a time; left with
   // the statistics that attend_part leaves, of the scores alone
 #pragma unroll
