@@ -132,9 +132,12 @@ uint64_t ibp_kv_attention_shared_workspace_bytes(const ibp_kv_cache *cache,
  * 0..p.  A query of a token that does not exist gets zeros; one that sees
  * neither a token of the prefix nor an own one gets zeros.
  * Scores, statistics, sums, what a query may not see, and scales that are not
- * finite are as for ibp_kv_attention.  With more than 32 query rows to a head over
- * all sequences (n_seqs * n_new * group) the prefix's weights enter the second
- * product with 11 bits for outputs of bf16, which have 8.  No weights are counted.
+ * finite are as for ibp_kv_attention.  So are the weights in the second product, 16
+ * bits each, but for one case: with more than 32 query rows to a head over all
+ * sequences (n_seqs * n_new * group) and outputs of bf16, which have 8 bits, a weight
+ * of the prefix may be off by half a step of 11 bits (2^-11 of itself) or by 2^-24
+ * of the row's largest, whichever is more; a sequence's result may differ by that
+ * with the batch it is in.  No weights are counted.
  *
  * workspace: as for ibp_kv_attention; about head_dim * 4 bytes for each query row
  * and part, of the prefix and of the rows.

@@ -994,15 +994,16 @@ __global__ __launch_bounds__(kThreads) void select_long_kernel(Select s) {
 // so that the second product takes z as it is, with the codes; its largest is what
 // M follows.  The softmax's sum needs exp2(s_j) alone: with L the logarithm of the
 // part's largest scale a tile's sum of z times 2^L / vs is that in units of
-// 2^(M - L).  This is for scales that are powers of two, as an append writes them,
-// and at most 2^kNear apart: a part with others takes attend_part's softmax and
-// second product.  (Were a page of a smaller scale, one of zeros say, to count with
-// another scale than its own, its scores would raise M above what the products of
-// the other pages reach.)
-// z is held between 2^-24 and 2^kTop, M a step of 2^kStart
-// below the largest so far: in fp16 that is 11 bits of each weight of at least
-// 2^-21 of the largest.  Outputs of bf16 have 8; for those of fp16 what the
-// rounding cuts off goes through the product as well.
+// 2^(M - L).
+// z goes into the product in fp16: at most 2^kTop, its largest at least 2^kStart
+// (M is that far below the largest when it is set), and off by 2^-11 of itself or by
+// 2^-25, half of fp16's smallest step.  That is 2^-32 of the largest z, so that
+// with scales at most 2^kNear apart a weight is off by 2^-11 of itself or 2^-24 of
+// the largest weight, whichever is more.  Outputs of bf16 have 8 bits; for those of
+// fp16 what the rounding cuts off goes through the product as well.
+// This is for scales that are powers of two, as an append writes them, and no
+// further apart: a part with others (pages of zeros have the smallest of all) takes
+// attend_part's softmax and second product, 16 bits of any weight.
 //
 // 96 x 64 queries of 128 dims over 32,768 tokens x 8 heads, and own rows of 70 to 700
 // tokens: calls back to back 126 us with 8 of joining, 0.83 PFLOP/s (a traced launch 133
@@ -1014,7 +1015,7 @@ __global__ __launch_bounds__(kThreads) void select_long_kernel(Select s) {
 // it; the exponentials alone, the loads and the order of the instructions nothing that
 // shows.  With attend_part's softmax and 16-bit terms for every part: 171 us.
 constexpr float kTop = 15.f, kStart = 7.f;
-constexpr int kNear = 64;
+constexpr int kNear = 8;
 constexpr int many_tiles(int dj) { return dj <= 2 ? 4 : 2; }  // groups of 16 query rows
 
 __device__ __forceinline__ float maximum(float a, float b) { return __builtin_elementwise_maximum(a, b); }
@@ -1031,7 +1032,7 @@ struct ManyLds {
   } scales[kWaves];
 };
 
-// The steps of a wave, from `step` on.  NEAR: with z, in units of 2^L.
+// The steps of a wave, from `step` on.  NEAR: with z, the part's scales near each other.
 template <int DJ, bool F16, bool NEAR>
 __device__ __forceinline__ void many_steps(const Attention& a, const Plan& p, const ManyLds<DJ, many_tiles(DJ)>& lds, int step, int last,
                                            int lane, int scale_log, State<DJ, many_tiles(DJ)>& st) {

@@ -125,7 +125,7 @@ def scales_of(scales, page_tokens, pages_row, n):
 
 
 def attention_shared(k_pool, v_pool, page_tokens, prefix_pages, prefix_lengths, pages, lengths, q, scale, counts=None,
-                     rounding=0.0, tiny=0.0, weight=2.0 ** -16):
+                     rounding=0.0, tiny=0.0, weight=2.0 ** -16, own_weight=None, floor=2.0 ** -32, least=0.0):
     """(out, error): float64 results and how far a computation in 32 bits may
     be off, derived as in kv_oracle.attention: a score is a sum of d products,
     each rounding at most 2^-23 of the sum of magnitudes; weights enter the
@@ -133,7 +133,11 @@ def attention_shared(k_pool, v_pool, page_tokens, prefix_pages, prefix_lengths, 
     (2^-11 for 16-bit numbers of 11 bits); sums over n tokens add n roundings.
     Numbers of 11 bits have their smallest step, 2^-24, where the row's largest
     product of weight and scale of values is at least 2^7: each product of a
-    weight and a code of values may be off by half of that.
+    weight and a code of values may be off by half of that (`floor`; 0 where
+    no such numbers are used).
+    own_weight: `weight` of the rows' own tokens, where it is another than the
+    prefix's.  least: one of those may be off by that much of
+    the row's largest.
     Exponentials below 2^-126, the smallest normal number of 32 bits, may come
     out as 0.  They are taken relative to a statistic that no score of the row
     exceeds by more than 2^8 once the sums are divided by their total, so that
@@ -149,18 +153,20 @@ def attention_shared(k_pool, v_pool, page_tokens, prefix_pages, prefix_lengths, 
         first_k, first_on = kv.read_rows(*k_pool, kp, page_tokens, prefix_pages[h], m)
         first_v, _ = kv.read_rows(*v_pool, vp, page_tokens, prefix_pages[h], m)
         first_s = scales_of(v_pool[1], page_tokens, prefix_pages[h], m)
+        first_w = np.full(m, weight)
         for s in range(n_seqs):
             n = kv.row_length(lengths[s, h], max_pages, page_tokens)
             origin, count = kv.new_tokens(n, counts, s, n_new)
             own_k, own_on = kv.read_rows(*k_pool, kp, page_tokens, pages[s, h], n)
             own_v, _ = kv.read_rows(*v_pool, vp, page_tokens, pages[s, h], n)
             own_s = scales_of(v_pool[1], page_tokens, pages[s, h], n)
+            own_w = np.full(n, weight if own_weight is None else own_weight)
             for i in range(max(0, -origin), count):
                 see = np.concatenate([first_on, own_on & (np.arange(n) <= origin + i)])
                 if not see.any():
                     continue
                 kk, vv = np.concatenate([first_k, own_k])[see], np.concatenate([first_v, own_v])[see]
-                unit = np.concatenate([first_s, own_s])[see]
+                unit, half_step = np.concatenate([first_s, own_s])[see], np.concatenate([first_w, own_w])[see]
                 for g in range(group):
                     x = q[s, i, h * group + g]
                     with np.errstate(invalid="ignore", over="ignore"):
@@ -172,11 +178,12 @@ def attention_shared(k_pool, v_pool, page_tokens, prefix_pages, prefix_lengths, 
                         p /= p.sum()
                         o = p @ vv
                         e = abs(scale) * (np.abs(kk) @ np.abs(x)) * (d + 4) * u + (np.abs(sc) + abs(top)) * 4 * u
-                        common = float(np.sum(p * e)) + len(kk) * u + weight
+                        common = float(np.sum(p * e)) + len(kk) * u + half_step
                         out[s, i, h * group + g] = o
                         err[s, i, h * group + g] += 2.0 ** -118 * np.abs(vv).sum(0)
+                        err[s, i, h * group + g] += least * p.max() * np.abs(vv[:int(first_on.sum())]).sum(0)
                         with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
                             codes = np.where(unit[:, None] != 0, np.abs(vv) / unit[:, None], 0.0)
-                            err[s, i, h * group + g] += 2.0 ** -32 * np.max(p * unit) * codes.sum(0)
+                            err[s, i, h * group + g] += floor * np.max(p * unit) * codes.sum(0)
                         err[s, i, h * group + g] += rounding * np.abs(o) + (1 + rounding) * ((p * (e + common)) @ np.abs(vv))
     return out, err

@@ -4,9 +4,10 @@ the 64-bit oracle and its bounds (oracle/kv_long_oracle.py): the paths of up to
 import numpy as np
 import pytest
 
+from oracle import kv_long_oracle as lorc
 from oracle import kv_oracle as orc
-from test_gpu_kv import grid, kv  # noqa: F401
-from test_gpu_kv_long import check_shared, shared_pool
+from test_gpu_kv import close, grid, kv  # noqa: F401
+from test_gpu_kv_long import check_shared, gpu, shared_pool
 from test_gpu_kv_paths import queries
 
 pytestmark = pytest.mark.gpu
@@ -59,3 +60,40 @@ def test_page_of_zeros_that_leads_by_its_score(kv, lead, scale, seqs, dtype):
     q[..., 0] = 8.0
     lengths = grid(seqs, 2, [(i * 7) % 90 + 1 for i in range(seqs)])
     check_shared(kv, p, [640, 333], lengths, q, scale=lead * np.log(2) / (8 * 240))
+
+
+def check_promise(kv, p, prefix_lengths, lengths, q, scale, far=False):
+    """Within what the header promises: 16 bits of each weight, or with more than 32
+    query rows and outputs of bf16 11 of the prefix's, no less than 2^-24 of the
+    largest.  `far`: scales that 16 bits are promised for in any case.  Rounding of
+    outputs, scores and sums as in check_shared."""
+    rows = q.shape[0] * q.shape[1] * q.shape[2] // p.pages.shape[1]
+    less = q.dtype == torch.bfloat16 and rows > 32 and not far
+    prefix_lengths = np.asarray(prefix_lengths, np.int32)
+    out = kv.ibp_kv_attention_shared(p.cache, gpu(p.prefix), gpu(prefix_lengths), p.gpu_pages, gpu(lengths), q.cuda(), scale=scale)
+    torch.cuda.synchronize()
+    fi = torch.finfo(q.dtype)
+    o, err = lorc.attention_shared(p.k, p.v, p.pt, p.prefix, prefix_lengths, p.pages, lengths, q.double().numpy(), scale,
+                                   rounding=fi.eps / 2, tiny=fi.tiny * fi.eps / 2, weight=2.0 ** (-11 if less else -16),
+                                   own_weight=2.0 ** -16, floor=0.0, least=2.0 ** -24 if less else 0.0)
+    close(out.cpu(), None, (o, None, err, None))
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("seqs", [3, 40])
+@pytest.mark.parametrize("apart", [9, 20, 40, 70])
+def test_pages_far_below_the_largest_scale(kv, apart, seqs, dtype):
+    """Half of the dims are zeros in the pages of the largest scale, so that the output
+    there is what the pages far below it give, under scores that are about equal."""
+    p = shared_pool(kv, seqs, 2, 40, 6, 16, 128, seed=apart)
+    rng = np.random.default_rng(apart)
+    p.k[1][:] = 2.0 ** -8
+    p.v[1] = rng.choice(np.array([1.0, 2.0 ** -apart], np.float32), p.n_pages)
+    low = orc.v_place(16, 128)[:, :64].reshape(-1)
+    p.v[0][np.ix_(p.v[1] == 1.0, low)] = 0
+    p.upload()
+    q = queries(1, seqs, 1, 6, 128, dtype)
+    out = check_promise(kv, p, [640, 333], grid(seqs, 2, [(i * 7) % 90 + 1 for i in range(seqs)]), q, 0.02, far=True)
+    if dtype == "bf16":
+        assert (out[..., :64] != 0).all()

@@ -382,3 +382,22 @@ def test_missing_library_raises():
             "kv._LONG_LIB_PATH = '/nonexistent/libibp_kv_long.so'\n"
             "try:\n    kv.long_lib()\nexcept RuntimeError as e:\n    assert 'is missing' in str(e)\nelse:\n    raise SystemExit(1)\n")
     assert subprocess.run([sys.executable, "-c", code], cwd=ROOT, timeout=120).returncode == 0
+
+
+def test_shared_oracle_bound_is_that_of_whole_rows():
+    """Without the smallest step of 11-bit numbers the bound is the unshared one; half
+    a step that counts for the prefix or for own tokens alone adds up to both."""
+    rng = np.random.default_rng(4)
+    pt, d, heads, seqs = 16, 64, 2, 3
+    pools = [(rng.integers(0, 0x50, (20, pt * d), dtype=np.uint8), (2.0 ** rng.integers(-3, 2, 20)).astype(np.float32)) for _ in range(2)]
+    prefix, pages = rng.integers(0, 20, (heads, 3)).astype(np.int32), rng.integers(0, 20, (seqs, heads, 4)).astype(np.int32)
+    q, lengths = rng.standard_normal((seqs, 2, 4, d)), np.array([[40, 40], [2, 2], [64, 33]], np.int32)
+
+    def bound(**more):
+        return lorc.attention_shared(*pools, pt, prefix, np.array([48, 48]), pages, lengths, q, 0.05, floor=0.0, **more)[1]
+    want = orc.attention(*pools, pt, np.concatenate([np.broadcast_to(prefix, (seqs, heads, 3)), pages], 2), lengths + 48, q, 0.05)[2]
+    assert np.allclose(bound(), want, rtol=1e-9)
+    none, first, own, both = bound(weight=0.0), bound(weight=2.0 ** -11, own_weight=0.0), bound(weight=0.0, own_weight=2.0 ** -11), bound(weight=2.0 ** -11)
+    assert np.allclose(first + own, none + both, rtol=1e-9)
+    for more in (first, own, bound(weight=0.0, least=2.0 ** -24)):     # the same where all values are zeros
+        assert (more >= none).all() and (more > none).any((1, 3)).all()
