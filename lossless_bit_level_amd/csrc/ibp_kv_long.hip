@@ -999,11 +999,11 @@ __global__ __launch_bounds__(kThreads) void select_long_kernel(Select s) {
 // (M is that far below the largest when it is set), and off by 2^-11 of itself or by
 // 2^-25, half of fp16's smallest step.  That is 2^-32 of the largest z, so that
 // with scales at most 2^kNear apart a weight is off by 2^-11 of itself or 2^-24 of
-// the largest weight, whichever is more.  Outputs of bf16 have 8 bits; for those of
-// fp16 what the rounding cuts off goes through the product as well.
-// This is for scales that are powers of two, as an append writes them, and no
-// further apart: a part with others (pages of zeros have the smallest of all) takes
-// attend_part's softmax and second product, 16 bits of any weight.
+// the largest weight, whichever is more.  Outputs of bf16 have 8 bits.
+// This is for these outputs, and for scales that are powers of two, as an append
+// writes them, and no further apart: a part with others (pages of zeros have the
+// smallest of all) and outputs of fp16 take attend_part's softmax and second product,
+// 16 bits of any weight.
 //
 // 96 x 64 queries of 128 dims over 32,768 tokens x 8 heads, and own rows of 70 to 700
 // tokens: calls back to back 126 us with 8 of joining, 0.83 PFLOP/s (a traced launch 133
@@ -1123,7 +1123,7 @@ __device__ __forceinline__ void many_steps(const Attention& a, const Plan& p, co
           for (int i = 0; i < 4 * DJ; ++i) st.o[mt][i] *= keep;
         }
       }
-      u32x4 hi[MT], lo[MT];
+      u32x4 z16[MT];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const float base = st.m[mt] == -INFINITY ? 0.f : st.m[mt];
@@ -1134,15 +1134,9 @@ __device__ __forceinline__ void many_steps(const Attention& a, const Plan& p, co
 #pragma unroll
           for (int r = 0; r < 4; ++r) z[r] = exp2_fast(__builtin_fmaf(s[mt][t][r], c[t], b));
           st.l[mt] = __builtin_fmaf((z[0] + z[1]) + (z[2] + z[3]), back[t], st.l[mt]);
-          f16x2 h0 = {(_Float16)z[0], (_Float16)z[1]}, h1 = {(_Float16)z[2], (_Float16)z[3]};
-          hi[mt][2 * t] = __builtin_bit_cast(uint32_t, h0);
-          hi[mt][2 * t + 1] = __builtin_bit_cast(uint32_t, h1);
-          if constexpr (F16) {
-            const f16x2 r0 = {(_Float16)(z[0] - (float)h0[0]), (_Float16)(z[1] - (float)h0[1])};
-            const f16x2 r1 = {(_Float16)(z[2] - (float)h1[0]), (_Float16)(z[3] - (float)h1[1])};
-            lo[mt][2 * t] = __builtin_bit_cast(uint32_t, r0);
-            lo[mt][2 * t + 1] = __builtin_bit_cast(uint32_t, r1);
-          }
+          const f16x2 h0 = {(_Float16)z[0], (_Float16)z[1]}, h1 = {(_Float16)z[2], (_Float16)z[3]};
+          z16[mt][2 * t] = __builtin_bit_cast(uint32_t, h0);
+          z16[mt][2 * t + 1] = __builtin_bit_cast(uint32_t, h1);
         }
       }
 #pragma unroll
@@ -1151,10 +1145,7 @@ __device__ __forceinline__ void many_steps(const Attention& a, const Plan& p, co
         for (int x = 0; x < 4; ++x) {
           const u32x4 vv = widen8<true>(v[0][h][x], v[1][h][x]);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            st.o[mt][h * 4 + x] = mfma<true>(vv, hi[mt], st.o[mt][h * 4 + x]);
-            if constexpr (F16) st.o[mt][h * 4 + x] = mfma<true>(vv, lo[mt], st.o[mt][h * 4 + x]);
-          }
+          for (int mt = 0; mt < MT; ++mt) st.o[mt][h * 4 + x] = mfma<true>(vv, z16[mt], st.o[mt][h * 4 + x]);
         }
     } else {
 #pragma unroll
@@ -1197,12 +1188,14 @@ __device__ __forceinline__ void attend_many(const Attention& a, uint32_t block) 
     lds.q[mt][j][0][lane] = x[0] ^ sign;
     lds.q[mt][j][1][lane] = x[1] ^ sign;
   }
-  // the largest and the smallest scale, as bits; all ones: one of them is no power of two
-  const int tiles_of_page = 1 << a.pool.tile_shift;
-  uint32_t high = 0, low = ~0u;
-  {
+  bool near = false;
+  int scale_log = 0;  // L
+  if constexpr (!F16) {
+    // the largest and the smallest scale, as bits; all ones: one of them is no power of two
+    const int tiles_of_page = 1 << a.pool.tile_shift;
     const int from = first * ST / tiles_of_page, to = (min(last * ST, p.tiles) + tiles_of_page - 1) / tiles_of_page;
     const int32_t* pages = a.rows.pages + (uint64_t)p.row * a.rows.max_pages;
+    uint32_t high = 0, low = ~0u;
     for (int i = from + (int)threadIdx.x; i < to; i += kThreads) {
       const uint32_t id = (uint32_t)pages[i];
       if (id >= a.pool.n_pages) continue;
@@ -1210,18 +1203,20 @@ __device__ __forceinline__ void attend_many(const Attention& a, uint32_t block) 
       high = max(high, (x & 0x807FFFFFu) || x == 0 || x >= 0x7F800000u ? ~0u : x);
       low = min(low, x);
     }
-  }
-  high = wave_max(high);
-  low = ~wave_max(~low);
-  if (lane == 0) lds.scales[wave] = {high, low};
-  __syncthreads();
+    high = wave_max(high);
+    low = ~wave_max(~low);
+    if (lane == 0) lds.scales[wave] = {high, low};
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    high = max(high, lds.scales[w].high);
-    low = min(low, lds.scales[w].low);
+    for (int w = 0; w < kWaves; ++w) {
+      high = max(high, lds.scales[w].high);
+      low = min(low, lds.scales[w].low);
+    }
+    near = uniform(high != ~0u && (int)(high >> 23) - (int)(low >> 23) <= kNear);
+    scale_log = uniform(near && high ? (int)(high >> 23) - 127 : 0);
+  } else {
+    __syncthreads();
   }
-  const bool near = uniform(high != ~0u && (int)(high >> 23) - (int)(low >> 23) <= kNear);
-  const int scale_log = uniform(near && high ? (int)(high >> 23) - 127 : 0);  // L
 
   State<DJ, MT> st;
 #pragma unroll
@@ -1231,10 +1226,10 @@ __device__ __forceinline__ void attend_many(const Attention& a, uint32_t block) 
 #pragma unroll
     for (int i = 0; i < 4 * DJ; ++i) st.o[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  if (near)
-    many_steps<DJ, F16, true>(a, p, lds, first + wave, last, lane, scale_log, st);
-  else
-    many_steps<DJ, F16, false>(a, p, lds, first + wave, last, lane, scale_log, st);
+  if constexpr (!F16) {
+    if (near) many_steps<DJ, F16, true>(a, p, lds, first + wave, last, lane, scale_log, st);
+  }
+  if (!near) many_steps<DJ, F16, false>(a, p, lds, first + wave, last, lane, scale_log, st);
   const float lift = near ? kTop : 0.f;  // of the statistics
   // the waves' sums together, a group of 16 query rows and 64 dims at a time; left with
   // the statistics that attend_part leaves, of the scores alone

@@ -97,3 +97,18 @@ def test_pages_far_below_the_largest_scale(kv, apart, seqs, dtype):
     out = check_promise(kv, p, [640, 333], grid(seqs, 2, [(i * 7) % 90 + 1 for i in range(seqs)]), q, 0.02, far=True)
     if dtype == "bf16":
         assert (out[..., :64] != 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("seqs", [3, 40])
+@pytest.mark.parametrize("lead", [12, 26, 40])
+def test_token_of_zeros_that_leads_by_its_score(kv, lead, seqs, dtype):
+    """The heaviest token, by 2^lead, has values of 0 in a page like the others: outputs
+    of fp16 keep 16 bits of the other weights, those of bf16 up to 2^-24 of the largest."""
+    p, page = led_pool(kv, seqs, 2, 64, seed=lead)
+    p.v[1][:] = 2.0 ** (lead // 2)
+    p.v[0][np.ix_(page, orc.v_place(16, 64)[5])] = 0
+    p.upload()
+    q = queries(3, seqs, 1, 6, 64, dtype)
+    q[..., 0] = 8.0
+    check_promise(kv, p, [640, 333], grid(seqs, 2, [(i * 7) % 90 + 1 for i in range(seqs)]), q, lead * np.log(2) / (8 * 240))
