@@ -112,3 +112,63 @@ def test_token_of_zeros_that_leads_by_its_score(kv, lead, seqs, dtype):
     q = queries(3, seqs, 1, 6, 64, dtype)
     q[..., 0] = 8.0
     check_promise(kv, p, [640, 333], grid(seqs, 2, [(i * 7) % 90 + 1 for i in range(seqs)]), q, lead * np.log(2) / (8 * 240))
+
+
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("seqs,group,new", [(1, 1, 1), (5, 3, 1), (32, 1, 1), (8, 4, 1), (33, 1, 1), (4, 5, 7), (16, 8, 1)])
+@pytest.mark.parametrize("odd", [False, True])
+def test_each_path_keeps_what_it_promises(kv, odd, seqs, group, new, dtype, d):
+    """1 to 140 query rows to a head: 16 bits of the weights of own tokens, and of the
+    prefix's up to 32 rows, for outputs of fp16, and with scales that are no powers of
+    two (`odd`); holes in the prefix, which ends inside a page."""
+    p = shared_pool(kv, seqs, 2, 30, 8, 32, d, seed=d + seqs)
+    if odd:
+        p.v[1] *= np.float32(0.75)
+    p.prefix[0, [2, 11]], p.prefix[1, 5] = -1, p.n_pages
+    p.upload()
+    q = queries(seqs, seqs, new, 2 * group, d, dtype)
+    check_promise(kv, p, [900, 417], grid(seqs, 2, [(i * 37) % 240 + new for i in range(seqs)]), q, 0.02, far=odd)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_some_parts_with_far_scales(kv, d):
+    """A long prefix in many parts, of which one has scales far apart and one is all
+    holes: their statistics join with those of the others; a head has other scales."""
+    p = shared_pool(kv, 41, 2, 700, 10, 16, d, seed=d)
+    p.prefix = np.random.default_rng(1).permutation(p.n_pages)[:700].astype(np.int32)[None].repeat(2, 0)
+    p.prefix[1] = p.prefix[1][::-1]
+    p.v[1][p.prefix[0, 100:110]] *= np.float32(2.0 ** -12)
+    p.v[1][p.prefix[0, 104]] *= np.float32(-1.5)
+    p.prefix[0, 300:420] = -1
+    p.upload()
+    q = queries(2, 41, 1, 2, d, "bf16")
+    check_promise(kv, p, [700 * 16 - 3, 699 * 16], grid(41, 2, [i % 50 + 1 for i in range(41)]), q, 0.02)
+
+
+@pytest.mark.parametrize("scale", [0.02, -0.05])
+def test_far_scales_nan_and_keys_of_every_scale(kv, scale):
+    """More than 32 rows and value scales that are no powers of two: NaN values reach
+    every query, those past the prefix's end none; negative, zero and extreme scales
+    of keys; a value scale that is not finite."""
+    seqs, d, pt = 20, 64, 16
+    p = shared_pool(kv, seqs, 1, 12, 8, pt, d, seed=5, n_pages=1 << 20)
+    ids = np.random.default_rng(5).permutation(p.n_pages)
+    p.prefix[0] = ids[:12]
+    p.pages = ids[12:12 + 20].reshape(seqs, 1, 1).astype(np.int32)
+    p.v[1] *= np.float32(1.25)
+    p.k[1] = np.random.default_rng(4).choice(np.array([1, 0.5, -1, -0.3, 0, 1.7, 2.0 ** -140], np.float32), p.n_pages)
+    place = orc.v_place(pt, d)
+    p.v[0][p.prefix[0, 9], place[7:].reshape(-1)] = 0x7F          # the prefix ends inside page 9
+    p.v[1][p.prefix[0, 10]] = np.nan
+    p.upload()
+    q, lengths = queries(3, seqs, 1, 2, d, "bf16"), grid(seqs, 1, [i % 16 + 1 for i in range(seqs)])
+    out = check_promise(kv, p, [9 * 16 + 7], lengths, q, scale, far=True)
+    assert not out.isnan().any()
+    p.v[0][p.prefix[0, 2], place[3, 40]] = 0xFF
+    p.upload()
+    nan = check_promise(kv, p, [9 * 16 + 7], lengths, q, scale, far=True).isnan()
+    assert nan[..., 40].all() and not nan[..., :40].any()
+    p.v[1][p.prefix[0, 1]] = np.inf
+    p.upload()
+    assert check_promise(kv, p, [9 * 16 + 7], lengths, q, scale, far=True).isnan().all()
