@@ -1699,9 +1699,9 @@ int ibp_kv_select(const ibp_kv_cache* cache, const ibp_kv_outlines* outlines, co
 
 uint64_t ibp_kv_attention_shared_workspace_bytes(const ibp_kv_cache* cache, const ibp_kv_table* prefix,
                                                  const ibp_kv_table* table, uint64_t q_heads, uint64_t n_new) {
-  if (check_cache(cache) || !prefix || !table || table->kv_heads == 0 || q_heads % table->kv_heads) return 0;
-  if (table->n_seqs && table->kv_heads > (1ull << 30) / table->n_seqs) return 0;
-  if (table->max_pages > 0x7FFFFFFFull / cache->page_tokens || prefix->max_pages > 0x7FFFFFFFull / cache->page_tokens) return 0;
+  uint64_t n_rows = 0;
+  if (check_cache(cache) || check_table(table, cache->page_tokens, &n_rows) || check_prefix(prefix, table, cache->page_tokens)) return 0;
+  if (n_rows == 0 || q_heads == 0 || q_heads % table->kv_heads || n_new == 0) return 0;
   SharedShape s;
   if (!make_shared_shape(table->n_seqs, table->kv_heads, prefix->max_pages, table->max_pages, cache->page_tokens,
                          cache->head_dim, q_heads / table->kv_heads, n_new, compute_units(), &s))

@@ -401,3 +401,17 @@ def test_shared_oracle_bound_is_that_of_whole_rows():
     assert np.allclose(first + own, none + both, rtol=1e-9)
     for more in (first, own, bound(weight=0.0, least=2.0 ** -24)):     # the same where all values are zeros
         assert (more >= none).all() and (more > none).any((1, 3)).all()
+
+
+def test_shared_workspace_is_0_for_what_the_call_refuses(kv):
+    g = kv.long_lib().ibp_kv_attention_shared_workspace_bytes
+    good = table(kv, n=1)
+    assert g(cache(kv), good, table(kv), 4, 1) > 0
+    for bad in (None, table(kv, n=2), table(kv, n=0), table(kv, n=1, h=3), table(kv, n=1, h=0), table(kv, n=1, lengths=None), table(kv, n=1, pages=None),
+                table(kv, n=1, lengths=FAKE + 2), table(kv, n=1, m=1 << 28)):
+        assert g(cache(kv), bad, table(kv), 4, 1) == 0
+    for bad in (None, table(kv, lengths=None), table(kv, pages=FAKE + 1), table(kv, m=1 << 28), table(kv, n=1 << 30)):
+        assert g(cache(kv), good, bad, 4, 1) == 0
+    assert g(None, good, table(kv), 4, 1) == 0 and g(cache(kv), good, table(kv), 0, 1) == 0
+    # nothing to do
+    assert g(cache(kv), good, table(kv), 4, 0) == 0 and g(cache(kv), good, table(kv, n=0, pages=None, lengths=None), 4, 1) == 0
