@@ -32,8 +32,9 @@ extern "C" {
  * each product and each sum rounded to 32 bits.  cos, sin: float
  * [n_positions][rotary_dim / 2], 16-byte aligned.  positions: int32
  * [n_seqs][n_new], the positions of the new tokens; null: their places in their
- * rows (once pages have been evicted these are not the same).  At a position
- * outside [0, n_positions) the rotated dims are NaN. */
+ * rows (which are others once pages have been evicted, and where rows are a
+ * sequence's own behind a shared prefix).  At a position outside [0, n_positions)
+ * the rotated dims are NaN. */
 typedef struct ibp_kv_rotation {
   uint64_t n_positions;
   uint32_t rotary_dim;
@@ -127,10 +128,11 @@ uint64_t ibp_kv_attention_shared_workspace_bytes(const ibp_kv_cache *cache,
 /*
  * ibp_kv_attention where all sequences begin with the same tokens: `prefix` is a
  * table of one sequence, of the same kv_heads, with the pages and lengths of
- * these.  Lengths and positions of `table` count a sequence's own tokens: the
- * query at position p sees the whole prefix and the own tokens at positions
- * 0..p.  A query of a token that does not exist gets zeros; one that sees
- * neither a token of the prefix nor an own one gets zeros.
+ * these.  Pages, lengths and positions of `table` are those of a sequence's own
+ * tokens, without the prefix: the query at position p sees the whole prefix and the
+ * own tokens at positions 0..p.  (ibp_kv_append_rotated takes the positions behind
+ * the prefix as `positions`.)  A query of a token that does not exist gets zeros;
+ * one that sees neither a token of the prefix nor an own one gets zeros.
  * Scores, statistics, sums, what a query may not see, and scales that are not
  * finite are as for ibp_kv_attention.  So are the weights in the second product, 16
  * bits each, but for one case: with more than 32 query rows to a head over all

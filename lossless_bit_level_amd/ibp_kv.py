@@ -274,7 +274,8 @@ def ibp_kv_append_rotated(cache: ibp_kv_cache, pages: torch.Tensor, lengths: tor
     """ibp_kv_append of keys whose positions are rotated on the way.  cos, sin:
     float32 [n_positions, rotary_dim / 2]; pairs are dims i and i +
     rotary_dim / 2 or, interleaved, 2 i and 2 i + 1.  positions: int32
-    [n_seqs, n_new] (default: the tokens' places in their rows).  With q
+    [n_seqs, n_new] (default: the tokens' places in their rows, which count
+    no prefix that other tables hold).  With q
     ([n_seqs, n_new, q_heads, head_dim], the type of k) the queries are rotated
     too, into q_out (default: a new tensor; q itself is allowed), which is
     returned.  outlines: (int8 [n_pages, 2, head_dim], float32 [n_pages]),
@@ -356,7 +357,7 @@ def ibp_kv_attention_shared(cache: ibp_kv_cache, prefix_pages: torch.Tensor,
     """ibp_kv_attention of sequences that begin with the same tokens, those of
     prefix_pages (int32 [kv_heads, max_prefix_pages]) and prefix_lengths (int32
     [kv_heads]), which are read once for all of them; pages and lengths are the
-    sequences' own.  workspace: a uint8 GPU tensor of at least
+    sequences' own, without these.  workspace: a uint8 GPU tensor of at least
     ibp_kv_attention_shared_workspace_bytes (default: allocated).  Returns out.
     Asynchronous on the current stream of the tensors' GPU, or on stream=."""
     if stream is not None:  # what the call allocates is the stream's too
