@@ -45,7 +45,8 @@ def command(out: str = LIB, extra=(), src: str = SRC) -> list[str]:
 
 
 def extension_command(out: str = KV_EXT, src: str = KV_EXT_SRC) -> list[str]:
-    """The KV libraries have to be built first: the module links to them."""
+    """libibp_kv.so has to be built first: the module links to it, and loads
+    libibp_kv_long.so if it is there."""
     import torch
     torch_dir = os.path.dirname(torch.__file__)
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
@@ -54,8 +55,7 @@ def extension_command(out: str = KV_EXT, src: str = KV_EXT_SRC) -> list[str]:
             "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
             "-isystem", sysconfig.get_paths()["include"], src, "-o", out,
             "-L", os.path.join(torch_dir, "lib"), "-L", PKG, f"-l:{os.path.basename(KV_LIB)}",
-            f"-l:{os.path.basename(KV_LONG_LIB)}",
-            "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-ldl", "-Wl,-rpath,$ORIGIN"]
 
 
 def build(verbose: bool = False) -> str:

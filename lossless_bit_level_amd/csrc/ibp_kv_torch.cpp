@@ -21,6 +21,8 @@
 #include <ATen/ops/empty_like.h>
 #include <c10/core/DeviceGuard.h>
 
+#include <dlfcn.h>
+
 #include <cmath>
 #include <cstring>
 #include <initializer_list>
@@ -420,6 +422,49 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // ---- libibp_kv_long ----
 
+// Its calls, found by load_long, so that those of libibp_kv do without the library.
+struct Long {
+  decltype(&ibp_kv_append_rotated) append_rotated;
+  decltype(&ibp_kv_outline) outline;
+  decltype(&ibp_kv_select) select;
+  decltype(&ibp_kv_select_workspace_bytes) select_workspace_bytes;
+  decltype(&ibp_kv_attention_shared) attention_shared;
+  decltype(&ibp_kv_attention_shared_workspace_bytes) attention_shared_workspace_bytes;
+  bool loaded;
+};
+Long g_long = {};
+
+template <class F>
+bool find(void* library, const char* name, F* out) {
+  *out = reinterpret_cast<F>(dlsym(library, name));
+  return *out != nullptr;
+}
+
+// load_long(path)
+PyObject* load_long(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arguments(n, 1)) return nullptr;
+  const char* path = PyUnicode_AsUTF8(a[0]);
+  if (!path) return nullptr;
+  void* library = dlopen(path, RTLD_NOW | RTLD_LOCAL);
+  Long x = {};
+  if (!library || !find(library, "ibp_kv_append_rotated", &x.append_rotated) || !find(library, "ibp_kv_outline", &x.outline) ||
+      !find(library, "ibp_kv_select", &x.select) || !find(library, "ibp_kv_select_workspace_bytes", &x.select_workspace_bytes) ||
+      !find(library, "ibp_kv_attention_shared", &x.attention_shared) ||
+      !find(library, "ibp_kv_attention_shared_workspace_bytes", &x.attention_shared_workspace_bytes)) {
+    PyErr_Format(PyExc_RuntimeError, "%s does not load: build it with `python -m lossless_bit_level_amd.build` (%s)", path, dlerror());
+    return nullptr;
+  }
+  x.loaded = true;
+  g_long = x;
+  Py_RETURN_NONE;
+}
+
+bool long_loaded() {
+  if (g_long.loaded) return true;
+  PyErr_SetString(PyExc_RuntimeError, "libibp_kv_long.so is missing: build it with `python -m lossless_bit_level_amd.build`");
+  return false;
+}
+
 // The outlines of a cache's pages.
 bool check_outlines(PyObject* codes, PyObject* scales, const ibp_kv_cache& cache, ibp_kv_outlines* out) {
   if (!check(codes, ScalarType::Char, "outline codes") || !check(scales, ScalarType::Float, "outline scales")) return false;
@@ -467,7 +512,7 @@ PyObject* append_rotated(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t* counts;
   void* stream;
   c10::Device gpu(c10::kCUDA, 0);
-  if (!arguments(n, 15) ||
+  if (!long_loaded() || !arguments(n, 15) ||
       !same_gpu({{tensor_of_cache(a[0]), "the cache"}, {a[1], "pages"}, {a[2], "lengths"}, {a[3], "k"}, {a[4], "v"}, {a[5], "cos"},
                  {a[6], "sin"}, {a[7], "positions"}, {a[8], "q"}, {a[9], "q_out"}, {a[10], "counts"}, {a[12], "outline codes"},
                  {a[13], "outline scales"}}, &gpu))
@@ -525,7 +570,7 @@ PyObject* append_rotated(PyObject*, PyObject* const* a, Py_ssize_t n) {
   written(a[9]);
   written(a[12]);
   written(a[13]);
-  const int status = ibp_kv_append_rotated(&cache, &table, dtype, (uint64_t)n_new, &k, &v, counts, &rotation, (uint64_t)q_heads,
+  const int status = g_long.append_rotated(&cache, &table, dtype, (uint64_t)n_new, &k, &v, counts, &rotation, (uint64_t)q_heads,
                                            queries ? &q : nullptr, queries ? &q_out : nullptr, outlined ? &outlines : nullptr, stream);
   gradients.mark({turned});
   PyObject* result = Py_None;
@@ -547,7 +592,7 @@ PyObject* outline(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t* counts;
   void* stream;
   c10::Device gpu(c10::kCUDA, 0);
-  if (!arguments(n, 8) ||
+  if (!long_loaded() || !arguments(n, 8) ||
       !same_gpu({{tensor_of_cache(a[0]), "the cache"}, {a[1], "outline codes"}, {a[2], "outline scales"}, {a[3], "pages"},
                  {a[4], "lengths"}, {a[6], "counts"}}, &gpu) ||
       !from_structure(a[0], &cache) || !check_outlines(a[1], a[2], cache, &outlines) || !check_table(a[3], a[4], &table) ||
@@ -556,7 +601,7 @@ PyObject* outline(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const OnGpu on(gpu);
   written(a[1]);
   written(a[2]);
-  return PyLong_FromLong(ibp_kv_outline(&cache, &outlines, &table, n_new, counts, stream));
+  return PyLong_FromLong(g_long.outline(&cache, &outlines, &table, n_new, counts, stream));
   END_HANDLE_TH_ERRORS
 }
 
@@ -581,7 +626,7 @@ PyObject* select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t* counts;
   void* stream;
   c10::Device gpu(c10::kCUDA, 0);
-  if (!arguments(n, 15) ||
+  if (!long_loaded() || !arguments(n, 15) ||
       !same_gpu({{tensor_of_cache(a[0]), "the cache"}, {a[1], "outline codes"}, {a[2], "outline scales"}, {a[3], "pages"},
                  {a[4], "lengths"}, {a[5], "q"}, {a[9], "counts"}, {a[10], "pages_out"}, {a[11], "lengths_out"}, {a[12], "places_out"},
                  {a[13], "workspace"}}, &gpu) ||
@@ -607,10 +652,10 @@ PyObject* select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor workspace;
   if (a[13] != Py_None)
     workspace = THPVariable_Unpack(a[13]);
-  else if (const uint64_t bytes = ibp_kv_select_workspace_bytes(&cache, &table))
+  else if (const uint64_t bytes = g_long.select_workspace_bytes(&cache, &table))
     workspace = at::empty({(int64_t)bytes}, options.dtype(at::kByte));
   for (int i = 10; i < 13; ++i) written(a[i]);
-  const int status = ibp_kv_select(&cache, &outlines, &table, dtype, (uint64_t)q_heads, (uint64_t)n_new, &q, counts, keep, sink, recent,
+  const int status = g_long.select(&cache, &outlines, &table, dtype, (uint64_t)q_heads, (uint64_t)n_new, &q, counts, keep, sink, recent,
                                    (int32_t*)p.data_ptr(), (int32_t*)l.data_ptr(), (int32_t*)w.data_ptr(),
                                    workspace.defined() ? workspace.data_ptr() : nullptr,
                                    workspace.defined() ? (uint64_t)workspace.numel() : 0, stream);
@@ -630,7 +675,7 @@ PyObject* attention_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t* counts;
   void* stream;
   c10::Device gpu(c10::kCUDA, 0);
-  if (!arguments(n, 11) ||
+  if (!long_loaded() || !arguments(n, 11) ||
       !same_gpu({{tensor_of_cache(a[0]), "the cache"}, {a[1], "prefix_pages"}, {a[2], "prefix_lengths"}, {a[3], "pages"},
                  {a[4], "lengths"}, {a[5], "q"}, {a[7], "counts"}, {a[8], "out"}, {a[9], "workspace"}}, &gpu))
     return nullptr;
@@ -660,10 +705,10 @@ PyObject* attention_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor workspace;
   if (a[9] != Py_None)
     workspace = THPVariable_Unpack(a[9]);
-  else if (const uint64_t bytes = ibp_kv_attention_shared_workspace_bytes(&cache, &prefix, &table, (uint64_t)q_heads, (uint64_t)n_new))
+  else if (const uint64_t bytes = g_long.attention_shared_workspace_bytes(&cache, &prefix, &table, (uint64_t)q_heads, (uint64_t)n_new))
     workspace = at::empty({(int64_t)bytes}, x.options().dtype(at::kByte));
   written(a[8]);
-  const int status = ibp_kv_attention_shared(&cache, &prefix, &table, dtype, (uint64_t)q_heads, (uint64_t)n_new, &q, &o, counts, scale,
+  const int status = g_long.attention_shared(&cache, &prefix, &table, dtype, (uint64_t)q_heads, (uint64_t)n_new, &q, &o, counts, scale,
                                              workspace.defined() ? workspace.data_ptr() : nullptr,
                                              workspace.defined() ? (uint64_t)workspace.numel() : 0, stream);
   gradients.mark({out});
@@ -676,6 +721,7 @@ PyMethodDef methods[] = {
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, nullptr},
     {"attention", (PyCFunction)(void (*)(void))attention, METH_FASTCALL, nullptr},
     {"evict", (PyCFunction)(void (*)(void))evict, METH_FASTCALL, nullptr},
+    {"load_long", (PyCFunction)(void (*)(void))load_long, METH_FASTCALL, nullptr},
     {"append_rotated", (PyCFunction)(void (*)(void))append_rotated, METH_FASTCALL, nullptr},
     {"outline", (PyCFunction)(void (*)(void))outline, METH_FASTCALL, nullptr},
     {"select", (PyCFunction)(void (*)(void))select, METH_FASTCALL, nullptr},

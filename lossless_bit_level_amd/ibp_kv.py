@@ -9,7 +9,8 @@ libibp_kv.so and libibp_kv_long.so.  The structures, lib() and long_lib() are
 ctypes; the calls take torch tensors through a small extension module
 (csrc/ibp_kv_torch.cpp), since a decoding step makes many short ones: it checks
 the arguments, allocates results and calls the C ABI.  If one of them has not
-been built this module raises on first use; there is no fallback.
+been built its calls raise (all do without libibp_kv.so or the module); there is
+no fallback.
 
 No call has a gradient.  Codes and scales carry none; going backward through a
 result of inputs that require one raises, and a given output with such inputs
@@ -164,12 +165,13 @@ def _ext():
     global _module
     if _module is None:
         lib()
-        long_lib()
         try:
             from . import _ibp_kv
         except ImportError as e:
             raise RuntimeError("_ibp_kv.so is missing or does not load: build it with "
                                f"`python -m lossless_bit_level_amd.build` ({e})") from e
+        if os.path.exists(_LONG_LIB_PATH):  # without it its calls raise, and the others work
+            _ibp_kv.load_long(_LONG_LIB_PATH)
         _module = _ibp_kv
     return _module
 

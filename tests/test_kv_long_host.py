@@ -4,6 +4,7 @@ refusal, which comes before anything is enqueued."""
 import ctypes
 import os
 import re
+import shutil
 import subprocess
 import sys
 import warnings
@@ -415,3 +416,24 @@ def test_shared_workspace_is_0_for_what_the_call_refuses(kv):
     assert g(None, good, table(kv), 4, 1) == 0 and g(cache(kv), good, table(kv), 0, 1) == 0
     # nothing to do
     assert g(cache(kv), good, table(kv), 4, 0) == 0 and g(cache(kv), good, table(kv, n=0, pages=None, lengths=None), 4, 1) == 0
+
+
+@built
+def test_calls_of_the_cache_do_without_the_long_library(tmp_path):
+    """Those of libibp_kv_long raise where it is missing, and no other does."""
+    package = tmp_path / "lossless_bit_level_amd"
+    package.mkdir()
+    for name in ("__init__.py", "ibp.py", "ibp_kv.py", "libibp_kv.so", "_ibp_kv.so"):
+        shutil.copy(os.path.join(ROOT, "lossless_bit_level_amd", name), package)
+    code = ("import torch\n"
+            "import lossless_bit_level_amd.ibp_kv as kv\n"
+            "def error(call, *args):\n"
+            "    try:\n        call(*args)\n"
+            "    except (RuntimeError, ValueError) as e:\n        return type(e).__name__ + ' ' + str(e)\n"
+            "i = torch.zeros(1, 1, 1, dtype=torch.int32)\n"
+            "assert 'GPU tensor' in error(kv.ibp_kv_evict, i, i.float(), i[0], 16, 2), error(kv.ibp_kv_evict, i, i.float(), i[0], 16, 2)\n"
+            "assert kv.status_string(0)\n"
+            "assert 'libibp_kv_long.so is missing' in error(kv.ibp_kv_outline, None, (None, None), i, i[0])\n"
+            "assert 'libibp_kv_long.so is missing' in error(kv.long_lib)\n")
+    run = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, timeout=120, capture_output=True, text=True)
+    assert run.returncode == 0, run.stderr
