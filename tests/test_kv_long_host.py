@@ -437,3 +437,30 @@ def test_calls_of_the_cache_do_without_the_long_library(tmp_path):
             "assert 'libibp_kv_long.so is missing' in error(kv.long_lib)\n")
     run = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, timeout=120, capture_output=True, text=True)
     assert run.returncode == 0, run.stderr
+
+
+@built
+def test_selection_buffers_bound_every_access(tmp_path):
+    """The selection reads ids and scores and writes what stays through buffers that
+    end with the row, whatever the scores are.  A buffer's scalar offset takes no part
+    in its bounds check, so that every access of the built kernels has it 0."""
+    objdump = "/opt/rocm/llvm/bin/llvm-objdump"
+    if not os.path.exists(objdump):
+        pytest.skip("no llvm-objdump")
+    copy = shutil.copy(LIB, tmp_path)
+    subprocess.run([objdump, "--offloading", copy], cwd=tmp_path, check=True, capture_output=True, timeout=60)
+    image = [f for f in os.listdir(tmp_path) if f.endswith("gfx950")]
+    assert len(image) == 1
+    text = subprocess.run([objdump, "-d", "--mcpu=gfx950", image[0]], cwd=tmp_path, check=True, capture_output=True,
+                          text=True, timeout=120).stdout
+    kernels = {"score_kernel": 0, "select_kernel": 0, "select_short_kernel": 0}
+    for kernel in re.split(r"\n(?=[0-9a-f]+ <)", text):
+        name = re.search(r"\d+(score_kernel|select_kernel|select_short_kernel)I", kernel.split("\n", 1)[0])
+        if not name:
+            continue
+        kernels[name[1]] += 1
+        found = re.findall(r"\tbuffer_(load|store)_dword(?:x\d)? \w+(?:\[[\d:]+\])?, v\d+, s\[\d+:\d+\], (\w+) offen", kernel)
+        assert {what for what, _ in found} == ({"load"} if name[1] == "score_kernel" else {"load", "store"})
+        assert len(found) == kernel.count("\tbuffer_") - kernel.count("\tbuffer_inv") - kernel.count("\tbuffer_wb")
+        assert {offset for _, offset in found} == {"0"}
+    assert kernels == {"score_kernel": 8, "select_kernel": 2, "select_short_kernel": 8}
