@@ -146,6 +146,8 @@ uint64_t ibp_kv_attention_workspace_bytes(const ibp_kv_cache *cache, const ibp_k
  *     s_j = scale * (q . k_j),  w_j = exp(s_j) / sum_i exp(s_i),
  *     out = sum_j w_j v_j       (rounded once, to dtype)
  *
+ * scale and scale * log2(e) must be finite.
+ *
  * A query that sees nothing (its position is negative, every page is a hole,
  * every score is minus infinity), and one past its sequence's count, gets
  * zeros.  Scores, statistics and sums are held in 32 bits, the sums up to 2^8

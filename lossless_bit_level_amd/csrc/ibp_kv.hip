@@ -452,7 +452,7 @@ int ibp_kv_attention(const ibp_kv_cache* cache, const ibp_kv_table* table, uint3
   uint64_t n_rows = 0;
   rc = check_table(table, cache->page_tokens, &n_rows);
   if (rc || n_rows == 0) return rc;
-  if (q_heads == 0 || q_heads % table->kv_heads || !weights != !weights_out || !(scale - scale == 0.f))
+  if (q_heads == 0 || q_heads % table->kv_heads || !weights != !weights_out || !std::isfinite(scale_log2(scale)))
     return IBP_ERR_INVALID_ARGUMENT;
   if (n_new && ((rc = check_tensor(q)) || (rc = check_tensor(out)))) return rc;
   if (n_new && (rows_overlap(table->n_seqs, out->seq_stride, cache->head_dim) ||
@@ -482,7 +482,7 @@ int ibp_kv_attention(const ibp_kv_cache* cache, const ibp_kv_table* table, uint3
   a.ws_ml = (f32x2*)((char*)workspace + s.ml_at);
   a.ws_mass = (float*)((char*)workspace + s.mass_at);
   a.ws_of = (int32_t*)((char*)workspace + s.of_at);
-  a.scale = scale * 1.44269504088896340736f;
+  a.scale = scale_log2(scale);
   a.group = make_divisor((uint32_t)(q_heads / table->kv_heads));
   a.m_rows = s.m_rows;
   a.m_groups = make_divisor((uint32_t)s.m_groups);

@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "ibp_kv.h"
 
@@ -1683,6 +1684,11 @@ bool make_shape(uint64_t n_rows, uint64_t max_pages, uint32_t page_tokens, uint3
   s->join_blocks = (uint32_t)join;
   return join <= max_grid(kThreads);
 }
+
+// The factor of scores as powers of two.  Refused where it is not finite, as it is not
+// for a scale above 2^127.47: a score of 0 would be NaN.
+float scale_log2(float scale) { return scale * 1.44269504088896340736f; }
+
 bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
   return na && nb && x < y + nb && y < x + na;

@@ -1720,7 +1720,7 @@ int ibp_kv_attention_shared(const ibp_kv_cache* cache, const ibp_kv_table* prefi
   rc = check_table(table, cache->page_tokens, &n_rows);
   if (rc || (rc = check_prefix(prefix, table, cache->page_tokens))) return rc;
   if (n_rows == 0) return IBP_OK;
-  if (q_heads == 0 || q_heads % table->kv_heads || !(scale - scale == 0.f)) return IBP_ERR_INVALID_ARGUMENT;
+  if (q_heads == 0 || q_heads % table->kv_heads || !std::isfinite(scale_log2(scale))) return IBP_ERR_INVALID_ARGUMENT;
   if (n_new == 0) return IBP_OK;
   if ((rc = check_tensor(q)) || (rc = check_tensor(out))) return rc;
   if (rows_overlap(table->n_seqs, out->seq_stride, cache->head_dim) ||
@@ -1743,7 +1743,7 @@ int ibp_kv_attention_shared(const ibp_kv_cache* cache, const ibp_kv_table* prefi
   if (cache->n_pages == 0) a.rows.capacity = b.rows.capacity = 0;  // holes only: nothing to see, and no page to read
   a.q = b.q = make_strided(q);
   a.out = b.out = make_strided(out);
-  a.scale = b.scale = scale * 1.44269504088896340736f;
+  a.scale = b.scale = scale_log2(scale);
   a.group = b.group = make_divisor((uint32_t)group);
   a.n_new = b.n_new = make_divisor((uint32_t)n_new);
   char* ws = (char*)workspace;

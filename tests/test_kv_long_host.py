@@ -464,3 +464,17 @@ def test_selection_buffers_bound_every_access(tmp_path):
         assert len(found) == kernel.count("\tbuffer_") - kernel.count("\tbuffer_inv") - kernel.count("\tbuffer_wb")
         assert {offset for _, offset in found} == {"0"}
     assert kernels == {"score_kernel": 8, "select_kernel": 2, "select_short_kernel": 8}
+
+
+def test_scales_whose_powers_of_two_are_infinite_are_refused(kv):
+    """A factor of scores of more than 2^128 / log2(e): with a score of 0 it would be NaN."""
+    INV, need = kv.IBP_ERR_INVALID_ARGUMENT, 1 << 40
+    last, past = 2.358e38, 2.36e38          # 2^128 / log2(e) is 2.3586e38
+    assert np.isfinite(np.float32(last) * np.float32(np.log2(np.e))) and np.isfinite(np.float32(past))
+    shared, plain = kv.long_lib().ibp_kv_attention_shared, kv.lib().ibp_kv_attention
+    for scale in (past, -past, 3.4e38, float("inf"), float("nan")):
+        assert shared(cache(kv), table(kv, n=1), table(kv), 0, 4, 1, tensor(kv), tensor(kv), None, scale, FAKE + 4, need, None) == INV
+        assert plain(cache(kv), table(kv), 0, 4, 1, tensor(kv), tensor(kv), None, scale, None, None, FAKE + 4, need, None) == INV
+    for scale in (last, -last):             # refused for the workspace's alignment, not for the scale
+        assert shared(cache(kv), table(kv, n=1), table(kv), 0, 4, 1, tensor(kv), tensor(kv), None, scale, FAKE + 4, need, None) == kv.IBP_ERR_LAYOUT
+        assert plain(cache(kv), table(kv), 0, 4, 1, tensor(kv), tensor(kv), None, scale, None, None, FAKE + 4, need, None) == kv.IBP_ERR_LAYOUT
