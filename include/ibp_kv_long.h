@@ -78,7 +78,8 @@ int ibp_kv_append_rotated(const ibp_kv_cache *cache, const ibp_kv_table *table, 
 
 /* Outlines of the pages that hold the last tokens of each row, n_new of them or,
  * with counts, counts[s] (clamped to [0, n_new]): of the tokens that a page
- * holds, old ones and new ones. */
+ * holds, old ones and new ones.  Rows that name the same page must hold the same
+ * number of its tokens. */
 int ibp_kv_outline(const ibp_kv_cache *cache, const ibp_kv_outlines *outlines,
                    const ibp_kv_table *table, uint64_t n_new, const int32_t *counts, void *stream);
 

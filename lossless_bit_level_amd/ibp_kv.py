@@ -300,7 +300,8 @@ def ibp_kv_outline(cache: ibp_kv_cache, outlines: tuple[torch.Tensor, torch.Tens
     """Outlines (int8 [n_pages, 2, head_dim], float32 [n_pages]) of the pages
     that hold the rows' last tokens: n_new of them or, with counts (int32
     [n_seqs]), each sequence's own number up to n_new; by default of all pages
-    that hold tokens.  Asynchronous on the current stream of the tensors' GPU,
+    that hold tokens.  Rows that name the same page must hold the same number
+    of its tokens.  Asynchronous on the current stream of the tensors' GPU,
     or on stream=."""
     if stream is not None:
         with _on(stream, pages):
