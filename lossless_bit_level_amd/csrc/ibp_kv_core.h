@@ -997,7 +997,8 @@ __device__ __forceinline__ void mask_step(const Plan& p, int step, int lane, con
   }
 }
 
-template <int DJ, int MT, int ST>
+// WEIGHTS: the tiles' shares are left for the pages' weights, where a call asks for them.
+template <int DJ, int MT, int ST, bool WEIGHTS>
 __device__ __forceinline__ void softmax(const Attention& a, const Plan& p, int step, int lane,
                                         const Where<ST>& w, f32x4 (&s)[MT][ST], float* mass_row,
                                         float* mass_lds, State<DJ, MT>& st, Probs<MT, ST>& out) {
@@ -1044,7 +1045,7 @@ __device__ __forceinline__ void softmax(const Attention& a, const Plan& p, int s
       mine = pair_sum32(mine, mine);
     const bool sole = ST == 4 || g < ST;
     if (sole) st.l[mt] += mine;
-    if (a.w_out) {
+    if (WEIGHTS && a.w_out) {
       const int tile = step * ST + g, m_local = mt * 16 + lane % 16;
       if (sole && tile < p.tiles && m_local < (int)a.unit_rows.d) {
         const float share = base + log2_fast(mine);
@@ -1140,7 +1141,7 @@ __device__ __forceinline__ void attend_part(const Attention& a, uint32_t block) 
   __shared__ __attribute__((aligned(16))) float s_o[kWaves][16][kPitch];
   __shared__ f32x2 s_ml[kWaves][MT * 16];
   __shared__ float s_lse[MT * 16];
-  __shared__ float s_mass[kLdsMass];
+  __shared__ float s_mass[MODE == Sums::kFinished ? kLdsMass : 1];  // no weights of sums that are left
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const bool whole = MODE == Sums::kFinished && a.n_parts == a.n_units, alone = whole && a.m_groups.d == 1;
   const Part part = MODE == Sums::kShared ? part_of_shared(a, block) : part_of_workgroup<ST>(a, block, lane);
@@ -1218,7 +1219,7 @@ __device__ __forceinline__ void attend_part(const Attention& a, uint32_t block) 
       }
       if (!plain) mask_step<DJ, MT, ST>(p, step, lane, seen, here, s, v, st);
       Probs<MT, ST> pr;
-      softmax<DJ, MT, ST>(a, p, step, lane, here, s, mass_row, s_mass, st, pr);
+      softmax<DJ, MT, ST, MODE == Sums::kFinished>(a, p, step, lane, here, s, mass_row, s_mass, st, pr);
       gather_values<DJ, MT, ST>(v, pr, st);
       load_tiles<DJ, ST, ONCE>(a.pool.v_codes, next, byte, v);
       if (!more) break;

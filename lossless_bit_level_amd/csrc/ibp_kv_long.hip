@@ -1154,7 +1154,7 @@ __device__ __forceinline__ void many_steps(const Attention& a, const Plan& p, co
         for (int mt = 0; mt < MT; ++mt) s[mt][t] *= c[t];
       if (!plain) mask_step<DJ, MT, ST>(p, step, lane, seen, here, s, v, st);
       Probs<MT, ST> pr;
-      softmax<DJ, MT, ST>(a, p, step, lane, here, s, nullptr, nullptr, st, pr);
+      softmax<DJ, MT, ST, false>(a, p, step, lane, here, s, nullptr, nullptr, st, pr);
       gather_values<DJ, MT, ST>(v, pr, st);
     }
     load_tiles<DJ, ST, false>(a.pool.v_codes, next, byte, v);
