@@ -1349,7 +1349,7 @@ struct ChoiceLds {
   uint32_t bound[2][kW];
   uint32_t pick[3];
   uint32_t chunk[256];       // pages that stay, and ties in the upper half
-  uint32_t key[R][THREADS];  // a thread reads its own only
+  uint32_t key[R][THREADS];  // from the choice on a thread reads its own only
 };
 
 // What stays: keys above `last` and the first `ties` equal to it.
