@@ -1006,14 +1006,17 @@ __global__ __launch_bounds__(kThreads) void select_long_kernel(Select s) {
 // 16 bits of any weight.
 //
 // 96 x 64 queries of 128 dims over 32,768 tokens x 8 heads, and own rows of 70 to 700
-// tokens: calls back to back 126 us with 8 of joining, 0.83 PFLOP/s (a traced launch 133
-// to 150), with the matrix cores busy for 36% of the time (40% while there is work) and
-// the vector units for half of it: a step of 64 x 32
-// scores is 64 matrix instructions (1043 cycles) and some 320 others (1400 cycles), of
-// which two waves to a SIMD overlap half.  (Own rows' workgroups before the prefix's, so
-// that their loads run beside its arithmetic: 3 to 8 us more.)  The softmax's instructions cost a quarter of
-// it; the exponentials alone, the loads and the order of the instructions nothing that
-// shows.  With attend_part's softmax and 16-bit terms for every part: 171 us.
+// tokens: calls back to back 125 us with 8 of joining, 0.83 PFLOP/s (a traced launch 130
+// to 155), with the matrix cores busy for 36% of the time and the vector units for half
+// of it.  A step of 64 x 32 scores is 64 matrix instructions (1043 cycles) and some 225
+// others (about 1080); the prefix alone takes 115 us at 2.17 GHz, 2440 cycles for each of
+// a SIMD's 102 steps: more than both one after the other, so that what its two waves
+// overlap goes into waits.  (Own rows' workgroups before the prefix's, so that their
+// loads run beside its arithmetic: 3 to 8 us more.)  The softmax's instructions cost a
+// quarter of it; the exponentials alone, the loads and the order of the instructions
+// nothing that shows.  With attend_part's softmax and product for every part, a step is
+// 96 matrix instructions and more of the others: 169 us; 16 x 4 queries over 16,384
+// tokens 24.8 and 25.8 us (the latter in fp16, which has no other way).
 constexpr float kTop = 15.f, kStart = 7.f;
 constexpr int kNear = 8;
 constexpr int many_tiles(int dj) { return dj <= 2 ? 4 : 2; }  // groups of 16 query rows
@@ -1424,9 +1427,13 @@ uint64_t select_bytes(uint64_t n_rows, uint64_t max_pages) { return max_pages <=
 template <int DJ, bool F16>
 void launch_select(const Select& s, uint64_t n_rows, uint64_t max_pages, hipStream_t st) {
   const dim3 rows((uint32_t)n_rows);
-  // Rows of few pages are scored and chosen from in one launch: 8 rows of 251 pages 8 us,
-  // 12 as two; 16 x 32 rows of up to 256 pages 12 us, 20 as two.  (With 1024 threads and all
-  // pages at once the latter take 19 us, 72 rows of 50 to 500 pages the same 10 us.)
+  // Rows of few pages are scored and chosen from in one launch, which needs no workspace:
+  // 8 rows of 251 pages 8 us, 11 to 12 as two; 16 x 32 rows of up to 256 pages 12 us, 20 as
+  // two; 64 x 8 rows of 1000 pages 31 us, 34 as two.  Few long rows pay for it, since a
+  // workgroup scores 256 pages at a time (128 of wide heads): 8 rows of 512 pages of 64, 128
+  // and 256 dims take 8.6, 10.4 and 14.4 us, of 1000 pages 12.1, 15.5 and 22; as two launches
+  // each of these takes 10.5 to 12.  (With 1024 threads and all pages at once the 16 x 32
+  // rows take 19 us, 72 rows of 50 to 500 pages the same 10 us.)
   if (max_pages <= kShortPages) {
     hipLaunchKernelGGL((select_short_kernel<DJ, F16, 256, 4>), rows, dim3(256), 0, st, s);
     return;
